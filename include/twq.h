@@ -394,6 +394,98 @@ twq_status twq_fold_lowrank(const double *w, const double *u, const double *s, c
                             void *l1t, void *l2t, float *w_res, void *workspace,
                             size_t workspace_bytes, void *stream);
 
+/*
+ * ---- low-rank adapters of many requests beside the shared layer ----
+ *
+ * Fine-tuned variants of one frozen layer: adapter a is a low-rank pair A_a, B_a with a
+ * scale c_a, and a batch's token rows may each use another adapter or none. For token row i
+ * with adapter a(i),
+ *
+ *   H[i] = A_a x_i,    out[i] = y_i + c_a B_a H[i]        (out[i] = y_i without one)
+ *
+ * where Y is the shared layer's output (twq_linear) or anything else. The gradients, given
+ * dY, are with G[i] = B_a^T dy_i
+ *
+ *   dX[i] = dx_i + c_a A_a^T G[i],  dA_a = c_a sum_i G[i] x_i^T,  dB_a = c_a sum_i dy_i H[i]^T
+ *
+ * (dx: the shared layer's own input gradient, twq_linear_dx). All operands with a 16-bit
+ * type have the type `type`; sums and H are binary32; outputs are rounded once. Sums have a
+ * fixed order: equal calls give equal bits.
+ *
+ *   at    [count][r][m], bt [count][n][r]   the adapters (layouts of l1t and l2t). Smaller
+ *                                           ranks are padded with zeros.
+ *   scale f32 [count]                       c_a, or NULL (1)
+ * Shapes: as above, n and r positive, n at most 2^22, count 0..4096. Non-finite values in
+ * rows without an adapter are not read; elsewhere they make the row (or the adapter's
+ * gradient) non-finite.
+ */
+#define TWQ_F16 0
+#define TWQ_BF16 1
+
+/*
+ * The plan of a batch: its token rows grouped by adapter, made once and used by every call
+ * on the same rows (each layer and projection, forward and backward).
+ *   index i32 [b]       adapter of each token row; values outside [0, count) mean none
+ *   plan  (out)         twq_adapter_plan_bytes(b, count) bytes, contents private
+ */
+size_t twq_adapter_plan_bytes(int64_t b, int64_t count);
+twq_status twq_adapter_plan(const int32_t *index, int64_t b, int64_t count, void *plan, size_t plan_bytes, void *stream);
+
+/*
+ *   x     [b][m]             y [b][n] or NULL (zeros)
+ *   plan                     from twq_adapter_plan with this b and count
+ *   out   [b][n] (out)       may be y (in place); otherwise overlaps no input
+ *   h     f32 [b][r] (out)   H, zeros in rows without an adapter; or NULL
+ *   workspace                at least twq_adapters_workspace_bytes(b, m, n, r, count) bytes; no
+ *                            initial contents are needed. Calls that share a workspace must
+ *                            not overlap in time.
+ */
+size_t twq_adapters_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count);
+twq_status twq_adapters(const void *x, const void *at, const void *bt, const float *scale, const void *plan,
+                        size_t plan_bytes, const void *y, void *out, float *h, int64_t b, int64_t m, int64_t n,
+                        int64_t r, int64_t count, int type, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ *   dy    [b][n]
+ *   x     [b][m], or NULL and  qc i8 [b][m], sc f32 [m/128][b] from twq_checkpoint_act: the
+ *                            gradient is then that of the restored activations
+ *   h     f32 [b][r]         from twq_adapters
+ *   dx    [b][m] or NULL (zeros);  dx_out [b][m] (out), may be dx
+ *   dat   [count][r][m] (out), dbt [count][n][r] (out): zeros for adapters without rows
+ */
+size_t twq_adapters_grad_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count);
+twq_status twq_adapters_grad(const void *dy, const void *x, const void *qc, const float *sc, const float *h,
+                             const void *at, const void *bt, const float *scale, const void *plan, size_t plan_bytes,
+                             const void *dx, void *dx_out, void *dat, void *dbt, int64_t b, int64_t m, int64_t n,
+                             int64_t r, int64_t count, int type, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Activations kept in 8 bits between forward and backward: eq. (1) with k = 8 bits on groups
+ * of 128 consecutive elements of a token row,
+ *   s = fl32(max|x| / 127),  q = round-half-even(fl32(x / s)),  restored value s q.
+ * A group that holds an infinity or NaN gets s = NaN (its restored values are NaN).
+ *   x     [b][m];  qc i8 [b][m] (out);  sc f32 [m/128][b] (out), group-major
+ */
+twq_status twq_checkpoint_act(const void *x, int64_t b, int64_t m, int type, void *qc, float *sc, void *stream);
+twq_status twq_restore_act(const void *qc, const float *sc, int64_t b, int64_t m, int type, void *x, void *stream);
+
+/*
+ * The frozen layer's input gradient: with W = s_W Q_W + L1 L2 (activations taken as
+ * unquantized, the straight-through reading of eq. (1)),
+ *
+ *   dX[i][k] = sum_j dY[i][j] s_W[j] Q_W[j][k] + sum_t (sum_j dY[i][j] L2[t][j]) L1[k][t]
+ *
+ *   dy    [b][n];  dx [b][m] (out), both of `type`
+ *   qw, sw from twq_pack_weight;  l1t, l2t fp16 as for twq_linear (NULL iff r == 0)
+ *   workspace: at least twq_linear_dx_workspace_bytes(b, m, n, r) bytes, rules as above
+ * dY s_W is rounded once to 11 bits for the matrix cores; sums are binary32. n is positive and
+ * at most 2^22. A non-finite element of dY makes its row of dX non-finite.
+ */
+size_t twq_linear_dx_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r);
+twq_status twq_linear_dx(const void *dy, const void *qw, const float *sw, const void *l1t, const void *l2t, int64_t r,
+                         void *dx, int64_t b, int64_t m, int64_t n, int type, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -35,7 +35,10 @@ EXPORTS = ("twq_status_string", "twq_last_error_string", "twq_last_hip_error", "
            "twq_quantize_act_lr4", "twq_debug_lr4_h", "twq_dual_linear_lr4", "twq_linear_lr4_workspace_bytes",
            "twq_linear_lr4", "twq_debug_linear_lr4_main", "twq_debug_linear_main",
            "twq_debug_linear_grouped_main", "twq_debug_linear_a8_main", "twq_linear_noalloc_max_bytes",
-           "twq_linear_noalloc", "twq_fold_workspace_bytes", "twq_fold_lowrank")
+           "twq_linear_noalloc", "twq_fold_workspace_bytes", "twq_fold_lowrank", "twq_adapter_plan_bytes",
+           "twq_adapter_plan", "twq_adapters_workspace_bytes", "twq_adapters", "twq_adapters_grad_workspace_bytes",
+           "twq_adapters_grad", "twq_checkpoint_act", "twq_restore_act", "twq_linear_dx_workspace_bytes",
+           "twq_linear_dx")
 
 GROUP = 128  # group size of the group-wise entry points
 
@@ -51,7 +54,7 @@ class TwqError(RuntimeError):
 
 _lib = None
 _lock = threading.Lock()
-_P, _I, _S = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
+_P, _I, _S, _T = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
 
 
 def lib() -> ctypes.CDLL:
@@ -131,6 +134,19 @@ def lib() -> ctypes.CDLL:
                 L.twq_linear_noalloc.argtypes = [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _P]
                 L.twq_debug_linear_grouped_main.restype = ctypes.c_int
                 L.twq_debug_linear_grouped_main.argtypes = [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _P, _S, _P]
+                for nm, args in (("twq_adapter_plan_bytes", [_I] * 2), ("twq_adapters_workspace_bytes", [_I] * 5),
+                                 ("twq_adapters_grad_workspace_bytes", [_I] * 5),
+                                 ("twq_linear_dx_workspace_bytes", [_I] * 4)):
+                    getattr(L, nm).restype = _S
+                    getattr(L, nm).argtypes = args
+                for nm, args in (("twq_adapter_plan", [_P, _I, _I, _P, _S, _P]),
+                                 ("twq_adapters", [_P] * 5 + [_S] + [_P] * 3 + [_I] * 5 + [_T, _P, _S, _P]),
+                                 ("twq_adapters_grad", [_P] * 9 + [_S] + [_P] * 4 + [_I] * 5 + [_T, _P, _S, _P]),
+                                 ("twq_checkpoint_act", [_P, _I, _I, _T, _P, _P, _P]),
+                                 ("twq_restore_act", [_P, _P, _I, _I, _T, _P, _P]),
+                                 ("twq_linear_dx", [_P] * 5 + [_I, _P, _I, _I, _I, _T, _P, _S, _P])):
+                    getattr(L, nm).restype = ctypes.c_int
+                    getattr(L, nm).argtypes = args
                 _lib = L
     return _lib
 
@@ -590,6 +606,209 @@ def dual_linear_lr4(qx, sx, qw, sw, qh, sh, ql2, out: torch.Tensor | None = None
     _check(lib().twq_dual_linear_lr4(_ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), _ptr(qh), _ptr(sh), _ptr(ql2), r,
                                      _ptr(y), b, 2 * kb, n, _stream(qx.device)), "twq_dual_linear_lr4")
     return y
+
+
+# ---- low-rank adapters beside the shared layer, and training them over it ----
+
+TYPES = {torch.float16: 0, torch.bfloat16: 1}  # TWQ_F16, TWQ_BF16
+
+
+def _type(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in TYPES:
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16 (got {t.dtype})")
+    return TYPES[t.dtype]
+
+
+def _want(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device):
+    _need(t, name, dtype, len(shape))
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _scratch(dev: torch.device, nbytes: int):
+    """Workspace of one call, from torch's allocator: its memory belongs to the call's place in
+    the stream (or to the graph that captures it), so neither other calls nor other captured
+    graphs share it."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+
+
+def _apart(out: torch.Tensor, name: str, *others):
+    """out shares no memory with any of the others."""
+    lo, hi = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    for t in others:
+        if t is not None and t.data_ptr() < hi and lo < t.data_ptr() + t.numel() * t.element_size():
+            raise ValueError(f"{name} overlaps an input it must not share memory with")
+
+
+class AdapterPlan:
+    """A batch's token rows grouped by adapter (adapter_plan)."""
+
+    def __init__(self, data: torch.Tensor, b: int, count: int):
+        self.data, self.b, self.count = data, b, count
+
+
+def adapter_plan(index: torch.Tensor, count: int) -> AdapterPlan:
+    """index int32 [b], each token row's adapter (outside [0, count): none) -> the plan that
+    adapters and adapters_grad take; made once for all layers that see the same rows."""
+    _need(index, "index", torch.int32, 1)
+    b, dev = index.shape[0], index.device
+    L = lib()
+    if not 0 <= count <= 4096:
+        raise ValueError(f"count must lie in [0, 4096] (got {count})")
+    data = torch.empty(L.twq_adapter_plan_bytes(b, count), dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(L.twq_adapter_plan(_ptr(index), b, count, _ptr(data), data.numel(), _stream(dev)), "twq_adapter_plan")
+    return AdapterPlan(data, b, count)
+
+
+def _adapter_shapes(at, bt, plan: AdapterPlan, scale, b: int, dtype: torch.dtype, dev: torch.device):
+    if not isinstance(plan, AdapterPlan):
+        raise TypeError("plan must come from adapter_plan")
+    if plan.b != b or plan.data.device != dev:
+        raise ValueError(f"plan is for {plan.b} rows on {plan.data.device}, not {b} on {dev}")
+    _need(at, "at", dtype, 3)
+    _need(bt, "bt", dtype, 3)
+    count, r, m = at.shape
+    n = bt.shape[1]
+    _want(at, "at", dtype, (plan.count, r, m), dev)
+    _want(bt, "bt", dtype, (count, n, r), dev)
+    if scale is not None:
+        _want(scale, "scale", torch.float32, (count,), dev)
+    return m, n, r
+
+
+def adapters(x: torch.Tensor, at: torch.Tensor, bt: torch.Tensor, plan: AdapterPlan, y: torch.Tensor | None,
+             scale: torch.Tensor | None = None, out: torch.Tensor | None = None, keep_h: bool = False):
+    """out[i] = y[i] + scale[a] (x[i] at[a]^T) bt[a]^T for each token row i with adapter a of
+    the plan; out[i] = y[i] without one.
+
+    x [b][m], y [b][n] (None: zeros), at [count][r][m], bt [count][n][r]: all fp16 or all bf16.
+    out may be y. keep_h: also returns x at^T, f32 [b][r], which adapters_grad needs."""
+    ty = _type(x, "x")
+    _need(x, "x", x.dtype, 2)
+    b, dev = x.shape[0], x.device
+    m, n, r = _adapter_shapes(at, bt, plan, scale, b, x.dtype, dev)
+    _want(x, "x", x.dtype, (b, m), dev)
+    if y is not None:
+        _want(y, "y", x.dtype, (b, n), dev)
+    if out is None:
+        out = torch.empty((b, n), dtype=x.dtype, device=dev)
+    else:
+        _want(out, "out", x.dtype, (b, n), dev)
+        _apart(out, "out", x, at, bt, scale, None if y is None or y.data_ptr() == out.data_ptr() else y)
+    h = torch.empty((b, r), dtype=torch.float32, device=dev) if keep_h else None
+    L = lib()
+    with torch.cuda.device(dev):
+        wsb = L.twq_adapters_workspace_bytes(b, m, n, r, plan.count)
+        ws = _scratch(dev, wsb)
+        _check(L.twq_adapters(_ptr(x), _ptr(at), _ptr(bt), _ptr(scale), _ptr(plan.data), plan.data.numel(), _ptr(y),
+                              _ptr(out), _ptr(h), b, m, n, r, plan.count, ty, _ptr(ws), wsb, _stream(dev)),
+               "twq_adapters")
+    return (out, h) if keep_h else out
+
+
+def adapters_grad(dy: torch.Tensor, x, h: torch.Tensor, at: torch.Tensor, bt: torch.Tensor, plan: AdapterPlan,
+                  scale: torch.Tensor | None = None, dx: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """The gradients of adapters(): (dat [count][r][m], dbt [count][n][r], dX [b][m]).
+
+    x: the activations [b][m], or their checkpoint (qc, sc) from checkpoint_act; h from
+    adapters(keep_h=True). dX = dx + the adapters' share (dx None: zeros), written to out if
+    given (out may be dx). Adapters without rows get zero gradients."""
+    ty = _type(dy, "dy")
+    _need(dy, "dy", dy.dtype, 2)
+    b, dev, dt = dy.shape[0], dy.device, dy.dtype
+    m, n, r = _adapter_shapes(at, bt, plan, scale, b, dt, dev)
+    _want(dy, "dy", dt, (b, n), dev)
+    _want(h, "h", torch.float32, (b, r), dev)
+    qc = sc = None
+    if isinstance(x, tuple):
+        qc, sc = x
+        x = None
+        _want(qc, "qc", torch.int8, (b, m), dev)
+        _want(sc, "sc", torch.float32, (m // GROUP, b), dev)
+    else:
+        _want(x, "x", dt, (b, m), dev)
+    if dx is not None:
+        _want(dx, "dx", dt, (b, m), dev)
+    if out is None:
+        out = torch.empty((b, m), dtype=dt, device=dev)
+    else:
+        _want(out, "out", dt, (b, m), dev)
+        _apart(out, "out", dy, x, qc, sc, h, at, bt, scale, None if dx is None or dx.data_ptr() == out.data_ptr() else dx)
+    dat, dbt = torch.empty_like(at), torch.empty_like(bt)
+    L = lib()
+    with torch.cuda.device(dev):
+        wsb = L.twq_adapters_grad_workspace_bytes(b, m, n, r, plan.count)
+        ws = _scratch(dev, wsb)
+        _check(L.twq_adapters_grad(_ptr(dy), _ptr(x), _ptr(qc), _ptr(sc), _ptr(h), _ptr(at), _ptr(bt), _ptr(scale),
+                                   _ptr(plan.data), plan.data.numel(), _ptr(dx), _ptr(out), _ptr(dat), _ptr(dbt), b, m, n,
+                                   r, plan.count, ty, _ptr(ws), wsb, _stream(dev)), "twq_adapters_grad")
+    return dat, dbt, out
+
+
+def checkpoint_act(x: torch.Tensor):
+    """x fp16 or bf16 [b][m] -> (codes int8 [b][m], scales f32 [m/128][b]): the activations in
+    8 bits, one scale per token and 128 elements."""
+    ty = _type(x, "x")
+    _need(x, "x", x.dtype, 2)
+    (b, m), dev = x.shape, x.device
+    qc = torch.empty((b, m), dtype=torch.int8, device=dev)
+    sc = torch.empty((m // GROUP, b), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().twq_checkpoint_act(_ptr(x), b, m, ty, _ptr(qc), _ptr(sc), _stream(dev)), "twq_checkpoint_act")
+    return qc, sc
+
+
+def restore_act(qc: torch.Tensor, sc: torch.Tensor, dtype: torch.dtype = torch.float16,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """The activations of checkpoint_act again, codes times scales, in fp16 or bf16."""
+    _need(qc, "qc", torch.int8, 2)
+    (b, m), dev = qc.shape, qc.device
+    _want(sc, "sc", torch.float32, (m // GROUP, b), dev)
+    if out is None:
+        out = torch.empty((b, m), dtype=dtype, device=dev)
+    ty = _type(out, "out")
+    _want(out, "out", dtype, (b, m), dev)
+    _apart(out, "out", qc, sc)
+    with torch.cuda.device(dev):
+        _check(lib().twq_restore_act(_ptr(qc), _ptr(sc), b, m, ty, _ptr(out), _stream(dev)), "twq_restore_act")
+    return out
+
+
+def linear_dx(dy: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor, l1t=None, l2t=None,
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """The layer's input gradient: dX [b][m] = dY (s_W Q_W)^T + (dY L2^T) L1^T, with the packed
+    weight of pack_weight and the low-rank pair of linear; dY and dX fp16 or bf16."""
+    ty = _type(dy, "dy")
+    _need(dy, "dy", dy.dtype, 2)
+    _need(qw, "qw", torch.uint8, 2)
+    b, dev, dt = dy.shape[0], dy.device, dy.dtype
+    n, m = qw.shape[0], 2 * qw.shape[1]
+    _want(dy, "dy", dt, (b, n), dev)
+    _want(qw, "qw", torch.uint8, (n, m // 2), dev)
+    _want(sw, "sw", torch.float32, (n,), dev)
+    r = 0
+    if l1t is not None or l2t is not None:
+        _need(l1t, "l1t", torch.float16, 2)
+        r = l1t.shape[0]
+        _want(l1t, "l1t", torch.float16, (r, m), dev)
+        _want(l2t, "l2t", torch.float16, (n, r), dev)
+    if out is None:
+        out = torch.empty((b, m), dtype=dt, device=dev)
+    else:
+        _want(out, "out", dt, (b, m), dev)
+        _apart(out, "out", dy, qw, sw, l1t, l2t)
+    L = lib()
+    with torch.cuda.device(dev):
+        wsb = L.twq_linear_dx_workspace_bytes(b, m, n, r)
+        ws = _scratch(dev, wsb)
+        _check(L.twq_linear_dx(_ptr(dy), _ptr(qw), _ptr(sw), _ptr(l1t), _ptr(l2t), r, _ptr(out), b, m, n, ty, _ptr(ws),
+                               wsb, _stream(dev)), "twq_linear_dx")
+    return out
 
 
 class DualLinear:

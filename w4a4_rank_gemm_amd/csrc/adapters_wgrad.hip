@@ -1,0 +1,247 @@
+// adapters_wgrad.hip -- the weight gradients of low-rank adapters (gfx950).
+//
+//   dA_a = c_a sum_i G[i] x_i^T   [r][m]        dB_a = c_a sum_i dy_i H[i]^T   [n][r]
+//
+// over the token rows i of adapter a: products whose long axis K is the tokens, so both
+// operands lie with K as the slow index. They are staged in LDS row by row and read
+// transposed. One CTA takes a piece of one adapter's rows and 128 columns of X or dY;
+// both gradients are one launch. Each element of X and dY is read once; X may come as an
+// 8-bit checkpoint, whose codes feed the matrix cores as they are.
+//
+// The binary32 factor (G or H, times c_a and, with a checkpoint, the group's scale of the
+// token) is split into two bf16 parts, 16 significant bits together; codes (at most 127)
+// and bf16 elements are exact in bf16, fp16 elements are split exactly into two parts.
+// bf16 rather than fp16: gradients span more binades than fp16 has.
+#include "twq_adapters.h"
+#include "twq_adapters_device.h"
+
+namespace twq {
+
+constexpr int kStep = 32;    // token rows of one matrix instruction
+constexpr int kCols = 128;   // columns of X or dY a CTA (one checkpoint group)
+
+enum Src { kSrcF16, kSrcBF16, kSrcI8 };
+
+// Eight codes (one column's eight rows) to bf16, exactly.
+__device__ __forceinline__ v4i codes_to_bf16(v2i c) {
+    v4i r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t p = (uint32_t)c[e / 2] >> (16 * (e % 2));
+        const float f0 = (float)(int8_t)p, f1 = (float)(int8_t)(p >> 8);
+        r[e] = (int)__builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, f1), __builtin_bit_cast(uint32_t, f0), 0x07060302u);
+    }
+    return r;
+}
+
+// OUT[c][s] (RB rank blocks x 2 column blocks of a wave) += P^T Z over the piece's rows.
+// RANKS_M: ranks are the rows of the result blocks (dB, stored with ranks contiguous), else
+// the columns of Z are (dA).
+template <int RB, Src SRC, bool RANKS_M>
+__device__ __forceinline__ void outer_piece(const OuterArgs &a, const PlanItem &it, int col0, int rank0, const int *rows,
+                                            uint8_t *smem, v4f (&acc)[2][RB]) {
+    constexpr int ZB = SRC == kSrcI8 ? 1 : 2;                  // bytes of an element of Z
+    constexpr int ZROW = kCols * ZB + 16, PROW = RB * 32 + 16; // padded LDS rows
+    constexpr int ZBYTES = kStep * ZROW, PBYTES = kStep * PROW, BUF = ZBYTES + 2 * PBYTES;
+    constexpr int ZN = kStep * kCols * ZB / 16 / 256;          // 16-byte chunks of Z a thread
+    constexpr int PC = RB * 4, PN = (kStep * PC + 255) / 256;  // chunks of four ranks a row; a thread
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, li = lane & 15, g = lane >> 4;
+    const int64_t ld = RANKS_M ? a.n : a.m;
+    const uint8_t *z = SRC == kSrcI8 ? reinterpret_cast<const uint8_t *>(a.qc)
+                                     : reinterpret_cast<const uint8_t *>(RANKS_M ? a.dy : a.x);
+    const float scale = a.scale ? a.scale[it.adapter] : 1.f;
+    const float *sc = SRC == kSrcI8 ? a.sc + (int64_t)(col0 / 128) * a.b : nullptr;
+    const int nst = (it.rows + kStep - 1) / kStep;
+
+    v4i zr[ZN];
+    v4f pr[PN];
+    float ps[PN];
+    auto load = [&](int st) {
+#pragma unroll
+        for (int j = 0; j < ZN; ++j) {
+            constexpr int PER = kCols * ZB / 16;
+            const int q = j * 256 + tid, i = st * kStep + q / PER;
+            const int64_t row = rows[i < it.rows ? i : it.rows - 1];
+            const int64_t c = col0 + q % PER * (16 / ZB);
+            zr[j] = load16(z + (row * ld + (c < ld ? c : ld - 16 / ZB)) * ZB);
+        }
+#pragma unroll
+        for (int j = 0; j < PN; ++j) {
+            const int q = j * 256 + tid, i = st * kStep + q / PC, rank = rank0 + q % PC * 4;
+            pr[j] = v4f{0.f, 0.f, 0.f, 0.f};
+            ps[j] = 0.f;
+            if (q < kStep * PC && i < it.rows && rank < a.r) {
+                const int64_t row = rows[i];
+                pr[j] = *reinterpret_cast<const v4f *>(RANKS_M ? a.h + row * a.r + rank : a.g + (int64_t)(it.first + i) * a.r + rank);
+                ps[j] = SRC == kSrcI8 ? scale * sc[row] : scale;
+            }
+        }
+    };
+    auto store = [&](int st) {
+        uint8_t *buf = smem + (st & 1) * BUF;
+#pragma unroll
+        for (int j = 0; j < ZN; ++j) {
+            constexpr int PER = kCols * ZB / 16;
+            const int q = j * 256 + tid;
+            *reinterpret_cast<v4i *>(buf + q / PER * ZROW + q % PER * 16) = zr[j];
+        }
+#pragma unroll
+        for (int j = 0; j < PN; ++j) {
+            const int q = j * 256 + tid;
+            if (kStep * PC % 256 && q >= kStep * PC) break;
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float v0 = pr[j][2 * e] * ps[j], v1 = pr[j][2 * e + 1] * ps[j];
+                const uint16_t h0 = BF16::from_f32(v0), h1 = BF16::from_f32(v1);
+                const uint16_t l0 = BF16::from_f32(v0 - BF16::to_f32(h0)), l1 = BF16::from_f32(v1 - BF16::to_f32(h1));
+                hi[e] = (uint32_t)h0 | (uint32_t)h1 << 16;
+                lo[e] = (uint32_t)l0 | (uint32_t)l1 << 16;
+            }
+            uint8_t *p = buf + ZBYTES + q / PC * PROW + q % PC * 8;
+            *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2 *>(p + PBYTES) = make_uint2(lo[0], lo[1]);
+        }
+    };
+    load(0);
+    for (int st = 0; st < nst; ++st) {
+        store(st);  // the buffer was last read in step st - 2, before the barrier of st - 1
+        if (st + 1 < nst) load(st + 1);
+        __syncthreads();
+        const uint8_t *buf = smem + (st & 1) * BUF;
+        v4i zf[2], zl[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int c = wave * 32 + s * 16;
+            if constexpr (SRC == kSrcI8) {
+                zf[s] = codes_to_bf16(read_tr8(buf + (g * 8 + li / 2) * ZROW + c + (li % 2) * 8));
+            } else {
+                const uint8_t *p = buf + (g * 8 + li / 4) * ZROW + (c + (li % 4) * 4) * 2;
+                const v4s z0 = read_tr16(p), z1 = read_tr16(p + 4 * ZROW);
+                zf[s] = join(z0, z1);
+                if constexpr (SRC == kSrcF16) split_f16(zf[s], zf[s], zl[s]);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < RB; ++c) {
+            const uint8_t *p = buf + ZBYTES + (g * 8 + li / 4) * PROW + (c * 16 + (li % 4) * 4) * 2;
+            const v4s h0 = read_tr16(p), h1 = read_tr16(p + 4 * PROW);
+            const v4s l0 = read_tr16(p + PBYTES), l1 = read_tr16(p + PBYTES + 4 * PROW);
+            const v4i hi = join(h0, h1), lo = join(l0, l1);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                auto add = [&](v4i p16, v4i z16) {
+                    acc[s][c] = RANKS_M ? BF16::mfma(p16, z16, acc[s][c]) : BF16::mfma(z16, p16, acc[s][c]);
+                };
+                if constexpr (SRC == kSrcF16) add(lo, zl[s]), add(hi, zl[s]);
+                add(lo, zf[s]);
+                add(hi, zf[s]);
+            }
+        }
+    }
+}
+
+// A result block's four values of this lane, to the gradient (rounded) or its partial sum.
+template <class T>
+__device__ __forceinline__ void outer_put(const OuterArgs &a, uint16_t *out, float *part, int64_t at, const v4f &v) {
+    if (part) {
+        *reinterpret_cast<v4f *>(part + at) = v;
+    } else {
+        *reinterpret_cast<uint2 *>(out + at) =
+            make_uint2((uint32_t)T::from_f32(v[0]) | (uint32_t)T::from_f32(v[1]) << 16,
+                       (uint32_t)T::from_f32(v[2]) | (uint32_t)T::from_f32(v[3]) << 16);
+    }
+}
+
+template <class T, int RB, bool CODES>
+__global__ __launch_bounds__(256) void outer_kernel(OuterArgs a) {
+    constexpr int BUF = kStep * (kCols * 2 + 16) + 2 * kStep * (RB * 32 + 16);
+    __shared__ __align__(16) uint8_t smem[2 * BUF];
+    __shared__ int rows[2048];
+    if ((int)blockIdx.x >= a.plan.head[1]) return;
+    const PlanItem it = a.plan.chunks[blockIdx.x];
+    for (int i = threadIdx.x; i < it.rows; i += 256) rows[i] = a.plan.order[it.first + i];
+    __syncthreads();
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, li = lane & 15, g = lane >> 4;
+    const int mt = (int)(a.m / kCols), rank0 = blockIdx.z * RB * 16;
+    float *const part = it.slot < 0 ? nullptr : a.part + (int64_t)it.slot * a.r * (a.m + a.n);
+    v4f acc[2][RB] = {};
+    if ((int)blockIdx.y < mt) {
+        const int col0 = blockIdx.y * kCols;
+        outer_piece<RB, CODES ? kSrcI8 : T::kBf16 ? kSrcBF16 : kSrcF16, false>(a, it, col0, rank0, rows, smem, acc);
+        uint16_t *const out = a.dat + (int64_t)it.adapter * a.r * a.m;
+#pragma unroll
+        for (int c = 0; c < RB; ++c) {
+            const int rank = rank0 + c * 16 + li;
+            if (rank >= a.r) continue;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                outer_put<T>(a, out, part, (int64_t)rank * a.m + col0 + wave * 32 + s * 16 + g * 4, acc[s][c]);
+        }
+    } else {
+        const int col0 = (blockIdx.y - mt) * kCols;
+        outer_piece<RB, T::kBf16 ? kSrcBF16 : kSrcF16, true>(a, it, col0, rank0, rows, smem, acc);
+        uint16_t *const out = a.dbt + (int64_t)it.adapter * a.r * a.n;
+        float *const bp = part ? part + (int64_t)a.r * a.m : nullptr;
+#pragma unroll
+        for (int c = 0; c < RB; ++c) {
+            const int rank = rank0 + c * 16 + g * 4;
+            if (rank >= a.r) continue;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int64_t col = col0 + wave * 32 + s * 16 + li;
+                if (col < a.n) outer_put<T>(a, out, bp, col * a.r + rank, acc[s][c]);
+            }
+        }
+    }
+}
+
+// Gradients of adapters whose rows were several pieces: the pieces' sums in order. Adapters
+// without rows get zeros; those of one piece were written whole.
+template <class T>
+__global__ __launch_bounds__(256) void outer_join_kernel(OuterArgs a) {
+    const int ad = blockIdx.y;
+    const int rows = a.plan.offsets[ad + 1] - a.plan.offsets[ad], parts = (rows + a.chunk - 1) / a.chunk;
+    if (parts == 1) return;
+    const int64_t per = (int64_t)a.r * (a.m + a.n), e4 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e4 * 4 >= per) return;
+    v4f s = {0.f, 0.f, 0.f, 0.f};
+    const float *src = a.part + (parts ? (int64_t)a.plan.slot0[ad] * per : 0) + e4 * 4;
+    for (int p = 0; p < parts; ++p) {
+        const v4f v = *reinterpret_cast<const v4f *>(src + p * per);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += v[e];
+    }
+    const int64_t at = e4 * 4, na = (int64_t)a.r * a.m;
+    if (at < na)
+        outer_put<T>(a, a.dat + ad * na, nullptr, at, s);
+    else
+        outer_put<T>(a, a.dbt + (int64_t)ad * a.r * a.n, nullptr, at - na, s);
+}
+
+template <class T, bool CODES>
+static hipError_t outer_ranks(const OuterArgs &a, hipStream_t stream) {
+    const int rb = a.r <= 16 ? 1 : a.r <= 32 ? 2 : a.r <= 64 ? 4 : 8;
+    const dim3 grid((unsigned)a.chunks, (unsigned)(a.m / kCols + (a.n + kCols - 1) / kCols),
+                    (unsigned)((a.r + 16 * rb - 1) / (16 * rb)));
+    if (rb == 1)
+        outer_kernel<T, 1, CODES><<<grid, 256, 0, stream>>>(a);
+    else if (rb == 2)
+        outer_kernel<T, 2, CODES><<<grid, 256, 0, stream>>>(a);
+    else if (rb == 4)
+        outer_kernel<T, 4, CODES><<<grid, 256, 0, stream>>>(a);
+    else
+        outer_kernel<T, 8, CODES><<<grid, 256, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t per4 = (int64_t)a.r * (a.m + a.n) / 4;
+    outer_join_kernel<T><<<dim3((unsigned)((per4 + 255) / 256), (unsigned)a.count), 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_outer(const OuterArgs &a, hipStream_t stream) {
+    if (a.bf16) return a.qc ? outer_ranks<BF16, true>(a, stream) : outer_ranks<BF16, false>(a, stream);
+    return a.qc ? outer_ranks<F16, true>(a, stream) : outer_ranks<F16, false>(a, stream);
+}
+
+}  // namespace twq

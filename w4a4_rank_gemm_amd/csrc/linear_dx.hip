@@ -1,0 +1,396 @@
+// linear_dx.hip -- the frozen layer's input gradient (gfx950).
+//
+//   dX = dY W^T,  W^T = diag(s_W) Q_W + L2 L1 (as [n][m]):
+//   dX[i][k] = sum_j dY[i][j] s_W[j] Q_W[j][k] + sum_t (sum_j dY[i][j] L2[t][j]) L1[k][t]
+//
+// The long sum runs over the output channels j, the slow axis of the packed weight. Packed
+// 4-bit codes go to LDS as they lie (a 16-channel panel piece is 16 rows of K) and are read
+// transposed as nibbles: a lane gets 16 channels of one input column in 8 bytes, which are
+// expanded to fp16 in registers. Codes are exact in fp16; the per-channel scale is folded
+// into dY by a first kernel, G[i][j] = fp16(dY[i][j] s_W[j] 2^-e_i) with a power of two per
+// token that brings the row's largest element to [2^14, 2^15): one rounding, and no
+// gradient too small or too large for fp16. T = dY L2 (the adapters' shrink kernel) is held
+// in binary32, then in two fp16 parts, and joins the same accumulator after the long sum.
+#include <utility>
+
+#include "twq_adapters.h"
+#include "twq_adapters_device.h"
+
+namespace twq {
+
+constexpr int kDxM = 256;      // input columns of a CTA: 64 a wave
+constexpr int kDxK = 64;       // output channels of a stage: four panels
+constexpr int kDxStages = 3;
+
+// ---- G and T in fp16 -------------------------------------------------------------------
+
+// One CTA a token row. Eight consecutive channels are stored in the order 0 4 1 5 2 6 3 7,
+// the order in which expanded codes come (dequant8).
+template <class T>
+__global__ __launch_bounds__(256) void dx_scale_kernel(DxArgs a, int64_t npad) {
+    __shared__ float red[8];
+    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+    const int64_t row = blockIdx.x;
+    const uint16_t *src = a.dy + row * a.n;
+    auto row_max = [&](float v, int slot) {  // of the CTA, NaN dropped
+        v = wave_max_f32(v);
+        if (lane == 0) red[slot + wave] = v;
+        __syncthreads();
+        return __builtin_fmaxf(__builtin_fmaxf(red[slot], red[slot + 1]), __builtin_fmaxf(red[slot + 2], red[slot + 3]));
+    };
+    float mx = 0.f;
+    for (int64_t c = tid * 8; c < a.n; c += 2048) {
+        const v4i v = load16(src + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            mx = __builtin_fmaxf(mx, __builtin_fabsf(T::to_f32(half_of(v[e / 2], e % 2)) * a.sw[c + e]));
+    }
+    mx = row_max(mx, 0);
+    int ge = exponent_or_zero(mx);
+    ge = ge < -100 ? -100 : ge;
+    const float gf = pow2(14 - ge);
+    uint16_t *dst = a.g + row * npad;
+    for (int64_t c = tid * 8; c < npad; c += 2048) {
+        v4i o = {0, 0, 0, 0};
+        if (c < a.n) {
+            const v4i v = load16(src + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint16_t lo = half_of(v[e / 2], e % 2), hi = half_of(v[(e + 4) / 2], e % 2);
+                const uint16_t f0 = F16::from_f32(T::to_f32(lo) * a.sw[c + e] * gf);
+                const uint16_t f1 = F16::from_f32(T::to_f32(hi) * a.sw[c + e + 4] * gf);
+                o[e] = (int)((uint32_t)f0 | (uint32_t)f1 << 16);
+            }
+        }
+        *reinterpret_cast<v4i *>(dst + c) = o;
+    }
+    int te = 0;
+    if (a.r > 0) {
+        const int r32 = (a.r + 31) / 32 * 32;
+        float v = 0.f;  // thread t < r holds T[row][t]
+        if (tid < a.r)
+            for (int s = 0; s < a.tks; ++s) v += a.t[(s * a.b + row) * a.r + tid];
+        const float tm = row_max(__builtin_fabsf(v), 4);
+        te = tm > 0.f ? exponent_or_zero(tm) : ge;
+        // the two exponents meet in one accumulator: far apart, T keeps fewer bits
+        te = te < ge - 40 ? ge - 40 : te;
+        te = te < -100 ? -100 : te;
+        if (tid < r32) {
+            const float s = v * pow2(14 - te);
+            const uint16_t hi = F16::from_f32(s), lo = F16::from_f32(s - F16::to_f32(hi));
+            uint16_t *p = a.t16 + (row * r32 + tid / 8 * 8) * 2 + tid % 8;
+            p[0] = hi;
+            p[8] = lo;
+        }
+    }
+    if (tid == 0) {
+        a.ge[row * 2] = ge - 14;
+        a.ge[row * 2 + 1] = te - 14;
+    }
+}
+
+hipError_t launch_dx_scale(const DxArgs &a, const DxPlan &p, hipStream_t stream) {
+    if (a.bf16)
+        dx_scale_kernel<BF16><<<(unsigned)a.b, 256, 0, stream>>>(a, p.npad);
+    else
+        dx_scale_kernel<F16><<<(unsigned)a.b, 256, 0, stream>>>(a, p.npad);
+    return hipGetLastError();
+}
+
+// ---- main kernel -----------------------------------------------------------------------
+
+// Eight codes of a dword (two's complement nibbles q, nibble k = channel k) as fp16 pairs
+// (0, 4), (1, 5), (2, 6), (3, 7): q + 8 in the low mantissa bits of 1024 (or, four bits up,
+// times 16), then the offset taken off. Exact.
+__device__ __forceinline__ v4i dequant8(uint32_t d) {
+    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+    const uint32_t u = d ^ 0x88888888u, s = u >> 8;
+    const v2h one = {(_Float16)1032.f, (_Float16)1032.f}, six = {(_Float16)0.0625f, (_Float16)0.0625f};
+    const v2h off = {(_Float16)72.f, (_Float16)72.f};
+    const v2h p0 = __builtin_bit_cast(v2h, (u & 0x000F000Fu) | 0x64006400u) - one;
+    const v2h p1 = __builtin_bit_cast(v2h, (u & 0x00F000F0u) | 0x64006400u) * six - off;
+    const v2h p2 = __builtin_bit_cast(v2h, (s & 0x000F000Fu) | 0x64006400u) - one;
+    const v2h p3 = __builtin_bit_cast(v2h, (s & 0x00F000F0u) | 0x64006400u) * six - off;
+    return v4i{__builtin_bit_cast(int, p0), __builtin_bit_cast(int, p1), __builtin_bit_cast(int, p2), __builtin_bit_cast(int, p3)};
+}
+
+// One pair of panels (32 channels): the codes of two 32-column blocks (addresses w0, w1) and
+// the two operands of each of TB 32-token blocks (addresses g0, g1), completed before
+// returning (one statement, so that no other in-flight direct-to-LDS load is waited for).
+template <int TB, int WOFF, int GOFF>
+__device__ __forceinline__ void dx_read(uint32_t w0, uint32_t w1, uint32_t g0, uint32_t g1, v2i (&w)[2], v4i (&r)[2 * TB]) {
+    static_assert(TB == 1 || TB == 2 || TB == 4, "token blocks");
+    if constexpr (TB == 4)
+        asm volatile(
+            "ds_read_b64_tr_b4 %0, %10 offset:%14\n\t"
+            "ds_read_b64_tr_b4 %1, %11 offset:%14\n\t"
+            "ds_read_b128 %2, %12 offset:%15\n\t"
+            "ds_read_b128 %3, %13 offset:%15\n\t"
+            "ds_read_b128 %4, %12 offset:%16\n\t"
+            "ds_read_b128 %5, %13 offset:%16\n\t"
+            "ds_read_b128 %6, %12 offset:%17\n\t"
+            "ds_read_b128 %7, %13 offset:%17\n\t"
+            "ds_read_b128 %8, %12 offset:%18\n\t"
+            "ds_read_b128 %9, %13 offset:%18\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(w[0]), "=&v"(w[1]), "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]),
+              "=&v"(r[6]), "=&v"(r[7])
+            : "v"(w0), "v"(w1), "v"(g0), "v"(g1), "n"(WOFF), "n"(GOFF), "n"(GOFF + 4096), "n"(GOFF + 8192), "n"(GOFF + 12288)
+            : "memory");
+    else if constexpr (TB == 2)
+        asm volatile(
+            "ds_read_b64_tr_b4 %0, %6 offset:%10\n\t"
+            "ds_read_b64_tr_b4 %1, %7 offset:%10\n\t"
+            "ds_read_b128 %2, %8 offset:%11\n\t"
+            "ds_read_b128 %3, %9 offset:%11\n\t"
+            "ds_read_b128 %4, %8 offset:%12\n\t"
+            "ds_read_b128 %5, %9 offset:%12\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(w[0]), "=&v"(w[1]), "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])
+            : "v"(w0), "v"(w1), "v"(g0), "v"(g1), "n"(WOFF), "n"(GOFF), "n"(GOFF + 4096)
+            : "memory");
+    else
+        asm volatile(
+            "ds_read_b64_tr_b4 %0, %4 offset:%8\n\t"
+            "ds_read_b64_tr_b4 %1, %5 offset:%8\n\t"
+            "ds_read_b128 %2, %6 offset:%9\n\t"
+            "ds_read_b128 %3, %7 offset:%9\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(w[0]), "=&v"(w[1]), "=&v"(r[0]), "=&v"(r[1])
+            : "v"(w0), "v"(w1), "v"(g0), "v"(g1), "n"(WOFF), "n"(GOFF)
+            : "memory");
+}
+
+// A CTA owns 32 TB tokens x 256 input columns over a slice of the channels; its four waves
+// take 64 columns each and share the tokens' operands. A stage of 64 channels is 8 KB of
+// codes and 4 TB KB of G, by direct-to-LDS loads into a ring of three stages (two in
+// flight). G rows are 128-byte lines with the 16-byte chunk index XORed by row % 8, code
+// rows 64 bytes with the chunk XORed by (row / 4) % 4, so both reads touch every bank once.
+template <class T, int TB>
+__global__ __launch_bounds__(256, 2) void dx_kernel(DxArgs a, int64_t npad, int64_t mtiles) {
+    constexpr int BT = 32 * TB, WBYTES = kDxK / 16 * 2048, GBYTES = BT * 128, STAGE = WBYTES + GBYTES;
+    constexpr int GL = GBYTES / 4096, LOADS = 2 + GL;  // direct-to-LDS loads of a wave per stage
+    __shared__ __align__(1024) uint8_t ring[kDxStages * STAGE];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int li = lane & 15, half = lane >> 5;
+    const int64_t mt = blockIdx.x % mtiles, tt = blockIdx.x / mtiles, slice = blockIdx.y;
+    const int64_t tok0 = tt * BT, m0 = mt * kDxM, pieces = a.m / 128, panels = a.n / 16;
+    const int64_t nst = npad / kDxK, s0 = slice * nst / a.ks, s1 = (slice + 1) * nst / a.ks;
+
+    // direct-to-LDS: lane l of a 1 KB block fetches row l / 8, chunk (l % 8) ^ row of G (8
+    // rows), or row l / 4, chunk (l % 4) ^ (row / 4) of a panel piece (16 rows)
+    uint32_t goff[GL];
+#pragma unroll
+    for (int j = 0; j < GL; ++j) {
+        const int64_t row = (j * 4 + wave) * 8 + lane / 8, rel = tok0 + row < a.b ? row : a.b - 1 - tok0;
+        goff[j] = (uint32_t)(rel * npad * 2 + ((lane % 8) ^ (lane / 8)) * 16);
+    }
+    const uint32_t woff = (lane / 4) * 64 + ((lane % 4) ^ (lane / 16)) * 16;
+    const uint8_t *gbase = reinterpret_cast<const uint8_t *>(a.g + tok0 * npad);
+    auto issue = [&](int64_t st, int slot) {
+        uint8_t *dst = ring + slot * STAGE;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {  // eight pieces a stage, two a wave
+            const int p = wave, pc = j;
+            const int64_t panel = st * 4 + p < panels ? st * 4 + p : panels - 1;  // past n: G is zero
+            const int64_t piece = m0 / 128 + pc < pieces ? m0 / 128 + pc : pieces - 1;
+            const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<uint8_t *>(a.qw + (panel * pieces + piece) * 1024), 0, 1024, 0x00020000);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (__attribute__((address_space(3))) void *)(dst + (p * 2 + pc) * 1024), 16,
+                                                     (int)woff, 0, 0, 0);
+        }
+        const __amdgpu_buffer_rsrc_t rg =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(gbase + st * kDxK * 2), 0, 0x7fffffff, 0x00020000);
+#pragma unroll
+        for (int j = 0; j < GL; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rg, (__attribute__((address_space(3))) void *)(dst + WBYTES + (j * 4 + wave) * 1024), 16, (int)goff[j], 0, 0, 0);
+    };
+
+    v16f acc[2][TB];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[q][t][e] = 0.f;
+
+    // read addresses: codes of column block q: panel 2 pair + half, this wave's piece, row li,
+    // chunk 2 (wave % 2) + q; G: token lane % 32, chunk 4 pair + 2 half + h
+    const uint32_t ring0 = lds_offset(ring);
+    uint32_t wa[2], ga[2][2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        wa[q] = ring0 + (half * 2 + wave / 2) * 1024 + li * 64 + (((wave % 2) * 2 + q) ^ (li / 4)) * 16 + ((lane >> 4) & 1) * 8;
+#pragma unroll
+    for (int pr = 0; pr < 2; ++pr)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            ga[pr][h] = ring0 + WBYTES + (lane % 32) * 128 + ((pr * 4 + half * 2 + h) ^ (lane % 8)) * 16;
+
+    const int64_t n_st = s1 - s0;
+    if (n_st > 0) issue(s0, 0);
+    if (n_st > 1) issue(s0 + 1, 1);
+    for (int64_t c0 = 0; c0 < n_st; c0 += kDxStages) {
+        static_for(std::make_integer_sequence<int, kDxStages>{}, [&](auto u) {
+            constexpr int U = decltype(u)::value, OFF = U * STAGE;
+            const int64_t c = c0 + U;
+            if (c >= n_st) return;
+            if (c + 1 < n_st)
+                wait_vmcnt<LOADS>();
+            else
+                wait_vmcnt<0>();
+            stage_barrier();  // stage c has landed for every wave, and stage c - 1 is read
+            if (c + 2 < n_st) issue(s0 + c + 2, (U + 2) % kDxStages);
+            static_for(std::make_integer_sequence<int, 2>{}, [&](auto pv) {
+                constexpr int PR = decltype(pv)::value;
+                v2i w[2];
+                v4i r[2 * TB];
+                dx_read<TB, OFF + PR * 4096, OFF>(wa[0], wa[1], ga[PR][0], ga[PR][1], w, r);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const v8h wf = __builtin_bit_cast(v8h, dequant8((uint32_t)w[q][h]));
+#pragma unroll
+                        for (int t = 0; t < TB; ++t) acc[q][t] = mfma_f16_32(wf, __builtin_bit_cast(v8h, r[2 * t + h]), acc[q][t]);
+                    }
+            });
+        });
+    }
+
+    // epilogue: lane holds token lane % 32 of each token block, columns 8 (v / 4) + 4 half + v % 4
+    float fin[TB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+        const int64_t tok = tok0 + t * 32 + lane % 32, tc = tok < a.b ? tok : a.b - 1;
+        int e = a.ge[tc * 2];
+        if (a.r > 0 && slice == 0) {
+            const int te = a.ge[tc * 2 + 1], d = e - te;
+            const float f = pow2(d < -126 ? -126 : d > 127 ? 127 : d);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[q][t][v] *= f;
+            e = te;
+        }
+        fin[t] = pow2(e);
+    }
+    if (a.r > 0 && slice == 0) {
+        const int r32 = (a.r + 31) / 32 * 32;
+        uint16_t *const l1 = reinterpret_cast<uint16_t *>(ring);  // [32 ranks][256 columns]
+        for (int k0 = 0; k0 < a.r; k0 += 32) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = j * 256 + tid, k = k0 + c / 32;
+                const int64_t col = m0 + c % 32 * 8;
+                *reinterpret_cast<v4i *>(l1 + c * 8) =
+                    load16(a.l1t + (int64_t)(k < a.r ? k : a.r - 1) * a.m + (col < a.m ? col : a.m - 8));
+            }
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // ranks 16 h + 8 half .. + 7
+                v4i wf[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const uint16_t *p = l1 + (h * 16 + half * 8 + li / 4) * 256 + wave * 64 + q * 32 + ((lane >> 4) & 1) * 16 + (li % 4) * 4;
+                    const v4s p0 = read_tr16(p), p1 = read_tr16(p + 4 * 256);
+                    wf[q] = join(p0, p1);
+                }
+#pragma unroll
+                for (int t = 0; t < TB; ++t) {
+                    const int64_t tok = tok0 + t * 32 + lane % 32, tc = tok < a.b ? tok : a.b - 1;
+                    const uint16_t *tp = a.t16 + (tc * r32 + k0 + h * 16 + half * 8) * 2;
+                    const v4i hi = load16(tp), lo = load16(tp + 8);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        acc[q][t] = mfma_f16_32(__builtin_bit_cast(v8h, wf[q]), __builtin_bit_cast(v8h, lo), acc[q][t]);
+                        acc[q][t] = mfma_f16_32(__builtin_bit_cast(v8h, wf[q]), __builtin_bit_cast(v8h, hi), acc[q][t]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+        const int64_t tok = tok0 + t * 32 + lane % 32;
+        if (tok >= a.b) continue;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int64_t col = m0 + wave * 64 + q * 32 + v * 8 + half * 4;
+                if (col >= a.m) continue;
+                v4f o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = acc[q][t][v * 4 + e] * fin[t];
+                if (a.ks > 1)
+                    *reinterpret_cast<v4f *>(a.part + (slice * a.b + tok) * a.m + col) = o;
+                else
+                    *reinterpret_cast<uint2 *>(a.dx + tok * a.m + col) =
+                        make_uint2((uint32_t)T::from_f32(o[0]) | (uint32_t)T::from_f32(o[1]) << 16,
+                                   (uint32_t)T::from_f32(o[2]) | (uint32_t)T::from_f32(o[3]) << 16);
+            }
+    }
+}
+
+// dX = the slices' sums in slice order, rounded once.
+template <class T>
+__global__ __launch_bounds__(256) void dx_join_kernel(const float *part, int ks, int64_t total, uint16_t *dx) {
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (at >= total) return;
+    v4f s = *reinterpret_cast<const v4f *>(part + at);
+    for (int p = 1; p < ks; ++p) {
+        const v4f v = *reinterpret_cast<const v4f *>(part + p * total + at);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += v[e];
+    }
+    *reinterpret_cast<uint2 *>(dx + at) = make_uint2((uint32_t)T::from_f32(s[0]) | (uint32_t)T::from_f32(s[1]) << 16,
+                                                     (uint32_t)T::from_f32(s[2]) | (uint32_t)T::from_f32(s[3]) << 16);
+}
+
+// Token rows a CTA: as many as the batch fills, up to 128. Channel slices: with fewer CTAs
+// than two a compute unit, at least four stages each and at most 16.
+DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
+    auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+    DxPlan p{};
+    p.bt = b <= 32 ? 32 : b <= 64 ? 64 : 128;
+    p.npad = (n + kDxK - 1) / kDxK * kDxK;
+    const int64_t ctas = (b + p.bt - 1) / p.bt * ((m + kDxM - 1) / kDxM), stages = p.npad / kDxK;
+    int64_t ks = ctas >= 512 ? 1 : 512 / ctas;
+    if (ks > stages / 4) ks = stages / 4;
+    if (ks > 16) ks = 16;
+    p.ks = ks < 1 ? 1 : (int)ks;
+    p.tks = r > 0 ? shrink_slices(b, n, r, (b + kTileRows - 1) / kTileRows) : 0;
+    p.g = 0;
+    p.ge = up((size_t)b * p.npad * 2);
+    p.t = p.ge + up((size_t)b * 8);
+    p.t16 = p.t + up((size_t)p.tks * b * r * 4);
+    p.part = p.t16 + up((size_t)b * ((r + 31) / 32 * 32) * 4);
+    p.total = p.part + (p.ks > 1 ? up((size_t)p.ks * b * m * 4) : 0);
+    return p;
+}
+
+template <class T>
+static hipError_t dx_typed(const DxArgs &a, const DxPlan &p, hipStream_t stream) {
+    const int64_t mtiles = (a.m + kDxM - 1) / kDxM;
+    const dim3 grid((unsigned)(mtiles * ((a.b + p.bt - 1) / p.bt)), (unsigned)p.ks);
+    if (p.bt == 32)
+        dx_kernel<T, 1><<<grid, 256, 0, stream>>>(a, p.npad, mtiles);
+    else if (p.bt == 64)
+        dx_kernel<T, 2><<<grid, 256, 0, stream>>>(a, p.npad, mtiles);
+    else
+        dx_kernel<T, 4><<<grid, 256, 0, stream>>>(a, p.npad, mtiles);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.ks == 1) return e;
+    const int64_t total = a.b * a.m;
+    dx_join_kernel<T><<<dim3((unsigned)((total / 4 + 255) / 256)), 256, 0, stream>>>(a.part, p.ks, total, a.dx);
+    return hipGetLastError();
+}
+
+hipError_t launch_dx(const DxArgs &a, const DxPlan &p, hipStream_t stream) {
+    return a.bf16 ? dx_typed<BF16>(a, p, stream) : dx_typed<F16>(a, p, stream);
+}
+
+}  // namespace twq

@@ -1,0 +1,83 @@
+// twq_adapters_device.h -- 16-bit element types and transposing LDS reads of the adapter
+// and input-gradient kernels (gfx950).
+#pragma once
+
+#include "twq_device.h"
+
+namespace twq {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+
+// A 16-bit element type: its matrix instruction and its conversions. Operands travel as
+// v4i (eight elements of one K run).
+struct F16 {
+    static constexpr bool kBf16 = false;
+    static __device__ __forceinline__ v4f mfma(v4i a, v4i b, v4f c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float to_f32(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
+    static __device__ __forceinline__ uint16_t from_f32(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+};
+struct BF16 {
+    static constexpr bool kBf16 = true;
+    static __device__ __forceinline__ v4f mfma(v4i a, v4i b, v4f c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float to_f32(uint16_t v) { return __builtin_bit_cast(float, (uint32_t)v << 16); }
+    static __device__ __forceinline__ uint16_t from_f32(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+};
+
+__device__ __forceinline__ v4i load16(const void *p) { return *reinterpret_cast<const v4i *>(p); }
+
+// 16-bit element e (0 or 1) of a dword
+__device__ __forceinline__ uint16_t half_of(int w, int e) { return (uint16_t)((uint32_t)w >> (16 * e)); }
+
+// Eight fp16 values as bf16 hi + lo: hi is the value cut to its upper 8 significant
+// bits, lo the rest (3 bits). The sum is the fp16 value exactly (the smallest fp16
+// subnormals are far inside bf16's range).
+__device__ __forceinline__ void split_f16(v4i v, v4i &hi, v4i &lo) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t f0 = __builtin_bit_cast(uint32_t, F16::to_f32(half_of(v[e], 0)));
+        const uint32_t f1 = __builtin_bit_cast(uint32_t, F16::to_f32(half_of(v[e], 1)));
+        hi[e] = (int)__builtin_amdgcn_perm(f1, f0, 0x07060302u);
+        const float l0 = __builtin_bit_cast(float, f0) - __builtin_bit_cast(float, f0 & 0xFFFF0000u);
+        const float l1 = __builtin_bit_cast(float, f1) - __builtin_bit_cast(float, f1 & 0xFFFF0000u);
+        lo[e] = (int)__builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, l1), __builtin_bit_cast(uint32_t, l0), 0x07060302u);
+    }
+}
+
+// Transposing LDS reads. The 16 lanes of a group address a block of 16-bit elements, 4
+// rows (K) x 16 columns: lane i gives the address of columns 4 (i % 4) .. + 3 of row
+// i / 4 (each quarter row anywhere), and receives column i's four rows.
+__device__ __forceinline__ v4s read_tr16(const void *p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)p);
+}
+// The same for bytes: 8 rows x 16 columns, lane i gives columns 8 (i % 2) .. + 7 of row
+// i / 2 and receives column i's eight rows.
+__device__ __forceinline__ v2i read_tr8(const void *p) {
+    return __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i *)p);
+}
+// The same for 4-bit codes: 16 rows x 16 columns, lane i gives row i (8 bytes) and
+// receives column i's sixteen rows, the first in the lowest nibble.
+__device__ __forceinline__ v2i read_tr4(const void *p) {
+    return __builtin_amdgcn_ds_read_tr4_b64_v2i32((__attribute__((address_space(3))) v2i *)p);
+}
+__device__ __forceinline__ v4i join(v4s a, v4s b) {
+    return __builtin_bit_cast(v4i, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Power of two 2^e, e in [-126, 127].
+__device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
+
+// Exponent e with 2^e <= v < 2^(e + 1) for a positive normal v; 0 for 0 (and for
+// subnormals, infinities and NaN, which then pass unscaled).
+__device__ __forceinline__ int exponent_or_zero(float v) {
+    const int e = (int)((__builtin_bit_cast(uint32_t, v) >> 23) & 0xFFu);
+    return e == 0 || e == 255 ? 0 : e - 127;
+}
+
+}  // namespace twq

@@ -7,9 +7,12 @@
 #include <cstdio>
 #include <cstring>
 
+#include "twq_check.h"
 #include "twq_kernels.h"
 
 namespace {
+
+using namespace twq;
 
 thread_local char g_last_error[256] = "";
 
@@ -18,17 +21,6 @@ twq_status hip_fail(hipError_t e, const char *where) {
     return TWQ_ERR_HIP;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-constexpr int64_t kMaxM = 131072;    // keeps 256 * 49 * m below 2^31 in the int32 accumulator
-constexpr int64_t kMaxTokens = int64_t(1) << 24;
-constexpr int64_t kMaxN = int64_t(1) << 24;
-constexpr int64_t kMaxRank = 256;
-
-bool valid_m(int64_t m) { return m > 0 && m % 128 == 0 && m <= kMaxM; }
-bool valid_b(int64_t b) { return b >= 0 && b <= kMaxTokens; }
-bool valid_n(int64_t n) { return n >= 0 && n % 16 == 0 && n <= kMaxN; }
-bool valid_r(int64_t r) { return r >= 0 && r % 16 == 0 && r <= kMaxRank; }
 bool valid_r4(int64_t r) { return r >= 0 && r % 32 == 0 && r <= kMaxRank; }  // int4 low-rank variant
 
 // Workspace of twq_linear: Q_X, s_X, T and the partial sums of T, each 256-byte
@@ -39,8 +31,6 @@ struct LinearLayout {
     bool direct;
     size_t qx, sx, t, partials, total;
 };
-
-size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // group: 0 (one scale per token) or twq::kGroup (s_X group-major [m / kGroup][b])
 // a8: 8-bit activation codes, one byte per element
