@@ -6,7 +6,7 @@
 //
 //   G[i] = B_a^T dy_i,   dX[i] = dx_i + c_a A_a^T G[i].
 //
-// Token rows are grouped by adapter (the plan), so a tile of up to 64 rows shares one
+// Token rows are grouped by adapter (the plan), so a tile of 16 or 64 rows shares one
 // adapter's weights, whatever the order of the requests in the batch; no row is moved.
 // Each product is a pair of launches: shrink (K = the long axis, partial sums over K
 // slices) and expand (K = the rank). Both are bound by memory: shrink by the rows and the
@@ -23,7 +23,7 @@ namespace twq {
 // rows, from which its own first position, first tile and first piece follow, then
 // scans the index again and writes its rows in token order.
 __global__ __launch_bounds__(256) void adapter_plan_kernel(const int32_t *index, int64_t b, int count, uint8_t *plan,
-                                                           PlanLayout L, int chunk) {
+                                                           PlanLayout L, int chunk, int trows) {
     __shared__ int hist[kMaxAdapters + 1];
     __shared__ int red[4][4];
     __shared__ int wsum[4];
@@ -40,7 +40,7 @@ __global__ __launch_bounds__(256) void adapter_plan_kernel(const int32_t *index,
     for (int k = tid; k < a; k += 256) {
         const int c = hist[k];
         s[0] += c;
-        s[1] += (c + kTileRows - 1) / kTileRows;
+        s[1] += (c + trows - 1) / trows;
         s[2] += (c + chunk - 1) / chunk;
         s[3] += c > chunk ? (c + chunk - 1) / chunk : 0;
     }
@@ -52,7 +52,7 @@ __global__ __launch_bounds__(256) void adapter_plan_kernel(const int32_t *index,
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < 4; ++q) s[q] = red[q][0] + red[q][1] + red[q][2] + red[q][3];
-    const int rows = hist[a], ntiles = (rows + kTileRows - 1) / kTileRows, nparts = (rows + chunk - 1) / chunk;
+    const int rows = hist[a], ntiles = (rows + trows - 1) / trows, nparts = (rows + chunk - 1) / chunk;
     int32_t *head = reinterpret_cast<int32_t *>(plan + L.head), *order = reinterpret_cast<int32_t *>(plan + L.order);
     int32_t *offsets = reinterpret_cast<int32_t *>(plan + L.offsets), *slot0 = reinterpret_cast<int32_t *>(plan + L.slot0);
     PlanItem *tiles = reinterpret_cast<PlanItem *>(plan + L.tiles), *chunks = reinterpret_cast<PlanItem *>(plan + L.chunks);
@@ -66,8 +66,8 @@ __global__ __launch_bounds__(256) void adapter_plan_kernel(const int32_t *index,
         }
     }
     for (int j = tid; j < ntiles; j += 256) {
-        const int left = rows - j * kTileRows;
-        tiles[s[1] + j] = PlanItem{a == count ? -1 : a, s[0] + j * kTileRows, left < kTileRows ? left : kTileRows, -1};
+        const int left = rows - j * trows;
+        tiles[s[1] + j] = PlanItem{a == count ? -1 : a, s[0] + j * trows, left < trows ? left : trows, -1};
     }
     if (a < count)
         for (int j = tid; j < nparts; j += 256) {
@@ -92,7 +92,14 @@ __global__ __launch_bounds__(256) void adapter_plan_kernel(const int32_t *index,
             before += w < wave ? wsum[w] : 0;
             all += wsum[w];
         }
-        if (mine) order[pos + before + __popcll(mask & ((uint64_t(1) << lane) - 1))] = (int32_t)i;
+        if (mine) {
+            const int at = pos + before + __popcll(mask & ((uint64_t(1) << lane) - 1)), local = at - s[0];
+            order[at] = (int32_t)i;
+            int32_t *tr = reinterpret_cast<int32_t *>(plan + L.rows) + (int64_t)(s[1] + local / trows) * trows;
+            tr[local % trows] = (int32_t)i;
+            if (local == rows - 1)
+                for (int k = local % trows + 1; k < trows; ++k) tr[k] = (int32_t)i;
+        }
         pos += all;
         __syncthreads();
     }
@@ -100,7 +107,7 @@ __global__ __launch_bounds__(256) void adapter_plan_kernel(const int32_t *index,
 
 hipError_t launch_adapter_plan(const int32_t *index, int64_t b, int64_t count, void *plan, hipStream_t stream) {
     adapter_plan_kernel<<<dim3((unsigned)(count + 1)), 256, 0, stream>>>(index, b, (int)count, static_cast<uint8_t *>(plan),
-                                                                        plan_layout(b, count), chunk_rows(b));
+                                                                        plan_layout(b, count), chunk_rows(b), tile_rows(b));
     return hipGetLastError();
 }
 
@@ -109,246 +116,228 @@ hipError_t launch_adapter_plan(const int32_t *index, int64_t b, int64_t count, v
 struct Tile {
     int adapter, rows;
     int64_t first;
+    const int32_t *row;  // its token rows, the last repeated up to R; NULL: first, first + 1, ..
+    __device__ __forceinline__ int64_t token(int i) const { return row ? (int64_t)row[i] : first + (i < rows ? i : rows - 1); }
 };
 
-// Tile t of the plan (rows == 0: none); without a plan, rows 64 t .. of one adapter.
+// Tile t of the plan (rows == 0: none); without a plan, rows R t .. of one adapter. The
+// plan's entries lie at places known from t alone, so that a CTA's first loads are all in
+// flight together; entries past the last tile are not used.
+template <int R>
 __device__ __forceinline__ Tile tile_of(const PlanView &p, int64_t t, int64_t b) {
-    if (p.order == nullptr) {
-        const int64_t left = b - t * kTileRows;
-        return Tile{0, (int)(left < kTileRows ? left : kTileRows), t * kTileRows};
+    if (p.rows == nullptr) {
+        const int64_t left = b - t * R;
+        return Tile{0, (int)(left < R ? left : R), t * R, nullptr};
     }
-    if (t >= p.head[0]) return Tile{-1, 0, 0};
     const PlanItem it = p.tiles[t];
-    return Tile{it.adapter, it.rows, it.first};
+    return Tile{it.adapter, t < p.head[0] ? it.rows : 0, it.first, p.rows + t * R};
 }
 
-// One tile of up to 16 NG rows x 16 RB ranks over steps [s0, s1) of 64 elements of K; the
-// four waves take batches of U steps in turn. A lane holds 16 elements of a step in two
-// operands (lane group g: elements 16 g .. + 15), the same for rows and weights, so every
-// 128-byte line of a row is read whole by its four lanes. KMAJOR weights ([k][r], ranks
-// contiguous) pass through this wave's own LDS and come back transposed. XW: bf16 rows on
-// fp16 weights, the weights split exactly into two bf16 parts.
-template <class T, int NG, int RB, int U, bool KMAJOR, bool XW>
-__device__ __forceinline__ void shrink_tile(const ShrinkArgs &a, const Tile &t, int rank0, int64_t s0, int64_t s1,
-                                            uint8_t *smem, v4f (&acc)[NG][RB]) {
-    static_assert(!KMAJOR || U == 1, "one step at a time through LDS");
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, li = lane & 15, g = lane >> 4;
-    const uint16_t *w = a.w + (int64_t)t.adapter * a.r * a.k;
-    const uint16_t *row[NG];
+// A tile of 16 NG rows x 16 RB ranks over a slice of K, in stages of 128 elements through
+// LDS. Global loads run along the rows (sixteen lanes to a row's 256 bytes): matrix operands
+// loaded straight to registers would put neighbouring lanes on different rows, which reads
+// L2 at about half the rate (2.9 against 4.4 TB/s of X at 4096 x 14336, 64 ranks). The next
+// stage is in registers while this one is used. With 64 rows (NG = 4) a wave owns 16 rows;
+// with 16 (NG = 1) a quarter of each stage, and the waves' sums are added in wave order.
+// KMAJOR weights ([k][r], ranks contiguous) are read back from LDS transposed. XW: bf16 rows
+// on fp16 weights, the weights split exactly into two bf16 parts.
+template <class T, int NG, int RB, bool KMAJOR, bool XW>
+__global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
+    constexpr int SK = 128, XS = SK * 2 + 16;                         // elements of a stage; padded LDS row of X
+    constexpr int WROWS = KMAJOR ? SK : 16 * RB, WCH = KMAJOR ? 2 * RB : SK / 8;  // rows and 16-byte chunks a row of W
+    constexpr int WS = WCH * 16 + 16;
+    constexpr int XB = 16 * NG * XS, BUF = XB + WROWS * WS;
+    constexpr int RED = NG == 1 ? 4 * RB * kWave * 16 : 0;
+    __shared__ __align__(16) uint8_t smem[2 * BUF > RED ? 2 * BUF : RED];
+    const int64_t id = xcd_order(blockIdx.x, gridDim.x);  // tiles of one slice, and so of one adapter's weights, on one XCD
+    const Tile t = tile_of<16 * NG>(a.plan, id % a.tiles, a.b);
+    if (t.rows == 0 || t.adapter < 0) return;
+    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave, li = lane & 15, g = lane >> 4;
+    const int rtiles = (a.r + 16 * RB - 1) / (16 * RB);
+    const int rank0 = (int)(id / a.tiles % rtiles) * 16 * RB;
+    const int64_t slice = id / a.tiles / rtiles, nst = (a.k + SK - 1) / SK;
+    const int64_t s0 = slice * nst / a.ks, s1 = (slice + 1) * nst / a.ks;
+
+    // chunk j of this thread: row 16 j + tid / 16, elements 8 (tid % 16) of a stage
+    int64_t at[NG];
+    if (t.row) {
 #pragma unroll
-    for (int q = 0; q < NG; ++q) {
-        const int i = q * 16 + li < t.rows ? q * 16 + li : t.rows - 1;
-        const int64_t pos = t.first + i;
-        row[q] = a.v + (a.plan.order ? (int64_t)a.plan.order[pos] : pos) * a.k;
+        for (int j = 0; j < NG; ++j) at[j] = t.row[j * 16 + tid / 16];
+    } else {
+#pragma unroll
+        for (int j = 0; j < NG; ++j) at[j] = t.token(j * 16 + tid / 16);
     }
-    const uint16_t *wrow[RB];
-    if constexpr (!KMAJOR) {
+    const uint16_t *xp[NG], *wp[RB];
+    const uint16_t *w = a.w + (int64_t)t.adapter * a.r * a.k;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) xp[j] = a.v + at[j] * a.k + tid % 16 * 8;
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+        if constexpr (KMAJOR) {
+            const int rr = rank0 + (j * 256 + tid) % WCH * 8;
+            wp[j] = w + (rr < a.r ? rr : a.r - 8);
+        } else {
+            const int rr = rank0 + j * 16 + tid / 16;
+            wp[j] = w + (int64_t)(rr < a.r ? rr : a.r - 1) * a.k + tid % 16 * 8;
+        }
+    }
+    v4i xr[NG], wr[RB];
+    auto load = [&](int64_t st) {
+        const int64_t k0 = st * SK;
+        const int left = (int)(a.k - k0 < SK ? a.k - k0 : SK);  // elements of this stage
+        const bool in = tid % 16 * 8 < left;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) xr[j] = load16(xp[j] + (in ? k0 : 0));
+#pragma unroll
+        for (int j = 0; j < RB; ++j) {
+            if constexpr (KMAJOR) {
+                const int kk = (j * 256 + tid) / WCH;
+                wr[j] = load16(wp[j] + (k0 + (kk < left ? kk : 0)) * a.r);
+            } else {
+                wr[j] = load16(wp[j] + (in ? k0 : 0));
+            }
+        }
+        if (!in) {  // past K: re-read elements, against zero rows
+#pragma unroll
+            for (int j = 0; j < NG; ++j) xr[j] = v4i{0, 0, 0, 0};
+        }
+    };
+    v4f acc[RB] = {};
+    if (s0 < s1) load(s0);
+    for (int64_t st = s0; st < s1; ++st) {
+        uint8_t *buf = smem + (st & 1) * BUF;  // last read two stages ago, before the previous barrier
+#pragma unroll
+        for (int j = 0; j < NG; ++j) *reinterpret_cast<v4i *>(buf + (j * 16 + tid / 16) * XS + tid % 16 * 16) = xr[j];
+#pragma unroll
+        for (int j = 0; j < RB; ++j) {
+            const int c = j * 256 + tid;
+            *reinterpret_cast<v4i *>(buf + XB + c / WCH * WS + c % WCH * 16) = wr[j];
+        }
+        if (st + 1 < s1) load(st + 1);
+        __syncthreads();
+        if (NG > 1 && wave * 16 >= t.rows) continue;
+#pragma unroll
+        for (int u = 0; u < (NG > 1 ? 4 : 1); ++u) {
+            const int e = (NG > 1 ? u : wave) * 32;  // elements e + 8 g .. + 7
+            const v4i xf = load16(buf + ((NG > 1 ? wave * 16 : 0) + li) * XS + (e + g * 8) * 2);
+#pragma unroll
+            for (int c = 0; c < RB; ++c) {
+                v4i wf;
+                if constexpr (KMAJOR) {
+                    const uint8_t *p = buf + XB + (e + g * 8 + li / 4) * WS + (c * 16 + (li % 4) * 4) * 2;
+                    const v4s w0 = read_tr16(p), w1 = read_tr16(p + 4 * WS);
+                    wf = join(w0, w1);
+                } else {
+                    wf = load16(buf + XB + (c * 16 + li) * WS + (e + g * 8) * 2);
+                }
+                if constexpr (XW) {
+                    v4i hi, lo;
+                    split_f16(wf, hi, lo);
+                    acc[c] = T::mfma(lo, xf, acc[c]);
+                    acc[c] = T::mfma(hi, xf, acc[c]);
+                } else {
+                    acc[c] = T::mfma(wf, xf, acc[c]);
+                }
+            }
+        }
+    }
+    // lane: row li, ranks 4 g .. + 3 of each block
+    if constexpr (NG > 1) {
+        const int i = wave * 16 + li;
 #pragma unroll
         for (int c = 0; c < RB; ++c) {
-            const int rank = rank0 + c * 16 + li;
-            wrow[c] = w + (int64_t)(rank < a.r ? rank : a.r - 1) * a.k;
+            const int rank = rank0 + c * 16 + g * 4;
+            if (i < t.rows && rank < a.r) *reinterpret_cast<v4f *>(a.p + ((slice * a.b + t.first + i) * a.r + rank)) = acc[c];
         }
-    }
-    // KMAJOR: this wave's [64 steps of K][16 RB ranks]
-    uint16_t *const wl = reinterpret_cast<uint16_t *>(smem) + wave * 64 * 16 * RB;
-    const int64_t nst = s1 - s0, nb = (nst + 4 * U - 1) / (4 * U);
-    v4i xb[2][U][NG][2], wb[2][U][RB][2];
-    auto load = [&](int64_t bt, auto slot) {
-        constexpr int S = decltype(slot)::value;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t st = s0 + (bt * 4 + wave) * U + u;
-            // steps and runs past the end re-read valid elements and are zeroed in use
-            const int64_t k0 = (st < s1 ? st : s1 - 1) * 64, kc = k0 + g * 16 < a.k ? k0 + g * 16 : a.k - 16;
-#pragma unroll
-            for (int q = 0; q < NG; ++q) {
-                xb[S][u][q][0] = load16(row[q] + kc);
-                xb[S][u][q][1] = load16(row[q] + kc + 8);
-            }
-            if constexpr (!KMAJOR) {
-#pragma unroll
-                for (int c = 0; c < RB; ++c) {
-                    wb[S][u][c][0] = load16(wrow[c] + kc);
-                    wb[S][u][c][1] = load16(wrow[c] + kc + 8);
-                }
-            } else {
-                // chunk q of 8 ranks: row q / (2 RB), ranks 8 (q % (2 RB)) ..
-#pragma unroll
-                for (int c = 0; c < RB; ++c)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int q = (c * 2 + e) * kWave + lane, kr = q / (2 * RB), rr = rank0 + q % (2 * RB) * 8;
-                        const int64_t kk = k0 + kr < a.k ? k0 + kr : a.k - 1;
-                        wb[S][u][c][e] = load16(w + kk * a.r + (rr < a.r ? rr : a.r - 8));
-                    }
-            }
-        }
-    };
-    auto use = [&](int64_t bt, auto slot) {
-        constexpr int S = decltype(slot)::value;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t st = s0 + (bt * 4 + wave) * U + u;
-            const bool live = st < s1 && st * 64 + g * 16 < a.k;
-            if (!live) {
-#pragma unroll
-                for (int q = 0; q < NG; ++q) xb[S][u][q][0] = xb[S][u][q][1] = v4i{0, 0, 0, 0};
-            }
-            if constexpr (KMAJOR) {
-#pragma unroll
-                for (int c = 0; c < RB; ++c)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<v4i *>(wl + ((c * 2 + e) * kWave + lane) * 8) = wb[S][u][c][e];
-                __builtin_amdgcn_wave_barrier();
-                // lane group g reads rows 16 g + 4 q + (li / 4), q = 0..3: its 16 elements of K
-#pragma unroll
-                for (int c = 0; c < RB; ++c)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint16_t *p = wl + (g * 16 + e * 8 + li / 4) * 16 * RB + c * 16 + (li % 4) * 4;
-                        const v4s lo4 = read_tr16(p), hi4 = read_tr16(p + 4 * 16 * RB);
-                        wb[S][u][c][e] = join(lo4, hi4);
-                    }
-                __builtin_amdgcn_wave_barrier();
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int c = 0; c < RB; ++c) {
-                    if constexpr (XW) {
-                        v4i hi, lo;
-                        split_f16(wb[S][u][c][e], hi, lo);
-#pragma unroll
-                        for (int q = 0; q < NG; ++q) {
-                            acc[q][c] = T::mfma(lo, xb[S][u][q][e], acc[q][c]);
-                            acc[q][c] = T::mfma(hi, xb[S][u][q][e], acc[q][c]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < NG; ++q) acc[q][c] = T::mfma(wb[S][u][c][e], xb[S][u][q][e], acc[q][c]);
-                    }
-                }
-        }
-    };
-    using I0 = std::integral_constant<int, 0>;
-    using I1 = std::integral_constant<int, 1>;
-    if (nb > 0) load(0, I0{});
-    for (int64_t bt = 0; bt < nb; bt += 2) {
-        if (bt + 1 < nb) load(bt + 1, I1{});
-        use(bt, I0{});
-        if (bt + 1 >= nb) break;
-        if (bt + 2 < nb) load(bt + 2, I0{});
-        use(bt + 1, I1{});
-    }
-}
-
-// The waves' sums, added in wave order through LDS, to this slice's rows of P.
-template <int NG, int RB>
-__device__ __forceinline__ void shrink_store(const ShrinkArgs &a, const Tile &t, int rank0, int64_t slice, uint8_t *smem,
-                                             const v4f (&acc)[NG][RB]) {
-    v4f *const red = reinterpret_cast<v4f *>(smem);  // [4 waves][RB][64 lanes]
-    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
-#pragma unroll
-    for (int q = 0; q < NG; ++q) {
+    } else {
+        v4f *const red = reinterpret_cast<v4f *>(smem);  // [4 waves][RB][64 lanes]
         __syncthreads();
 #pragma unroll
-        for (int c = 0; c < RB; ++c) red[(wave * RB + c) * kWave + lane] = acc[q][c];
+        for (int c = 0; c < RB; ++c) red[(wave * RB + c) * kWave + lane] = acc[c];
         __syncthreads();
         if (tid < RB * kWave) {
-            const int c = tid / kWave, i = q * 16 + (tid & 15), rank = rank0 + c * 16 + (tid % kWave) / 16 * 4;
+            const int i = tid & 15, rank = rank0 + tid / kWave * 16 + tid % kWave / 16 * 4;
             v4f s = red[tid];
 #pragma unroll
-            for (int w = 1; w < 4; ++w) {
-                const v4f o = red[w * RB * kWave + tid];
+            for (int q = 1; q < 4; ++q) {
+                const v4f o = red[q * RB * kWave + tid];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[e] += o[e];
             }
-            if (i < t.rows && rank < a.r)
-                *reinterpret_cast<v4f *>(a.p + ((slice * a.b + t.first + i) * a.r + rank)) = s;
+            if (i < t.rows && rank < a.r) *reinterpret_cast<v4f *>(a.p + ((slice * a.b + t.first + i) * a.r + rank)) = s;
         }
     }
 }
 
-template <class T, int RB, bool KMAJOR, bool XW>
-__global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
-    __shared__ __align__(16) uint8_t smem[KMAJOR ? 4 * 64 * 16 * RB * 2 : 4 * RB * kWave * 16];
-    const Tile t = tile_of(a.plan, blockIdx.x, a.b);
-    if (t.rows == 0 || t.adapter < 0) return;
-    const int rank0 = blockIdx.y * 16 * RB;
-    const int64_t slice = blockIdx.z, nst = (a.k + 63) / 64;
-    const int64_t s0 = slice * nst / a.ks, s1 = (slice + 1) * nst / a.ks;
-    if (t.rows <= 16) {
-        v4f acc[1][RB] = {};
-        shrink_tile<T, 1, RB, KMAJOR ? 1 : (RB == 1 ? 4 : 2), KMAJOR, XW>(a, t, rank0, s0, s1, smem, acc);
-        shrink_store<1, RB>(a, t, rank0, slice, smem, acc);
-    } else {
-        v4f acc[4][RB] = {};
-        shrink_tile<T, 4, RB, 1, KMAJOR, XW>(a, t, rank0, s0, s1, smem, acc);
-        shrink_store<4, RB>(a, t, rank0, slice, smem, acc);
-    }
-}
-
-// K slices: enough CTAs to fill the 256 compute units twice, at least four steps of 64 a
-// wave-quartet, at most 16 (their partial sums are read again by every expand CTA).
+// K slices: enough CTAs to fill the 256 compute units twice, at least two stages of 128
+// each, at most 16 (the partial sums are read again).
 int shrink_slices(int64_t b, int64_t k, int64_t r, int64_t tiles) {
     (void)b;
-    const int64_t rt = r <= 16 ? 1 : r <= 32 ? 1 : (r + 63) / 64, steps = (k + 63) / 64;
+    const int64_t rt = r <= 16 ? 1 : r <= 32 ? 1 : (r + 63) / 64, steps = (k + 127) / 128;
     int64_t ks = 512 / (tiles * rt);
-    if (ks > steps / 4) ks = steps / 4;
+    if (ks > steps / 2) ks = steps / 2;
     if (ks > 16) ks = 16;
     return ks < 1 ? 1 : (int)ks;
 }
 
-template <class T, bool KMAJOR, bool XW>
+template <class T, int NG, bool KMAJOR, bool XW>
 static hipError_t shrink_ranks(const ShrinkArgs &a, hipStream_t stream) {
     const int rb = a.r <= 16 ? 1 : a.r <= 32 ? 2 : 4;
-    const dim3 grid((unsigned)a.tiles, (unsigned)((a.r + 16 * rb - 1) / (16 * rb)), (unsigned)a.ks);
+    const unsigned grid = (unsigned)(a.tiles * ((a.r + 16 * rb - 1) / (16 * rb)) * a.ks);
     if (rb == 1)
-        shrink_kernel<T, 1, KMAJOR, XW><<<grid, 256, 0, stream>>>(a);
+        shrink_kernel<T, NG, 1, KMAJOR, XW><<<grid, 256, 0, stream>>>(a);
     else if (rb == 2)
-        shrink_kernel<T, 2, KMAJOR, XW><<<grid, 256, 0, stream>>>(a);
+        shrink_kernel<T, NG, 2, KMAJOR, XW><<<grid, 256, 0, stream>>>(a);
     else
-        shrink_kernel<T, 4, KMAJOR, XW><<<grid, 256, 0, stream>>>(a);
+        shrink_kernel<T, NG, 4, KMAJOR, XW><<<grid, 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
+template <class T, bool KMAJOR, bool XW>
+static hipError_t shrink_rows(const ShrinkArgs &a, hipStream_t stream) {
+    return a.b <= kFewRows ? shrink_ranks<T, 1, KMAJOR, XW>(a, stream) : shrink_ranks<T, 4, KMAJOR, XW>(a, stream);
+}
+
 hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t stream) {
-    if (a.bf16 && !a.wbf16) return a.kmajor ? shrink_ranks<BF16, true, true>(a, stream) : hipErrorInvalidValue;
-    if (a.bf16) return a.kmajor ? shrink_ranks<BF16, true, false>(a, stream) : shrink_ranks<BF16, false, false>(a, stream);
-    return a.kmajor ? shrink_ranks<F16, true, false>(a, stream) : shrink_ranks<F16, false, false>(a, stream);
+    if (a.bf16 && !a.wbf16) return a.kmajor ? shrink_rows<BF16, true, true>(a, stream) : hipErrorInvalidValue;
+    if (a.bf16) return a.kmajor ? shrink_rows<BF16, true, false>(a, stream) : shrink_rows<BF16, false, false>(a, stream);
+    return a.kmajor ? shrink_rows<F16, true, false>(a, stream) : shrink_rows<F16, false, false>(a, stream);
 }
 
 // ---- expand --------------------------------------------------------------------------
 
-// The tile's rows of the first product, summed over the slices, times the adapter's
-// scale, as two 16-bit parts hi + lo in LDS: 8 ranks are 32 bytes, hi then lo. One part
-// would round H to the element type, an error of the size of the output's own rounding;
-// the second part costs a matrix instruction on operands at hand. fp16 rows are first
+// A row of the first product, summed over the slices, times the adapter's scale, as two
+// 16-bit parts hi + lo (8 ranks are 32 bytes, hi then lo), by the TPR threads q of a row.
+// One part would round H to the element type, an error of the size of the output's own
+// rounding; the second costs a matrix instruction on operands at hand. fp16 rows are first
 // scaled by a power of two to a largest element in [2^13, 2^14), so neither part can
-// overflow and only elements below 2^-27 of the largest lose bits; rexp holds the exponent
-// to undo. Ranks past r (the last half step) are zero.
-template <class T, int NG>
-__device__ __forceinline__ void expand_rows(const ExpandArgs &a, const Tile &t, float scale, uint8_t *hl, int stride,
-                                            float *rfac, bool store_sum) {
-    constexpr int TPR = 256 / (16 * NG);  // threads a row
-    const int tid = threadIdx.x, i = tid / TPR, q = tid % TPR;
-    const bool live = i < t.rows;
-    const int64_t pos = t.first + (live ? i : 0);
+// overflow and only elements below 2^-27 of the largest lose bits; the return value is
+// the factor that undoes it. Ranks past r (the last half step) are zero. dst also holds
+// the binary32 sums in between.
+template <class T, int TPR>
+__device__ __forceinline__ float split_row(const ExpandArgs &a, int64_t pos, int64_t to, bool live, int q, float scale,
+                                           bool store_sum, uint8_t *dst) {
     const float *src = a.p + pos * a.r;
-    uint8_t *dst = hl + i * stride;
     float mx = 0.f;
     for (int c = q * 8; c < a.r; c += TPR * 8) {
         v4f s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
         if (live) {
-            for (int s = 0; s < a.ks; ++s) {
-                const v4f p0 = *reinterpret_cast<const v4f *>(src + s * a.b * a.r + c);
-                const v4f p1 = *reinterpret_cast<const v4f *>(src + s * a.b * a.r + c + 4);
+            for (int s = 0; s < a.ks; s += 8) {  // eight slices in flight
+                v4f p0[8], p1[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s0[e] += p0[e], s1[e] += p1[e];
+                for (int j = 0; j < 8; ++j) {
+                    const float *ps = src + (s + j < a.ks ? s + j : s) * a.b * a.r + c;
+                    p0[j] = *reinterpret_cast<const v4f *>(ps);
+                    p1[j] = *reinterpret_cast<const v4f *>(ps + 4);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (s + j < a.ks) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s0[e] += p0[j][e], s1[e] += p1[j][e];
+                    }
             }
             if (store_sum) {
-                const int64_t to = a.sum_by_pos || !a.plan.order ? pos : (int64_t)a.plan.order[pos];
                 *reinterpret_cast<v4f *>(a.sum + to * a.r + c) = s0;
                 *reinterpret_cast<v4f *>(a.sum + to * a.r + c + 4) = s1;
             }
@@ -361,13 +350,12 @@ __device__ __forceinline__ void expand_rows(const ExpandArgs &a, const Tile &t, 
         *reinterpret_cast<v4f *>(dst + c * 4) = s0;
         *reinterpret_cast<v4f *>(dst + c * 4 + 16) = s1;
     }
-    float f = 1.f;
+    float f = 1.f, undo = 1.f;
     if constexpr (!T::kBf16) {
         for (int off = TPR / 2; off > 0; off >>= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, off, kWave));
         int e = exponent_or_zero(mx);
         e = e < -100 ? -100 : e;  // 13 - e <= 113, inside the range of pow2
-        f = mx > 0.f && mx < __builtin_inff() ? pow2(13 - e) : 1.f;
-        if (q == 0) rfac[i] = mx > 0.f && mx < __builtin_inff() ? pow2(e - 13) : 1.f;
+        if (mx > 0.f && mx < __builtin_inff()) f = pow2(13 - e), undo = pow2(e - 13);
     }
     for (int c = q * 8; c < a.r; c += TPR * 8) {
         float v[8];
@@ -384,159 +372,294 @@ __device__ __forceinline__ void expand_rows(const ExpandArgs &a, const Tile &t, 
         *reinterpret_cast<v4i *>(dst + c * 4) = hi;
         *reinterpret_cast<v4i *>(dst + c * 4 + 16) = lo;
     }
-    if (a.r % 32)
-        for (int c = a.r + q * 8; c < (a.r + 31) / 32 * 32; c += TPR * 8)
-            *reinterpret_cast<v4i *>(dst + c * 4) = *reinterpret_cast<v4i *>(dst + c * 4 + 16) = v4i{0, 0, 0, 0};
+    for (int c = a.r + q * 8; c < (a.r + 31) / 32 * 32; c += TPR * 8)
+        *reinterpret_cast<v4i *>(dst + c * 4) = *reinterpret_cast<v4i *>(dst + c * 4 + 16) = v4i{0, 0, 0, 0};
+    return undo;
 }
 
-// 64 output columns from col0 of the tile's rows, by one wave. Sub-tile s (of four) of
-// the matrix product holds columns 16 (i / 4) + 4 s + i % 4, i = 0..15, so a lane ends
-// with 16 consecutive columns of one row: two 16-byte loads and stores.
-template <class T, int NG, bool KMAJOR>
-__device__ __forceinline__ void expand_block(const ExpandArgs &a, const Tile &t, const uint16_t *w, int64_t col0,
-                                             const uint8_t *hl, int stride, const float *rfac, const int *rows,
-                                             uint16_t *wl) {
-    const int lane = threadIdx.x % kWave, li = lane & 15, g = lane >> 4;
-    v4f acc[NG][4] = {};
-    const int64_t mycol = col0 + g * 16;
-    v4i base[NG][2];
-#pragma unroll
-    for (int q = 0; q < NG; ++q) {
-        const int i = q * 16 + li;
-        if (a.base && i < t.rows && mycol < a.n) {
-            const uint16_t *p = a.base + (int64_t)rows[i] * a.n + mycol;
-            base[q][0] = load16(p);
-            base[q][1] = load16(p + 8);
-        } else {
-            base[q][0] = base[q][1] = v4i{0, 0, 0, 0};
-        }
+// Bytes of a row's parts.
+__host__ __device__ inline int parts_bytes(int r) { return (r + 31) / 32 * 128; }
+
+// Many rows: every column block of expand needs the rows' parts, so one launch forms them
+// once, 16 threads a row. (With few rows expand forms them itself and saves the launch.)
+template <class T>
+__global__ __launch_bounds__(256) void split_kernel(ExpandArgs a) {
+    const Tile t = tile_of<64>(a.plan, blockIdx.x / 4, a.b);
+    const int i = (blockIdx.x % 4) * 16 + threadIdx.x / 16, q = threadIdx.x % 16;
+    if (i >= t.rows) return;
+    const int64_t pos = t.first + i, row = t.row[i];
+    if (t.adapter < 0) {
+        if (a.sum && !a.sum_by_pos)
+            for (int c = q * 4; c < a.r; c += 64) *reinterpret_cast<v4f *>(a.sum + row * a.r + c) = v4f{0.f, 0.f, 0.f, 0.f};
+        return;
     }
-    for (int k0 = 0; k0 < a.r; k0 += 32) {
-        v4i wf[4];
-        if constexpr (!KMAJOR) {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int64_t col = col0 + (li / 4) * 16 + s * 4 + li % 4;
-                const int k = k0 + g * 8 < a.r ? k0 + g * 8 : a.r - 8;
-                wf[s] = load16(w + (col < a.n ? col : a.n - 1) * a.r + k);
-            }
-        } else {
-            // 32 ranks x 64 columns to this wave's LDS, eight columns a chunk
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = j * kWave + lane, k = k0 + c / 8;
-                const int64_t col = col0 + c % 8 * 8;
-                const v4i v = load16(w + (int64_t)(k < a.r ? k : a.r - 1) * a.n + (col < a.n ? col : a.n - 8));
-                *reinterpret_cast<v4i *>(wl + c * 8) = v;
-            }
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const uint16_t *p = wl + (g * 8 + li / 4) * 64 + (li % 4) * 16 + s * 4;
-                const v4s p0 = read_tr16(p), p1 = read_tr16(p + 4 * 64);
-                wf[s] = join(p0, p1);
-            }
-            __builtin_amdgcn_wave_barrier();
-        }
-#pragma unroll
-        for (int q = 0; q < NG; ++q) {
-            const uint8_t *p = hl + (q * 16 + li) * stride + (k0 + g * 8) * 4;
-            const v4i hi = load16(p), lo = load16(p + 16);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                acc[q][s] = T::mfma(wf[s], lo, acc[q][s]);
-                acc[q][s] = T::mfma(wf[s], hi, acc[q][s]);
-            }
-        }
-    }
-    if (mycol >= a.n) return;
-#pragma unroll
-    for (int q = 0; q < NG; ++q) {
-        const int i = q * 16 + li;
-        if (i >= t.rows) continue;
-        const float f = T::kBf16 ? 1.f : rfac[i];
-        v4i o[2];
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int word = base[q][s / 2][(s % 2) * 2 + e];
-                const float v0 = T::to_f32(half_of(word, 0)) + acc[q][s][2 * e] * f;
-                const float v1 = T::to_f32(half_of(word, 1)) + acc[q][s][2 * e + 1] * f;
-                o[s / 2][(s % 2) * 2 + e] = (int)((uint32_t)T::from_f32(v0) | (uint32_t)T::from_f32(v1) << 16);
-            }
-        uint16_t *p = a.out + (int64_t)rows[i] * a.n + mycol;
-        *reinterpret_cast<v4i *>(p) = o[0];
-        *reinterpret_cast<v4i *>(p + 8) = o[1];
-    }
+    const float undo = split_row<T, 16>(a, pos, a.sum_by_pos ? pos : row, true, q, a.scale ? a.scale[t.adapter] : 1.f,
+                                        a.sum != nullptr, a.parts + pos * parts_bytes(a.r));
+    if (q == 0) a.undo[pos] = undo;
 }
+
+// The weights of 64 output columns from col0, for one wave: KS steps of 32 ranks x four
+// sub-tiles of 16 columns. Memory is read along its rows ([n][r], or [r][n] if KMAJOR) into
+// registers (fetch); then, 32 KP ranks at a time, through this wave's LDS into matrix operands
+// (place), transposed if KMAJOR.
+template <int KS, bool KMAJOR>
+struct Weights {
+    static constexpr int KP = KMAJOR || KS < 2 ? 1 : 2;             // steps of 32 ranks a pass
+    static constexpr int STRIDE = KMAJOR ? 64 * 2 + 16 : KP * 64 + 16;  // padded LDS row
+    static constexpr int BYTES = (KMAJOR ? 32 : 64) * STRIDE;
+    v4i in[KS / KP][KP * 4];
+    __device__ __forceinline__ void fetch(const ExpandArgs &a, const uint16_t *w, int64_t col0) {
+        const int lane = threadIdx.x % kWave;
+#pragma unroll
+        for (int p = 0; p < KS / KP; ++p)
+#pragma unroll
+            for (int j = 0; j < KP * 4; ++j) {
+                const int c = j * kWave + lane;
+                if constexpr (KMAJOR) {
+                    const int k = p * 32 + c / 8;
+                    const int64_t col = col0 + c % 8 * 8;
+                    in[p][j] = load16(w + (int64_t)(k < a.r ? k : a.r - 1) * a.n + (col < a.n ? col : a.n - 8));
+                } else {
+                    const int k = p * KP * 32 + c % (KP * 4) * 8;  // past r: parts are zero
+                    const int64_t col = col0 + c / (KP * 4);
+                    in[p][j] = load16(w + (col < a.n ? col : a.n - 1) * a.r + (k < a.r ? k : a.r - 8));
+                }
+            }
+    }
+    __device__ __forceinline__ void place(uint8_t *wl, v4i (&wf)[KS][4]) const {
+        const int lane = threadIdx.x % kWave, li = lane & 15, g = lane >> 4;
+        constexpr int CH = KMAJOR ? 8 : KP * 4;  // 16-byte chunks a row
+#pragma unroll
+        for (int p = 0; p < KS / KP; ++p) {
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int j = 0; j < KP * 4; ++j) {
+                const int c = j * kWave + lane;
+                *reinterpret_cast<v4i *>(wl + c / CH * STRIDE + c % CH * 16) = in[p][j];
+            }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int k = 0; k < KP; ++k)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    if constexpr (KMAJOR) {
+                        const uint8_t *q = wl + (g * 8 + li / 4) * STRIDE + (s * 16 + (li % 4) * 4) * 2;
+                        const v4s q0 = read_tr16(q), q1 = read_tr16(q + 4 * STRIDE);
+                        wf[p][s] = join(q0, q1);
+                    } else {
+                        wf[p * KP + k][s] = load16(wl + (s * 16 + li) * STRIDE + (k * 32 + g * 8) * 2);
+                    }
+                }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+};
 
 // Rows without an adapter: out = base (or 0), sums 0.
-__device__ __forceinline__ void expand_plain(const ExpandArgs &a, const int *rows, int nrows, int64_t c0, int64_t c1,
-                                             bool store_sum) {
+__device__ __forceinline__ void expand_plain(const ExpandArgs &a, const Tile &t, int64_t c0, int64_t c1, bool store_sum) {
     if (store_sum && !a.sum_by_pos)
-        for (int j = threadIdx.x; j < nrows * (a.r / 4); j += 256)
-            *reinterpret_cast<v4f *>(a.sum + (int64_t)rows[j / (a.r / 4)] * a.r + j % (a.r / 4) * 4) = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int j = threadIdx.x; j < t.rows * (a.r / 4); j += 256)
+            *reinterpret_cast<v4f *>(a.sum + (int64_t)t.row[j / (a.r / 4)] * a.r + j % (a.r / 4) * 4) =
+                v4f{0.f, 0.f, 0.f, 0.f};
     if (a.base == a.out) return;
     const int per = (int)((c1 - c0) / 8);
-    for (int j = threadIdx.x; j < nrows * per; j += 256) {
-        const int64_t at = (int64_t)rows[j / per] * a.n + c0 + j % per * 8;
+    for (int j = threadIdx.x; j < t.rows * per; j += 256) {
+        const int64_t at = (int64_t)t.row[j / per] * a.n + c0 + j % per * 8;
         *reinterpret_cast<v4i *>(a.out + at) = a.base ? load16(a.base + at) : v4i{0, 0, 0, 0};
     }
 }
 
-template <class T, bool KMAJOR>
-__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int64_t nc) {
-    extern __shared__ __align__(16) uint8_t dyn[];
-    const Tile t = tile_of(a.plan, blockIdx.x, a.b);
-    if (t.rows == 0) return;
-    int *const rows = reinterpret_cast<int *>(dyn);             // [64] token rows
-    float *const rfac = reinterpret_cast<float *>(dyn + 256);   // [64]
-    uint16_t *const wl = reinterpret_cast<uint16_t *>(dyn + 512) + (threadIdx.x / kWave) * (KMAJOR ? 2048 : 0);
-    uint8_t *const hl = dyn + 512 + (KMAJOR ? 16384 : 0);
-    if ((int)threadIdx.x < t.rows)
-        rows[threadIdx.x] = (int)(a.plan.order ? a.plan.order[t.first + threadIdx.x] : t.first + threadIdx.x);
-    const int64_t c0 = blockIdx.y * nc, c1 = c0 + nc < a.n ? c0 + nc : a.n;
-    const bool store_sum = a.sum && blockIdx.y == 0;
-    if (t.adapter < 0) {
-        __syncthreads();
-        expand_plain(a, rows, t.rows, c0, c1, store_sum);
-        return;
+// 16 rows x 64 columns of one wave: products with the rows' parts in LDS (i0: the first row),
+// turned in this wave's LDS so that eight lanes hold one row's 64 columns, added to the base
+// and stored. rows[h], base[h]: this lane's row 8 h + lane / 8 of the 16 (negative: none) and
+// its base at columns col0 + 8 (lane % 8).
+template <class T, int KS, int STRIDE>
+__device__ __forceinline__ void expand_store(const ExpandArgs &a, const uint8_t *parts, const float *undo, int i0, int last,
+                                             const int64_t (&rows)[2], int64_t col0, const v4i (&wf)[KS][4],
+                                             const v4i (&base)[2], uint8_t *wl) {
+    constexpr int TS = 64 * 4 + 16;  // padded row of the turned block
+    const int lane = threadIdx.x % kWave, li = lane & 15, g = lane >> 4;
+    const int i = i0 + li < last ? i0 + li : last;
+    v4f acc[4] = {};
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+        if (k * 32 >= a.r) break;  // r = 96: the last step has no parts
+        const uint8_t *p = parts + i * STRIDE + (k * 32 + g * 8) * 4;
+        const v4i hi = load16(p), lo = load16(p + 16);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            acc[s] = T::mfma(wf[k][s], lo, acc[s]);
+            acc[s] = T::mfma(wf[k][s], hi, acc[s]);
+        }
     }
-    const float scale = a.scale ? a.scale[t.adapter] : 1.f;
-    const int stride = (a.r + 31) / 32 * 128 + 16;
-    const uint16_t *w = a.w + (int64_t)t.adapter * a.r * a.n;
-    const int wave = threadIdx.x / kWave;
-    if (t.rows <= 16) {
-        expand_rows<T, 1>(a, t, scale, hl, stride, rfac, store_sum);
-        __syncthreads();
-        for (int64_t c = c0 + wave * 64; c < c1; c += 256) expand_block<T, 1, KMAJOR>(a, t, w, c, hl, stride, rfac, rows, wl);
-    } else {
-        expand_rows<T, 4>(a, t, scale, hl, stride, rfac, store_sum);
-        __syncthreads();
-        for (int64_t c = c0 + wave * 64; c < c1; c += 256) expand_block<T, 4, KMAJOR>(a, t, w, c, hl, stride, rfac, rows, wl);
+    const float f = T::kBf16 ? 1.f : undo[i];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[s][e] *= f;
+        *reinterpret_cast<v4f *>(wl + li * TS + (s * 16 + g * 4) * 4) = acc[s];
+    }
+    __builtin_amdgcn_wave_barrier();
+    const int64_t col = col0 + lane % 8 * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint8_t *p = wl + (h * 8 + lane / 8) * TS + lane % 8 * 32;
+        const v4f d0 = *reinterpret_cast<const v4f *>(p), d1 = *reinterpret_cast<const v4f *>(p + 16);
+        v4i o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float x0 = e < 2 ? d0[2 * e] : d1[2 * e - 4], x1 = e < 2 ? d0[2 * e + 1] : d1[2 * e - 3];
+            const float v0 = T::to_f32(half_of(base[h][e], 0)) + x0, v1 = T::to_f32(half_of(base[h][e], 1)) + x1;
+            o[e] = (int)((uint32_t)T::from_f32(v0) | (uint32_t)T::from_f32(v1) << 16);
+        }
+        if (rows[h] >= 0 && col < a.n) *reinterpret_cast<v4i *>(a.out + rows[h] * a.n + col) = o;
     }
 }
 
-template <class T, bool KMAJOR>
-static hipError_t expand_launch(const ExpandArgs &a, hipStream_t stream) {
-    // columns a CTA: 256 (64 a wave), more where that still leaves four CTAs a compute unit
-    int64_t nc = 256;
-    while (nc < 1024 && a.tiles * ((a.n + 2 * nc - 1) / (2 * nc)) >= 1024) nc *= 2;
-    const size_t lds = 512 + (KMAJOR ? 16384 : 0) + (size_t)kTileRows * ((a.r + 31) / 32 * 128 + 16);
-    const dim3 grid((unsigned)a.tiles, (unsigned)((a.n + nc - 1) / nc));
-    if (lds > 65536) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(expand_kernel<T, KMAJOR>),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-        if (e != hipSuccess) return e;
+// This lane's rows 8 h + lane / 8 of the 16 from row i0 of the tile (past its end: the
+// complement of the last row).
+__device__ __forceinline__ void expand_rows(const ExpandArgs &a, const Tile &t, int i0, int64_t (&rows)[2]) {
+    const int lane = threadIdx.x % kWave;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = i0 + h * 8 + lane / 8;
+        const int32_t row = t.row[i];
+        rows[h] = i < t.rows ? row : ~row;
     }
-    expand_kernel<T, KMAJOR><<<grid, 256, lds, stream>>>(a, nc);
+}
+
+// Their base at this lane's eight columns (0 without a base). Rows and columns past the end
+// re-read others.
+__device__ __forceinline__ void expand_base(const ExpandArgs &a, const int64_t (&rows)[2], int64_t col0, v4i (&base)[2]) {
+    const int64_t col = col0 + threadIdx.x % 8 * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        base[h] = a.base ? load16(a.base + (rows[h] < 0 ? ~rows[h] : rows[h]) * a.n + (col < a.n ? col : a.n - 8)) : v4i{0, 0, 0, 0};
+}
+
+constexpr int kTurnBytes = 16 * (64 * 4 + 16);
+
+// Many rows: a tile of 64 x 256 columns, 64 a wave. Row numbers, bases, weights and the rows'
+// parts (split_kernel's, to LDS) are all requested before the first is used, and nothing is
+// loaded after the first store (loads and stores share a counter).
+template <class T, int KS, bool KMAJOR>
+__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int ncol) {
+    using W = Weights<KS, KMAJOR>;
+    constexpr int R = 64, STRIDE = KS * 128 + 16, NQ = R / 16;  // padded LDS row of parts
+    constexpr int WB = W::BYTES > kTurnBytes ? W::BYTES : kTurnBytes;
+    __shared__ __align__(16) uint8_t parts[R * STRIDE];
+    __shared__ float undo[R];
+    __shared__ __align__(16) uint8_t wlds[4][WB];
+    const int64_t id = xcd_order(blockIdx.x, gridDim.x);  // a tile's columns, and one adapter's weights, on one XCD
+    const Tile t = tile_of<R>(a.plan, id / ncol, a.b);
+    if (t.rows == 0) return;
+    const int64_t c0 = id % ncol * 256, c1 = c0 + 256 < a.n ? c0 + 256 : a.n;
+    if (t.adapter < 0) return expand_plain(a, t, c0, c1, false);
+    const int tid = threadIdx.x, wave = tid / kWave;
+    const int64_t col0 = c0 + wave * 64;
+
+    int64_t rows[NQ][2];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) expand_rows(a, t, q * 16, rows[q]);
+    v4i base[NQ][2], wf[KS][4];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) expand_base(a, rows[q], col0, base[q]);
+    W in;
+    in.fetch(a, a.w + (int64_t)t.adapter * a.r * a.n, col0);
+    const int per = parts_bytes(a.r) / 16, total = t.rows * per;
+    const uint8_t *src = a.parts + t.first * parts_bytes(a.r);
+    constexpr int N = R * KS * 8 / 256;
+    v4i pin[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int c = j * 256 + tid;
+        pin[j] = load16(src + (c < total ? c : total - 1) * 16);
+    }
+    const float u = a.undo[t.first + (tid < t.rows ? tid : 0)];
+    in.place(wlds[wave], wf);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int c = j * 256 + tid;
+        if (c < total) *reinterpret_cast<v4i *>(parts + c / per * STRIDE + c % per * 16) = pin[j];
+    }
+    if (tid < R) undo[tid] = u;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+        if (q * 16 >= t.rows) break;
+        expand_store<T, KS, STRIDE>(a, parts, undo, q * 16, t.rows - 1, rows[q], col0, wf, base[q], wlds[wave]);
+    }
+}
+
+// Few rows: a tile of 16 x `blocks` runs of 256 columns, 64 a wave. The rows' parts are
+// formed here, once for all the runs, while the first run's weights are on their way; the
+// next run's weights are requested before this one's are used.
+template <class T, int KS, bool KMAJOR>
+__global__ __launch_bounds__(256) void expand_few_kernel(ExpandArgs a, int ncol, int blocks) {
+    using W = Weights<KS, KMAJOR>;
+    constexpr int STRIDE = KS * 128 + 16;
+    constexpr int WB = W::BYTES > kTurnBytes ? W::BYTES : kTurnBytes;
+    __shared__ __align__(16) uint8_t parts[16 * STRIDE];
+    __shared__ float undo[16];
+    __shared__ __align__(16) uint8_t wlds[4][WB];
+    const Tile t = tile_of<16>(a.plan, blockIdx.x / ncol, a.b);
+    if (t.rows == 0) return;
+    const int64_t c0 = (int64_t)(blockIdx.x % ncol) * 256 * blocks, c1 = c0 + 256 * blocks < a.n ? c0 + 256 * blocks : a.n;
+    const bool store_sum = a.sum && c0 == 0;
+    if (t.adapter < 0) return expand_plain(a, t, c0, c1, store_sum);
+    const int tid = threadIdx.x, wave = tid / kWave;
+    const uint16_t *w = a.w + (int64_t)t.adapter * a.r * a.n;
+    int64_t col0 = c0 + wave * 64, rows[2];
+    v4i base[2], wf[KS][4];
+    W in;
+    in.fetch(a, w, col0);
+    expand_rows(a, t, 0, rows);
+    {
+        const int i = tid / 16, q = tid % 16;
+        const int64_t pos = t.first + (i < t.rows ? i : 0);
+        const float u = split_row<T, 16>(a, pos, a.sum_by_pos ? pos : (int64_t)t.row[i], i < t.rows, q,
+                                         a.scale ? a.scale[t.adapter] : 1.f, store_sum, parts + i * STRIDE);
+        if (q == 0) undo[i] = u;
+    }
+    __syncthreads();
+    for (; col0 < c1; col0 += 256) {
+        in.place(wlds[wave], wf);
+        expand_base(a, rows, col0, base);
+        if (col0 + 256 < c1) in.fetch(a, w, col0 + 256);
+        expand_store<T, KS, STRIDE>(a, parts, undo, 0, t.rows - 1, rows, col0, wf, base, wlds[wave]);
+    }
+}
+
+template <class T, int KS, bool KMAJOR>
+static hipError_t expand_launch(const ExpandArgs &a, hipStream_t stream) {
+    if (a.b > kFewRows) {
+        const int ncol = (int)((a.n + 255) / 256);
+        split_kernel<T><<<(unsigned)(a.tiles * 4), 256, 0, stream>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        expand_kernel<T, KS, KMAJOR><<<(unsigned)(a.tiles * ncol), 256, 0, stream>>>(a, ncol);
+        return hipGetLastError();
+    }
+    // runs a CTA: more where that still leaves four CTAs a compute unit
+    int blocks = 1;
+    while (blocks < 8 && a.tiles * ((a.n + 511 * blocks) / (512 * blocks)) >= 1024) blocks *= 2;
+    const int ncol = (int)((a.n + 256 * blocks - 1) / (256 * blocks));
+    expand_few_kernel<T, KS, KMAJOR><<<(unsigned)(a.tiles * ncol), 256, 0, stream>>>(a, ncol, blocks);
     return hipGetLastError();
 }
 
+template <class T, bool KMAJOR>
+static hipError_t expand_ranks(const ExpandArgs &a, hipStream_t stream) {
+    if (a.r <= 32) return expand_launch<T, 1, KMAJOR>(a, stream);
+    if (a.r <= 64) return expand_launch<T, 2, KMAJOR>(a, stream);
+    if (a.r <= 128) return expand_launch<T, 4, KMAJOR>(a, stream);
+    return expand_launch<T, 8, KMAJOR>(a, stream);
+}
+
 hipError_t launch_expand(const ExpandArgs &a, hipStream_t stream) {
-    if (a.bf16) return a.kmajor ? expand_launch<BF16, true>(a, stream) : expand_launch<BF16, false>(a, stream);
-    return a.kmajor ? expand_launch<F16, true>(a, stream) : expand_launch<F16, false>(a, stream);
+    if (a.bf16) return a.kmajor ? expand_ranks<BF16, true>(a, stream) : expand_ranks<BF16, false>(a, stream);
+    return a.kmajor ? expand_ranks<F16, true>(a, stream) : expand_ranks<F16, false>(a, stream);
 }
 
 }  // namespace twq

@@ -25,13 +25,29 @@ twq_status done(hipError_t e, const char *name) { return e == hipSuccess ? TWQ_O
 
 const uint16_t *u16(const void *p) { return static_cast<const uint16_t *>(p); }
 
-struct GradLayout {
+struct ForwardLayout {
     int ks;
-    size_t p, g, part, total;
+    size_t p, parts, total;
 };
 
-size_t forward_bytes(int64_t b, int64_t k, int64_t r, int64_t count) {
-    return align256((size_t)shrink_slices(b, k, r, plan_layout(b, count).max_tiles) * b * r * 4);
+struct GradLayout {
+    int ks;
+    size_t p, parts, g, part, total;
+};
+
+ForwardLayout forward_layout(int64_t b, int64_t k, int64_t r, int64_t count) {
+    ForwardLayout L{};
+    L.ks = shrink_slices(b, k, r, plan_layout(b, count).max_tiles);
+    L.p = 0;
+    L.parts = align256((size_t)L.ks * b * r * 4);
+    L.total = L.parts + align256(expand_parts_bytes(b, r));
+    return L;
+}
+
+// The two scratch arrays of expand, one behind the other.
+void set_parts(ExpandArgs &a, uint8_t *at) {
+    a.parts = at;
+    a.undo = reinterpret_cast<float *>(at + (size_t)a.b * ((size_t)(a.r + 31) / 32 * 128));
 }
 
 GradLayout grad_layout(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count) {
@@ -39,7 +55,8 @@ GradLayout grad_layout(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count
     GradLayout L{};
     L.ks = b > 0 ? shrink_slices(b, n, r, pl.max_tiles) : 1;
     L.p = 0;
-    L.g = align256((size_t)L.ks * b * r * 4);
+    L.parts = align256((size_t)L.ks * b * r * 4);
+    L.g = L.parts + align256(expand_parts_bytes(b, r));
     L.part = L.g + align256((size_t)b * r * 4);
     L.total = L.part + align256((size_t)pl.max_slots * r * (m + n) * 4);
     return L;
@@ -64,7 +81,7 @@ twq_status twq_adapter_plan(const int32_t *index, int64_t b, int64_t count, void
 
 size_t twq_adapters_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count) {
     if (!valid_shape(b, m, n, r) || r == 0 || !valid_count(count) || b == 0) return 0;
-    return forward_bytes(b, m, r, count);
+    return forward_layout(b, m, r, count).total;
 }
 
 twq_status twq_adapters(const void *x, const void *at, const void *bt, const float *scale, const void *plan,
@@ -78,7 +95,8 @@ twq_status twq_adapters(const void *x, const void *at, const void *bt, const flo
         !aligned16(out) || !aligned16(h))
         return TWQ_ERR_ALIGN;
     const PlanLayout pl = plan_layout(b, count);
-    if (plan_bytes < pl.total || !workspace || workspace_bytes < forward_bytes(b, m, r, count)) return TWQ_ERR_WORKSPACE;
+    const ForwardLayout L = forward_layout(b, m, r, count);
+    if (plan_bytes < pl.total || !workspace || workspace_bytes < L.total) return TWQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return TWQ_ERR_ALIGN;
     const hipStream_t st = static_cast<hipStream_t>(stream);
 
@@ -91,7 +109,7 @@ twq_status twq_adapters(const void *x, const void *at, const void *bt, const flo
     s.bf16 = s.wbf16 = type == TWQ_BF16;
     s.plan = plan_view(plan, pl);
     s.tiles = pl.max_tiles;
-    s.ks = shrink_slices(b, m, r, pl.max_tiles);
+    s.ks = L.ks;
     s.p = static_cast<float *>(workspace);
     hipError_t e = launch_shrink(s, st);
     if (e != hipSuccess) return done(e, "twq_adapters");
@@ -110,6 +128,7 @@ twq_status twq_adapters(const void *x, const void *at, const void *bt, const flo
     x2.base = u16(y);
     x2.out = static_cast<uint16_t *>(out);
     x2.sum = h;
+    set_parts(x2, static_cast<uint8_t *>(workspace) + L.parts);
     return done(launch_expand(x2, st), "twq_adapters");
 }
 
@@ -171,6 +190,7 @@ twq_status twq_adapters_grad(const void *dy, const void *x, const void *qc, cons
     x2.out = static_cast<uint16_t *>(dx_out);
     x2.sum = reinterpret_cast<float *>(ws + L.g);
     x2.sum_by_pos = 1;
+    set_parts(x2, ws + L.parts);
     if (b > 0) e = launch_expand(x2, st);
     if (e != hipSuccess || count == 0) return done(e, "twq_adapters_grad");
 
@@ -247,7 +267,7 @@ twq_status twq_linear_dx(const void *dy, const void *qw, const float *sw, const 
         s.r = (int)r;
         s.bf16 = type == TWQ_BF16;
         s.kmajor = 1;
-        s.tiles = (b + kTileRows - 1) / kTileRows;
+        s.tiles = (b + tile_rows(b) - 1) / tile_rows(b);
         s.ks = p.tks;
         s.p = reinterpret_cast<float *>(ws + p.t);
         e = launch_shrink(s, st);

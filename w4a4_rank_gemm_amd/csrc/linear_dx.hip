@@ -362,7 +362,7 @@ DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
     if (ks > stages / 4) ks = stages / 4;
     if (ks > 16) ks = 16;
     p.ks = ks < 1 ? 1 : (int)ks;
-    p.tks = r > 0 ? shrink_slices(b, n, r, (b + kTileRows - 1) / kTileRows) : 0;
+    p.tks = r > 0 ? shrink_slices(b, n, r, (b + tile_rows(b) - 1) / tile_rows(b)) : 0;
     p.g = 0;
     p.ge = up((size_t)b * p.npad * 2);
     p.t = p.ge + up((size_t)b * 8);

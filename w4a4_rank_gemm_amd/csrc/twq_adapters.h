@@ -10,7 +10,10 @@ namespace twq {
 
 // ---- the plan of a batch: its token rows sorted by adapter ---------------------------
 
-constexpr int kTileRows = 64;         // token rows of one tile (never two adapters in one)
+// Token rows of one tile (never two adapters in one): 16 up to 256 rows, which the kernels
+// for few rows take, 64 above.
+constexpr int kFewRows = 256;
+inline int tile_rows(int64_t b) { return b <= kFewRows ? 16 : 64; }
 constexpr int64_t kMaxAdapters = 4096;
 
 // Rows of one piece of an adapter's tokens in the weight-gradient kernel. Longer pieces
@@ -31,6 +34,7 @@ struct PlanLayout {
     size_t offsets;  // int32 [count + 2]: first position of each adapter; of the rows without; b
     size_t slot0;    // int32 [count]: first partial-sum slot of each adapter
     size_t tiles;    // PlanItem [max_tiles]
+    size_t rows;     // int32 [max_tiles][tile_rows(b)]: each tile's token rows, the last one repeated to the end
     size_t chunks;   // PlanItem [max_chunks]
     int64_t max_tiles, max_chunks, max_slots;
     size_t total;
@@ -40,7 +44,7 @@ inline PlanLayout plan_layout(int64_t b, int64_t count) {
     auto up = [](size_t v) { return (v + 63) & ~size_t(63); };
     PlanLayout L{};
     // sum over adapters of ceil(n_a / T) <= b / T + the number of adapters with tokens
-    L.max_tiles = b / kTileRows + (count + 1 < b ? count + 1 : b);
+    L.max_tiles = b / tile_rows(b) + (count + 1 < b ? count + 1 : b);
     L.max_chunks = b / chunk_rows(b) + (count < b ? count : b);
     // adapters of several pieces only: ceil(n / T) < 2 n / T for n > T
     L.max_slots = 2 * b / chunk_rows(b);
@@ -49,13 +53,14 @@ inline PlanLayout plan_layout(int64_t b, int64_t count) {
     L.offsets = up(L.order + (size_t)b * 4);
     L.slot0 = up(L.offsets + (size_t)(count + 2) * 4);
     L.tiles = up(L.slot0 + (size_t)count * 4);
-    L.chunks = up(L.tiles + (size_t)L.max_tiles * sizeof(PlanItem));
+    L.rows = up(L.tiles + (size_t)L.max_tiles * sizeof(PlanItem));
+    L.chunks = up(L.rows + (size_t)L.max_tiles * tile_rows(b) * 4);
     L.total = up(L.chunks + (size_t)L.max_chunks * sizeof(PlanItem));
     return L;
 }
 
 struct PlanView {
-    const int32_t *head, *order, *offsets, *slot0;
+    const int32_t *head, *order, *offsets, *slot0, *rows;
     const PlanItem *tiles, *chunks;
 };
 
@@ -63,6 +68,7 @@ inline PlanView plan_view(const void *plan, const PlanLayout &L) {
     const uint8_t *p = static_cast<const uint8_t *>(plan);
     return PlanView{reinterpret_cast<const int32_t *>(p + L.head),    reinterpret_cast<const int32_t *>(p + L.order),
                     reinterpret_cast<const int32_t *>(p + L.offsets), reinterpret_cast<const int32_t *>(p + L.slot0),
+                    reinterpret_cast<const int32_t *>(p + L.rows),
                     reinterpret_cast<const PlanItem *>(p + L.tiles),  reinterpret_cast<const PlanItem *>(p + L.chunks)};
 }
 
@@ -78,7 +84,7 @@ struct ShrinkArgs {
     int bf16;            // type of v
     int wbf16;           // type of w
     int kmajor;
-    PlanView plan;       // order == NULL: one adapter, positions are rows
+    PlanView plan;       // rows == NULL: one adapter, positions are rows
     int64_t tiles;       // grid bound
     int ks;              // K slices
     float *p;            // [ks][b][r]
@@ -103,7 +109,12 @@ struct ExpandArgs {
     uint16_t *out;         // [b][n]; may be base
     float *sum;            // sum_s P (unscaled), or NULL
     int sum_by_pos;        // sum is [b][r] by position in the plan instead of by token row
+    uint8_t *parts;        // more than kFewRows rows: [b][r rounded up to 32][2] 16-bit scratch
+    float *undo;           // more than kFewRows rows: [b] scratch
 };
+inline size_t expand_parts_bytes(int64_t b, int64_t r) {
+    return b > kFewRows ? (size_t)b * ((size_t)(r + 31) / 32 * 128 + 4) : 0;
+}
 hipError_t launch_expand(const ExpandArgs &a, hipStream_t stream);
 
 // ---- weight gradients -------------------------------------------------------------------
