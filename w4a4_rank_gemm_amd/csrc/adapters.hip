@@ -19,40 +19,57 @@ namespace twq {
 
 // ---- plan ----------------------------------------------------------------------------
 
+constexpr int kPlanThreads = 1024;
+
 // CTA a owns adapter a (CTA `count`: the rows without one). It counts every adapter's
 // rows, from which its own first position, first tile and first piece follow, then
 // scans the index again and writes its rows in token order.
-__global__ __launch_bounds__(256) void adapter_plan_kernel(const int32_t *index, int64_t b, int count, uint8_t *plan,
+__global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_t *index, int64_t b, int count, uint8_t *plan,
                                                            PlanLayout L, int chunk, int trows) {
     __shared__ int hist[kMaxAdapters + 1];
-    __shared__ int red[4][4];
-    __shared__ int wsum[4];
+    __shared__ int red[7][kPlanThreads / kWave];
+    __shared__ int wsum[kPlanThreads / kWave];
     const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
     const int a = blockIdx.x;
-    for (int k = tid; k <= count; k += 256) hist[k] = 0;
+    for (int k = tid; k <= count; k += kPlanThreads) hist[k] = 0;
     __syncthreads();
-    for (int64_t i = tid; i < b; i += 256) {
+    for (int64_t i = tid; i < b; i += kPlanThreads) {
         const int key = index[i];
         atomicAdd(&hist[(unsigned)key < (unsigned)count ? key : count], 1);
     }
     __syncthreads();
-    int s[4] = {0, 0, 0, 0};  // rows, tiles, pieces, partial-sum slots before adapter a
-    for (int k = tid; k < a; k += 256) {
+    const int rows = hist[a], rest = rows % chunk;
+    // Rows, tiles, whole pieces and partial-sum slots before adapter a; all whole pieces; the
+    // shorter pieces before a's; all shorter pieces. Pieces lie longest first, so that no long
+    // one starts last.
+    int s[7] = {0, 0, 0, 0, 0, 0, 0};
+    for (int k = tid; k <= count; k += kPlanThreads) {
         const int c = hist[k];
-        s[0] += c;
-        s[1] += (c + trows - 1) / trows;
-        s[2] += (c + chunk - 1) / chunk;
-        s[3] += c > chunk ? (c + chunk - 1) / chunk : 0;
+        if (k < a) {
+            s[0] += c;
+            s[1] += (c + trows - 1) / trows;
+            s[2] += c / chunk;
+            s[3] += c > chunk ? (c + chunk - 1) / chunk : 0;
+        }
+        if (k < count) {
+            s[4] += c / chunk;
+            const int other = c % chunk;
+            s[5] += other > rest || (other == rest && k < a);
+            s[6] += other > 0;
+        }
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 7; ++q) {
         for (int off = 32; off > 0; off >>= 1) s[q] += __shfl_xor(s[q], off, kWave);
         if (lane == 0) red[q][wave] = s[q];
     }
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) s[q] = red[q][0] + red[q][1] + red[q][2] + red[q][3];
-    const int rows = hist[a], ntiles = (rows + trows - 1) / trows, nparts = (rows + chunk - 1) / chunk;
+    for (int q = 0; q < 7; ++q) {
+        s[q] = 0;
+        for (int w = 0; w < kPlanThreads / kWave; ++w) s[q] += red[q][w];
+    }
+    const int ntiles = (rows + trows - 1) / trows, nparts = (rows + chunk - 1) / chunk;
     int32_t *head = reinterpret_cast<int32_t *>(plan + L.head), *order = reinterpret_cast<int32_t *>(plan + L.order);
     int32_t *offsets = reinterpret_cast<int32_t *>(plan + L.offsets), *slot0 = reinterpret_cast<int32_t *>(plan + L.slot0);
     PlanItem *tiles = reinterpret_cast<PlanItem *>(plan + L.tiles), *chunks = reinterpret_cast<PlanItem *>(plan + L.chunks);
@@ -62,21 +79,22 @@ __global__ __launch_bounds__(256) void adapter_plan_kernel(const int32_t *index,
         if (a == count) {
             offsets[count + 1] = s[0] + rows;
             head[0] = s[1] + ntiles;
-            head[1] = s[2];
+            head[1] = s[4] + s[6];
         }
     }
-    for (int j = tid; j < ntiles; j += 256) {
+    for (int j = tid; j < ntiles; j += kPlanThreads) {
         const int left = rows - j * trows;
         tiles[s[1] + j] = PlanItem{a == count ? -1 : a, s[0] + j * trows, left < trows ? left : trows, -1};
     }
     if (a < count)
-        for (int j = tid; j < nparts; j += 256) {
+        for (int j = tid; j < nparts; j += kPlanThreads) {
             const int left = rows - j * chunk;
-            chunks[s[2] + j] = PlanItem{a, s[0] + j * chunk, left < chunk ? left : chunk, nparts > 1 ? s[3] + j : -1};
+            chunks[left < chunk ? s[4] + s[5] : s[2] + j] =
+                PlanItem{a, s[0] + j * chunk, left < chunk ? left : chunk, nparts > 1 ? s[3] + j : -1};
         }
     if (rows == 0) return;
     int pos = s[0];
-    for (int64_t i0 = 0; i0 < b; i0 += 256) {
+    for (int64_t i0 = 0; i0 < b; i0 += kPlanThreads) {
         const int64_t i = i0 + tid;
         bool mine = false;
         if (i < b) {
@@ -88,7 +106,7 @@ __global__ __launch_bounds__(256) void adapter_plan_kernel(const int32_t *index,
         __syncthreads();
         int before = 0, all = 0;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < kPlanThreads / kWave; ++w) {
             before += w < wave ? wsum[w] : 0;
             all += wsum[w];
         }
@@ -106,7 +124,7 @@ __global__ __launch_bounds__(256) void adapter_plan_kernel(const int32_t *index,
 }
 
 hipError_t launch_adapter_plan(const int32_t *index, int64_t b, int64_t count, void *plan, hipStream_t stream) {
-    adapter_plan_kernel<<<dim3((unsigned)(count + 1)), 256, 0, stream>>>(index, b, (int)count, static_cast<uint8_t *>(plan),
+    adapter_plan_kernel<<<dim3((unsigned)(count + 1)), kPlanThreads, 0, stream>>>(index, b, (int)count, static_cast<uint8_t *>(plan),
                                                                         plan_layout(b, count), chunk_rows(b), tile_rows(b));
     return hipGetLastError();
 }
@@ -306,6 +324,20 @@ hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t stream) {
 
 // ---- expand --------------------------------------------------------------------------
 
+// Four binary32 values as bf16 hi + lo (16 significant bits) to two arrays.
+__device__ __forceinline__ void put_planes(uint16_t *hi, uint16_t *lo, const v4f &v) {
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const uint16_t h0 = BF16::from_f32(v[2 * e]), h1 = BF16::from_f32(v[2 * e + 1]);
+        const uint16_t l0 = BF16::from_f32(v[2 * e] - BF16::to_f32(h0)), l1 = BF16::from_f32(v[2 * e + 1] - BF16::to_f32(h1));
+        h[e] = (uint32_t)h0 | (uint32_t)h1 << 16;
+        l[e] = (uint32_t)l0 | (uint32_t)l1 << 16;
+    }
+    *reinterpret_cast<uint2 *>(hi) = make_uint2(h[0], h[1]);
+    *reinterpret_cast<uint2 *>(lo) = make_uint2(l[0], l[1]);
+}
+
 // A row of the first product, summed over the slices, times the adapter's scale, as two
 // 16-bit parts hi + lo (8 ranks are 32 bytes, hi then lo), by the TPR threads q of a row.
 // One part would round H to the element type, an error of the size of the output's own
@@ -315,7 +347,7 @@ hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t stream) {
 // the factor that undoes it. Ranks past r (the last half step) are zero. dst also holds
 // the binary32 sums in between.
 template <class T, int TPR>
-__device__ __forceinline__ float split_row(const ExpandArgs &a, int64_t pos, int64_t to, bool live, int q, float scale,
+__device__ __forceinline__ float split_row(const ExpandArgs &a, int64_t pos, int64_t row, bool live, int q, float scale,
                                            bool store_sum, uint8_t *dst) {
     const float *src = a.p + pos * a.r;
     float mx = 0.f;
@@ -337,15 +369,26 @@ __device__ __forceinline__ float split_row(const ExpandArgs &a, int64_t pos, int
                         for (int e = 0; e < 4; ++e) s0[e] += p0[j][e], s1[e] += p1[j][e];
                     }
             }
-            if (store_sum) {
-                *reinterpret_cast<v4f *>(a.sum + to * a.r + c) = s0;
-                *reinterpret_cast<v4f *>(a.sum + to * a.r + c + 4) = s1;
+            if (store_sum && a.sum) {
+                const int64_t to = (a.sum_by_pos ? pos : row) * a.r + c;
+                *reinterpret_cast<v4f *>(a.sum + to) = s0;
+                *reinterpret_cast<v4f *>(a.sum + to + 4) = s1;
             }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             s0[e] *= scale, s1[e] *= scale;
             mx = __builtin_fmaxf(mx, __builtin_fmaxf(__builtin_fabsf(s0[e]), __builtin_fabsf(s1[e])));
+        }
+        if (store_sum && live && a.planes) {
+            const int64_t n = a.b * a.r, to = pos * a.r + c;
+            put_planes(a.planes + to, a.planes + n + to, s0);
+            put_planes(a.planes + to + 4, a.planes + n + to + 4, s1);
+            v4f h0 = *reinterpret_cast<const v4f *>(a.h + row * a.r + c), h1 = *reinterpret_cast<const v4f *>(a.h + row * a.r + c + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h0[e] *= scale, h1[e] *= scale;
+            put_planes(a.planes + 2 * n + to, a.planes + 3 * n + to, h0);
+            put_planes(a.planes + 2 * n + to + 4, a.planes + 3 * n + to + 4, h1);
         }
         *reinterpret_cast<v4f *>(dst + c * 4) = s0;
         *reinterpret_cast<v4f *>(dst + c * 4 + 16) = s1;
@@ -393,8 +436,8 @@ __global__ __launch_bounds__(256) void split_kernel(ExpandArgs a) {
             for (int c = q * 4; c < a.r; c += 64) *reinterpret_cast<v4f *>(a.sum + row * a.r + c) = v4f{0.f, 0.f, 0.f, 0.f};
         return;
     }
-    const float undo = split_row<T, 16>(a, pos, a.sum_by_pos ? pos : row, true, q, a.scale ? a.scale[t.adapter] : 1.f,
-                                        a.sum != nullptr, a.parts + pos * parts_bytes(a.r));
+    const float undo = split_row<T, 16>(a, pos, row, true, q, a.scale ? a.scale[t.adapter] : 1.f, true,
+                                        a.parts + pos * parts_bytes(a.r));
     if (q == 0) a.undo[pos] = undo;
 }
 
@@ -606,8 +649,8 @@ __global__ __launch_bounds__(256) void expand_few_kernel(ExpandArgs a, int ncol,
     const Tile t = tile_of<16>(a.plan, blockIdx.x / ncol, a.b);
     if (t.rows == 0) return;
     const int64_t c0 = (int64_t)(blockIdx.x % ncol) * 256 * blocks, c1 = c0 + 256 * blocks < a.n ? c0 + 256 * blocks : a.n;
-    const bool store_sum = a.sum && c0 == 0;
-    if (t.adapter < 0) return expand_plain(a, t, c0, c1, store_sum);
+    const bool store_sum = c0 == 0;
+    if (t.adapter < 0) return expand_plain(a, t, c0, c1, store_sum && a.sum);
     const int tid = threadIdx.x, wave = tid / kWave;
     const uint16_t *w = a.w + (int64_t)t.adapter * a.r * a.n;
     int64_t col0 = c0 + wave * 64, rows[2];
@@ -618,7 +661,7 @@ __global__ __launch_bounds__(256) void expand_few_kernel(ExpandArgs a, int ncol,
     {
         const int i = tid / 16, q = tid % 16;
         const int64_t pos = t.first + (i < t.rows ? i : 0);
-        const float u = split_row<T, 16>(a, pos, a.sum_by_pos ? pos : (int64_t)t.row[i], i < t.rows, q,
+        const float u = split_row<T, 16>(a, pos, t.row[i], i < t.rows, q,
                                          a.scale ? a.scale[t.adapter] : 1.f, store_sum, parts + i * STRIDE);
         if (q == 0) undo[i] = u;
     }

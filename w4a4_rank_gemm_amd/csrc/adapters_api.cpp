@@ -32,7 +32,7 @@ struct ForwardLayout {
 
 struct GradLayout {
     int ks;
-    size_t p, parts, g, part, total;
+    size_t p, parts, g, planes, part, total;
 };
 
 ForwardLayout forward_layout(int64_t b, int64_t k, int64_t r, int64_t count) {
@@ -57,7 +57,8 @@ GradLayout grad_layout(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count
     L.p = 0;
     L.parts = align256((size_t)L.ks * b * r * 4);
     L.g = L.parts + align256(expand_parts_bytes(b, r));
-    L.part = L.g + align256((size_t)b * r * 4);
+    L.planes = L.g + align256((size_t)b * r * 4);
+    L.part = L.planes + align256((size_t)b * r * 8);
     L.total = L.part + align256((size_t)pl.max_slots * r * (m + n) * 4);
     return L;
 }
@@ -188,15 +189,17 @@ twq_status twq_adapters_grad(const void *dy, const void *x, const void *qc, cons
     x2.tiles = pl.max_tiles;
     x2.base = u16(dx);
     x2.out = static_cast<uint16_t *>(dx_out);
-    x2.sum = reinterpret_cast<float *>(ws + L.g);
+    x2.sum = x ? nullptr : reinterpret_cast<float *>(ws + L.g);
     x2.sum_by_pos = 1;
+    x2.planes = reinterpret_cast<uint16_t *>(ws + L.planes);
+    x2.h = h;
     set_parts(x2, ws + L.parts);
     if (b > 0) e = launch_expand(x2, st);
     if (e != hipSuccess || count == 0) return done(e, "twq_adapters_grad");
 
     OuterArgs o{};
     o.g = x2.sum;
-    o.h = h;
+    o.planes = x2.planes;
     o.x = u16(x);
     o.qc = x ? nullptr : static_cast<const int8_t *>(qc);
     o.sc = sc;

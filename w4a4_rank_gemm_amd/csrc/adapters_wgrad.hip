@@ -8,19 +8,21 @@
 // both gradients are one launch. Each element of X and dY is read once; X may come as an
 // 8-bit checkpoint, whose codes feed the matrix cores as they are.
 //
-// The binary32 factor (G or H, times c_a and, with a checkpoint, the group's scale of the
-// token) is split into two bf16 parts, 16 significant bits together; codes (at most 127)
-// and bf16 elements are exact in bf16, fp16 elements are split exactly into two parts.
-// bf16 rather than fp16: gradients span more binades than fp16 has.
+// The binary32 factor, c_a G or c_a H, comes as two bf16 parts, 16 significant bits together
+// (expand's planes); with a checkpoint c_a G still takes the group's scale of the token and is
+// split here. Codes (at most 127) and bf16 elements are exact in bf16, fp16 elements are split
+// exactly into two parts. bf16 rather than fp16: gradients span more binades than fp16 has.
 #include "twq_adapters.h"
 #include "twq_adapters_device.h"
 
 namespace twq {
 
 constexpr int kStep = 32;    // token rows of one matrix instruction
-constexpr int kCols = 128;   // columns of X or dY a CTA (one checkpoint group)
 
 enum Src { kSrcF16, kSrcBF16, kSrcI8 };
+
+// Columns of X or dY a CTA, 32 a wave; of a checkpoint that is one group.
+constexpr int kCols = 128, kBlocks = 2;
 
 // Eight codes (one column's eight rows) to bf16, exactly.
 __device__ __forceinline__ v4i codes_to_bf16(v2i c) {
@@ -34,51 +36,66 @@ __device__ __forceinline__ v4i codes_to_bf16(v2i c) {
     return r;
 }
 
-// OUT[c][s] (RB rank blocks x 2 column blocks of a wave) += P^T Z over the piece's rows.
+// OUT[s][c] (RB rank blocks x the column blocks of a wave) += P^T Z over the piece's rows.
 // RANKS_M: ranks are the rows of the result blocks (dB, stored with ranks contiguous), else
 // the columns of Z are (dA).
 template <int RB, Src SRC, bool RANKS_M>
 __device__ __forceinline__ void outer_piece(const OuterArgs &a, const PlanItem &it, int col0, int rank0, const int *rows,
-                                            uint8_t *smem, v4f (&acc)[2][RB]) {
+                                            uint8_t *smem, v4f (&acc)[kBlocks][RB]) {
     constexpr int ZB = SRC == kSrcI8 ? 1 : 2;                  // bytes of an element of Z
     constexpr int ZROW = kCols * ZB + 16, PROW = RB * 32 + 16; // padded LDS rows
     constexpr int ZBYTES = kStep * ZROW, PBYTES = kStep * PROW, BUF = ZBYTES + 2 * PBYTES;
     constexpr int ZN = kStep * kCols * ZB / 16 / 256;          // 16-byte chunks of Z a thread
-    constexpr int PC = RB * 4, PN = (kStep * PC + 255) / 256;  // chunks of four ranks a row; a thread
+    // the factor's chunks of a step: four binary32 ranks (codes), or eight bf16 ranks of a plane
+    constexpr int PC = SRC == kSrcI8 ? RB * 4 : RB * 2, PALL = kStep * PC * (SRC == kSrcI8 ? 1 : 2), PN = (PALL + 255) / 256;
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, li = lane & 15, g = lane >> 4;
-    const int64_t ld = RANKS_M ? a.n : a.m;
+    const uint32_t ld = (uint32_t)(RANKS_M ? a.n : a.m);
     const uint8_t *z = SRC == kSrcI8 ? reinterpret_cast<const uint8_t *>(a.qc)
                                      : reinterpret_cast<const uint8_t *>(RANKS_M ? a.dy : a.x);
-    const float scale = a.scale ? a.scale[it.adapter] : 1.f;
+    const float scale = SRC == kSrcI8 && a.scale ? a.scale[it.adapter] : 1.f;
+    const uint16_t *planes = a.planes + (RANKS_M ? 2 : 0) * a.b * a.r + (int64_t)it.first * a.r + rank0;
     const float *sc = SRC == kSrcI8 ? a.sc + (int64_t)(col0 / 128) * a.b : nullptr;
     const int nst = (it.rows + kStep - 1) / kStep;
 
-    v4i zr[ZN];
-    v4f pr[PN];
-    float ps[PN];
-    auto load = [&](int st) {
+    v4i zr2[2][ZN];
+    v4f pr2[2][PN];
+    float ps2[2][PN];
+    // Unconditional, with clamped addresses: a load under a condition would leave the number of
+    // loads in flight open, and the wait for the older step would wait for the newer one too.
+    // Rows and ranks past the end re-read others and are cleared when stored.
+    auto load = [&](int st, auto slot) {
+        constexpr int S = decltype(slot)::value;
+        v4i (&zr)[ZN] = zr2[S];
+        v4f (&pr)[PN] = pr2[S];
+        float (&ps)[PN] = ps2[S];
 #pragma unroll
         for (int j = 0; j < ZN; ++j) {
             constexpr int PER = kCols * ZB / 16;
             const int q = j * 256 + tid, i = st * kStep + q / PER;
-            const int64_t row = rows[i < it.rows ? i : it.rows - 1];
-            const int64_t c = col0 + q % PER * (16 / ZB);
-            zr[j] = load16(z + (row * ld + (c < ld ? c : ld - 16 / ZB)) * ZB);
+            const uint32_t row = (uint32_t)rows[i < it.rows ? i : it.rows - 1];
+            const uint32_t c = col0 + q % PER * (16 / ZB);
+            zr[j] = load16(z + ((uint64_t)row * (ld * ZB) + (c < ld ? c : ld - 16 / ZB) * ZB));
         }
 #pragma unroll
         for (int j = 0; j < PN; ++j) {
-            const int q = j * 256 + tid, i = st * kStep + q / PC, rank = rank0 + q % PC * 4;
-            pr[j] = v4f{0.f, 0.f, 0.f, 0.f};
-            ps[j] = 0.f;
-            if (q < kStep * PC && i < it.rows && rank < a.r) {
-                const int64_t row = rows[i];
-                pr[j] = *reinterpret_cast<const v4f *>(RANKS_M ? a.h + row * a.r + rank : a.g + (int64_t)(it.first + i) * a.r + rank);
-                ps[j] = SRC == kSrcI8 ? scale * sc[row] : scale;
+            const int q = j * 256 + tid, i0 = st * kStep + q / PC % kStep, i = i0 < it.rows ? i0 : it.rows - 1;
+            if constexpr (SRC == kSrcI8) {
+                const int rank = rank0 + q % PC * 4;
+                pr[j] = *reinterpret_cast<const v4f *>(a.g + (int64_t)(it.first + i) * a.r + (rank < a.r ? rank : 0));
+                ps[j] = sc[rows[i]];
+            } else {
+                const int rank = q % PC * 8;
+                pr[j] = *reinterpret_cast<const v4f *>(planes + q / (kStep * PC) % 2 * a.b * a.r +
+                                                       (uint64_t)(uint32_t)i * (uint32_t)a.r + (rank0 + rank < a.r ? rank : 0));
             }
         }
     };
-    auto store = [&](int st) {
-        uint8_t *buf = smem + (st & 1) * BUF;
+    auto store = [&](int st, auto slot) {
+        constexpr int S = decltype(slot)::value;
+        const v4i (&zr)[ZN] = zr2[S];
+        const v4f (&pr)[PN] = pr2[S];
+        const float (&ps)[PN] = ps2[S];
+        uint8_t *buf = smem + S * BUF;
 #pragma unroll
         for (int j = 0; j < ZN; ++j) {
             constexpr int PER = kCols * ZB / 16;
@@ -87,12 +104,19 @@ __device__ __forceinline__ void outer_piece(const OuterArgs &a, const PlanItem &
         }
 #pragma unroll
         for (int j = 0; j < PN; ++j) {
-            const int q = j * 256 + tid;
-            if (kStep * PC % 256 && q >= kStep * PC) break;
+            const int q = j * 256 + tid, rank = rank0 + q % PC * (SRC == kSrcI8 ? 4 : 8);
+            if (PALL % 256 && q >= PALL) break;
+            const bool live = st * kStep + q / PC % kStep < it.rows && rank < a.r;
+            if constexpr (SRC != kSrcI8) {
+                *reinterpret_cast<v4f *>(buf + ZBYTES + q / (kStep * PC) * PBYTES + q / PC % kStep * PROW + q % PC * 16) =
+                    live ? pr[j] : v4f{0.f, 0.f, 0.f, 0.f};
+                continue;
+            }
+            const float f = live ? scale * ps[j] : 0.f;
             uint32_t hi[2], lo[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float v0 = pr[j][2 * e] * ps[j], v1 = pr[j][2 * e + 1] * ps[j];
+                const float v0 = live ? pr[j][2 * e] * f : 0.f, v1 = live ? pr[j][2 * e + 1] * f : 0.f;
                 const uint16_t h0 = BF16::from_f32(v0), h1 = BF16::from_f32(v1);
                 const uint16_t l0 = BF16::from_f32(v0 - BF16::to_f32(h0)), l1 = BF16::from_f32(v1 - BF16::to_f32(h1));
                 hi[e] = (uint32_t)h0 | (uint32_t)h1 << 16;
@@ -103,16 +127,18 @@ __device__ __forceinline__ void outer_piece(const OuterArgs &a, const PlanItem &
             *reinterpret_cast<uint2 *>(p + PBYTES) = make_uint2(lo[0], lo[1]);
         }
     };
-    load(0);
-    for (int st = 0; st < nst; ++st) {
-        store(st);  // the buffer was last read in step st - 2, before the barrier of st - 1
-        if (st + 1 < nst) load(st + 1);
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    auto step = [&](int st, auto slot) {
+        __builtin_amdgcn_sched_barrier(0);  // keep this step's waits from moving before the last step's work
+        store(st, slot);  // the buffer was last read in step st - 2, before the barrier of st - 1
+        load(st + 2, slot);
         __syncthreads();
-        const uint8_t *buf = smem + (st & 1) * BUF;
-        v4i zf[2], zl[2];
+        const uint8_t *buf = smem + decltype(slot)::value * BUF;
+        v4i zf[kBlocks], zl[kBlocks];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int c = wave * 32 + s * 16;
+        for (int s = 0; s < kBlocks; ++s) {
+            const int c = (wave * kBlocks + s) * 16;
             if constexpr (SRC == kSrcI8) {
                 zf[s] = codes_to_bf16(read_tr8(buf + (g * 8 + li / 2) * ZROW + c + (li % 2) * 8));
             } else {
@@ -129,7 +155,7 @@ __device__ __forceinline__ void outer_piece(const OuterArgs &a, const PlanItem &
             const v4s l0 = read_tr16(p + PBYTES), l1 = read_tr16(p + PBYTES + 4 * PROW);
             const v4i hi = join(h0, h1), lo = join(l0, l1);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
+            for (int s = 0; s < kBlocks; ++s) {
                 auto add = [&](v4i p16, v4i z16) {
                     acc[s][c] = RANKS_M ? BF16::mfma(p16, z16, acc[s][c]) : BF16::mfma(z16, p16, acc[s][c]);
                 };
@@ -138,6 +164,14 @@ __device__ __forceinline__ void outer_piece(const OuterArgs &a, const PlanItem &
                 add(hi, zf[s]);
             }
         }
+    };
+    // Two steps of rows in flight; an odd last step is followed by one of cleared rows, so that
+    // the loop has no branch (which would cost a wait for every load at its end).
+    load(0, S0{});
+    load(1, S1{});
+    for (int st = 0; st < nst; st += 2) {
+        step(st, S0{});
+        step(st + 1, S1{});
     }
 }
 
@@ -155,32 +189,47 @@ __device__ __forceinline__ void outer_put(const OuterArgs &a, uint16_t *out, flo
 
 template <class T, int RB, bool CODES>
 __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a) {
+    constexpr Src ZS = T::kBf16 ? kSrcBF16 : kSrcF16, XS = CODES ? kSrcI8 : ZS;
     constexpr int BUF = kStep * (kCols * 2 + 16) + 2 * kStep * (RB * 32 + 16);
     __shared__ __align__(16) uint8_t smem[2 * BUF];
-    __shared__ int rows[2048];
-    if ((int)blockIdx.x >= a.plan.head[1]) return;
-    const PlanItem it = a.plan.chunks[blockIdx.x];
-    for (int i = threadIdx.x; i < it.rows; i += 256) rows[i] = a.plan.order[it.first + i];
+    __shared__ int rows[kMaxChunk];
+    const int nt = (int)((a.n + kCols - 1) / kCols), ct = nt + (int)(a.m / kCols), tile = (int)(blockIdx.x % ct);
+    const int64_t piece = blockIdx.x / ct;
+    if (piece >= a.plan.head[1]) return;
+    const PlanItem it = a.plan.chunks[piece];
+    {
+        int in[kMaxChunk / 256];
+#pragma unroll
+        for (int j = 0; j < kMaxChunk / 256; ++j) {
+            const int i = j * 256 + threadIdx.x;
+            in[j] = a.plan.order[it.first + (i < it.rows ? i : it.rows - 1)];
+        }
+#pragma unroll
+        for (int j = 0; j < kMaxChunk / 256; ++j) rows[j * 256 + threadIdx.x] = in[j];
+    }
     __syncthreads();
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, li = lane & 15, g = lane >> 4;
-    const int mt = (int)(a.m / kCols), rank0 = blockIdx.z * RB * 16;
+    const int rank0 = blockIdx.y * RB * 16;
     float *const part = it.slot < 0 ? nullptr : a.part + (int64_t)it.slot * a.r * (a.m + a.n);
-    v4f acc[2][RB] = {};
-    if ((int)blockIdx.y < mt) {
-        const int col0 = blockIdx.y * kCols;
-        outer_piece<RB, CODES ? kSrcI8 : T::kBf16 ? kSrcBF16 : kSrcF16, false>(a, it, col0, rank0, rows, smem, acc);
+    if (tile >= nt) {
+        v4f acc[kBlocks][RB] = {};
+        const int col0 = (tile - nt) * kCols;
+        outer_piece<RB, XS, false>(a, it, col0, rank0, rows, smem, acc);
         uint16_t *const out = a.dat + (int64_t)it.adapter * a.r * a.m;
 #pragma unroll
         for (int c = 0; c < RB; ++c) {
             const int rank = rank0 + c * 16 + li;
             if (rank >= a.r) continue;
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-                outer_put<T>(a, out, part, (int64_t)rank * a.m + col0 + wave * 32 + s * 16 + g * 4, acc[s][c]);
+            for (int s = 0; s < kBlocks; ++s) {
+                const int64_t col = col0 + (wave * kBlocks + s) * 16 + g * 4;
+                outer_put<T>(a, out, part, (int64_t)rank * a.m + col, acc[s][c]);
+            }
         }
     } else {
-        const int col0 = (blockIdx.y - mt) * kCols;
-        outer_piece<RB, T::kBf16 ? kSrcBF16 : kSrcF16, true>(a, it, col0, rank0, rows, smem, acc);
+        v4f acc[kBlocks][RB] = {};
+        const int col0 = tile * kCols;
+        outer_piece<RB, ZS, true>(a, it, col0, rank0, rows, smem, acc);
         uint16_t *const out = a.dbt + (int64_t)it.adapter * a.r * a.n;
         float *const bp = part ? part + (int64_t)a.r * a.m : nullptr;
 #pragma unroll
@@ -188,8 +237,8 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a) {
             const int rank = rank0 + c * 16 + g * 4;
             if (rank >= a.r) continue;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int64_t col = col0 + wave * 32 + s * 16 + li;
+            for (int s = 0; s < kBlocks; ++s) {
+                const int64_t col = col0 + (wave * kBlocks + s) * 16 + li;
                 if (col < a.n) outer_put<T>(a, out, bp, col * a.r + rank, acc[s][c]);
             }
         }
@@ -222,7 +271,7 @@ __global__ __launch_bounds__(256) void outer_join_kernel(OuterArgs a) {
 template <class T, bool CODES>
 static hipError_t outer_ranks(const OuterArgs &a, hipStream_t stream) {
     const int rb = a.r <= 16 ? 1 : a.r <= 32 ? 2 : a.r <= 64 ? 4 : 8;
-    const dim3 grid((unsigned)a.chunks, (unsigned)(a.m / kCols + (a.n + kCols - 1) / kCols),
+    const dim3 grid((unsigned)(a.chunks * (a.m / kCols + (a.n + kCols - 1) / kCols)),
                     (unsigned)((a.r + 16 * rb - 1) / (16 * rb)));
     if (rb == 1)
         outer_kernel<T, 1, CODES><<<grid, 256, 0, stream>>>(a);

@@ -17,8 +17,11 @@ inline int tile_rows(int64_t b) { return b <= kFewRows ? 16 : 64; }
 constexpr int64_t kMaxAdapters = 4096;
 
 // Rows of one piece of an adapter's tokens in the weight-gradient kernel. Longer pieces
-// write fewer partial sums, shorter ones give more CTAs.
-inline int chunk_rows(int64_t b) { return b >= 8192 ? 2048 : b >= 2048 ? 1024 : 512; }
+// write fewer partial sums, shorter ones share the work better. At 8192 rows of 16 ragged
+// adapters (4096 -> 14336, 64 ranks) pieces of 2048, 1024 and 512 rows took 87, 94 and 103 us
+// with the joining of the sums; at 2048 rows of 8 (32 ranks) 1024 and 512 rows 24.6 and 28 us.
+constexpr int kMaxChunk = 2048;
+inline int chunk_rows(int64_t b) { return b >= 8192 ? kMaxChunk : b >= 2048 ? 1024 : 512; }
 
 // One tile or piece: adapter (-1: the rows without one), first position in `order`, rows,
 // and for a piece the slot of its partial sums (-1: the only piece of its adapter, which
@@ -107,8 +110,10 @@ struct ExpandArgs {
     int64_t tiles;
     const uint16_t *base;  // [b][n] or NULL (0)
     uint16_t *out;         // [b][n]; may be base
-    float *sum;            // sum_s P (unscaled), or NULL
-    int sum_by_pos;        // sum is [b][r] by position in the plan instead of by token row
+    float *sum;            // sum_s P (unscaled) [b][r], or NULL
+    int sum_by_pos;        // sum is by position in the plan instead of by token row
+    uint16_t *planes;      // bf16 [4][b][r] by position: c sum_s P as hi + lo, c h as hi + lo; or NULL
+    const float *h;        // with planes: [b][r] by token row
     uint8_t *parts;        // more than kFewRows rows: [b][r rounded up to 32][2] 16-bit scratch
     float *undo;           // more than kFewRows rows: [b] scratch
 };
@@ -120,8 +125,8 @@ hipError_t launch_expand(const ExpandArgs &a, hipStream_t stream);
 // ---- weight gradients -------------------------------------------------------------------
 
 struct OuterArgs {
-    const float *g;        // [b][r] by position: dY B (unscaled)
-    const float *h;        // [b][r] by token row: X A
+    const float *g;        // [b][r] by position: dY B (unscaled); with qc
+    const uint16_t *planes;  // bf16 [4][b][r] by position: c dY B as hi + lo, c X A as hi + lo
     const uint16_t *x;     // [b][m], or NULL: qc, sc
     const int8_t *qc;      // [b][m] codes
     const float *sc;       // [m / 128][b]
