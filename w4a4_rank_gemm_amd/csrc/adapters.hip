@@ -157,9 +157,10 @@ __device__ __forceinline__ Tile tile_of(const PlanView &p, int64_t t, int64_t b)
 // L2 at about half the rate (2.9 against 4.4 TB/s of X at 4096 x 14336, 64 ranks). The next
 // stage is in registers while this one is used. With 64 rows (NG = 4) a wave owns 16 rows;
 // with 16 (NG = 1) a quarter of each stage, and the waves' sums are added in wave order.
-// KMAJOR weights ([k][r], ranks contiguous) are read back from LDS transposed. XW: bf16 rows
-// on fp16 weights, the weights split exactly into two bf16 parts.
-template <class T, int NG, int RB, bool KMAJOR, bool XW>
+// KMAJOR weights ([k][r], ranks contiguous) are read back from LDS transposed. DX (the frozen
+// layer's input gradient): fp16 weights whatever the rows, split exactly into two bf16 parts
+// for bf16 rows; and the rows' largest |v sw| on the way.
+template <class T, int NG, int RB, bool KMAJOR, bool DX>
 __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
     constexpr int SK = 128, XS = SK * 2 + 16;                         // elements of a stage; padded LDS row of X
     constexpr int WROWS = KMAJOR ? SK : 16 * RB, WCH = KMAJOR ? 2 * RB : SK / 8;  // rows and 16-byte chunks a row of W
@@ -200,6 +201,8 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
         }
     }
     v4i xr[NG], wr[RB];
+    v4f sr[2];
+    uint32_t mx[NG] = {};
     auto load = [&](int64_t st) {
         const int64_t k0 = st * SK;
         const int left = (int)(a.k - k0 < SK ? a.k - k0 : SK);  // elements of this stage
@@ -215,6 +218,11 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
                 wr[j] = load16(wp[j] + (in ? k0 : 0));
             }
         }
+        if constexpr (DX) {
+            const float *s = a.sw + (in ? k0 : 0) + tid % 16 * 8;
+            sr[0] = *reinterpret_cast<const v4f *>(s);
+            sr[1] = *reinterpret_cast<const v4f *>(s + 4);
+        }
         if (!in) {  // past K: re-read elements, against zero rows
 #pragma unroll
             for (int j = 0; j < NG; ++j) xr[j] = v4i{0, 0, 0, 0};
@@ -226,6 +234,16 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
         uint8_t *buf = smem + (st & 1) * BUF;  // last read two stages ago, before the previous barrier
 #pragma unroll
         for (int j = 0; j < NG; ++j) *reinterpret_cast<v4i *>(buf + (j * 16 + tid / 16) * XS + tid % 16 * 16) = xr[j];
+        if constexpr (DX) {  // magnitudes in the order of their bit patterns, NaN above all
+#pragma unroll
+            for (int j = 0; j < NG; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float v = T::to_f32(half_of(xr[j][e / 2], e % 2)) * sr[e / 4][e % 4];
+                    const uint32_t m = __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
+                    mx[j] = mx[j] > m ? mx[j] : m;
+                }
+        }
 #pragma unroll
         for (int j = 0; j < RB; ++j) {
             const int c = j * 256 + tid;
@@ -248,7 +266,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
                 } else {
                     wf = load16(buf + XB + (c * 16 + li) * WS + (e + g * 8) * 2);
                 }
-                if constexpr (XW) {
+                if constexpr (DX && T::kBf16) {
                     v4i hi, lo;
                     split_f16(wf, hi, lo);
                     acc[c] = T::mfma(lo, xf, acc[c]);
@@ -256,6 +274,16 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
                 } else {
                     acc[c] = T::mfma(wf, xf, acc[c]);
                 }
+            }
+        }
+    }
+    if constexpr (DX) {
+        if (rank0 == 0) {
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                const uint32_t m = row16_max(mx[j]);
+                if (tid % 16 == 0 && j * 16 + tid / 16 < t.rows)
+                    a.rowmax[slice * a.b + t.first + j * 16 + tid / 16] = __builtin_bit_cast(float, m);
             }
         }
     }
@@ -298,26 +326,26 @@ int shrink_slices(int64_t b, int64_t k, int64_t r, int64_t tiles) {
     return ks < 1 ? 1 : (int)ks;
 }
 
-template <class T, int NG, bool KMAJOR, bool XW>
+template <class T, int NG, bool KMAJOR, bool DX>
 static hipError_t shrink_ranks(const ShrinkArgs &a, hipStream_t stream) {
     const int rb = a.r <= 16 ? 1 : a.r <= 32 ? 2 : 4;
     const unsigned grid = (unsigned)(a.tiles * ((a.r + 16 * rb - 1) / (16 * rb)) * a.ks);
     if (rb == 1)
-        shrink_kernel<T, NG, 1, KMAJOR, XW><<<grid, 256, 0, stream>>>(a);
+        shrink_kernel<T, NG, 1, KMAJOR, DX><<<grid, 256, 0, stream>>>(a);
     else if (rb == 2)
-        shrink_kernel<T, NG, 2, KMAJOR, XW><<<grid, 256, 0, stream>>>(a);
+        shrink_kernel<T, NG, 2, KMAJOR, DX><<<grid, 256, 0, stream>>>(a);
     else
-        shrink_kernel<T, NG, 4, KMAJOR, XW><<<grid, 256, 0, stream>>>(a);
+        shrink_kernel<T, NG, 4, KMAJOR, DX><<<grid, 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
-template <class T, bool KMAJOR, bool XW>
+template <class T, bool KMAJOR, bool DX>
 static hipError_t shrink_rows(const ShrinkArgs &a, hipStream_t stream) {
-    return a.b <= kFewRows ? shrink_ranks<T, 1, KMAJOR, XW>(a, stream) : shrink_ranks<T, 4, KMAJOR, XW>(a, stream);
+    return a.b <= kFewRows ? shrink_ranks<T, 1, KMAJOR, DX>(a, stream) : shrink_ranks<T, 4, KMAJOR, DX>(a, stream);
 }
 
 hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t stream) {
-    if (a.bf16 && !a.wbf16) return a.kmajor ? shrink_rows<BF16, true, true>(a, stream) : hipErrorInvalidValue;
+    if (a.rowmax) return a.bf16 ? shrink_rows<BF16, true, true>(a, stream) : shrink_rows<F16, true, true>(a, stream);
     if (a.bf16) return a.kmajor ? shrink_rows<BF16, true, false>(a, stream) : shrink_rows<BF16, false, false>(a, stream);
     return a.kmajor ? shrink_rows<F16, true, false>(a, stream) : shrink_rows<F16, false, false>(a, stream);
 }

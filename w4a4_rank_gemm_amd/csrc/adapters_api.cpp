@@ -107,7 +107,7 @@ twq_status twq_adapters(const void *x, const void *at, const void *bt, const flo
     s.b = b;
     s.k = m;
     s.r = (int)r;
-    s.bf16 = s.wbf16 = type == TWQ_BF16;
+    s.bf16 = type == TWQ_BF16;
     s.plan = plan_view(plan, pl);
     s.tiles = pl.max_tiles;
     s.ks = L.ks;
@@ -166,7 +166,7 @@ twq_status twq_adapters_grad(const void *dy, const void *x, const void *qc, cons
     s.b = b;
     s.k = n;
     s.r = (int)r;
-    s.bf16 = s.wbf16 = type == TWQ_BF16;
+    s.bf16 = type == TWQ_BF16;
     s.kmajor = 1;
     s.plan = plan_view(plan, pl);
     s.tiles = pl.max_tiles;
@@ -273,6 +273,8 @@ twq_status twq_linear_dx(const void *dy, const void *qw, const float *sw, const 
         s.tiles = (b + tile_rows(b) - 1) / tile_rows(b);
         s.ks = p.tks;
         s.p = reinterpret_cast<float *>(ws + p.t);
+        s.sw = sw;
+        s.rowmax = reinterpret_cast<float *>(ws + p.rowmax);
         e = launch_shrink(s, st);
         if (e != hipSuccess) return done(e, "twq_linear_dx");
     }
@@ -288,13 +290,16 @@ twq_status twq_linear_dx(const void *dy, const void *qw, const float *sw, const 
     a.bf16 = type == TWQ_BF16;
     a.g = reinterpret_cast<uint16_t *>(ws + p.g);
     a.ge = reinterpret_cast<int32_t *>(ws + p.ge);
+    a.rowmax = reinterpret_cast<float *>(ws + p.rowmax);
+    a.rks = r > 0 ? p.tks : 1;
     a.t = reinterpret_cast<const float *>(ws + p.t);
     a.tks = p.tks;
     a.t16 = reinterpret_cast<uint16_t *>(ws + p.t16);
     a.ks = p.ks;
     a.part = reinterpret_cast<float *>(ws + p.part);
     a.dx = static_cast<uint16_t *>(dx);
-    e = launch_dx_scale(a, p, st);
+    if (r == 0) e = launch_dx_max(a, st);
+    if (e == hipSuccess) e = launch_dx_scale(a, p, st);
     if (e == hipSuccess) e = launch_dx(a, p, st);
     return done(e, "twq_linear_dx");
 }

@@ -11,19 +11,6 @@ namespace twq {
 
 constexpr int kCkRows = 16, kCkGroups = 8;  // a CTA: 16 token rows x 8 groups
 
-// Maximum over the 16 lanes of a row of lanes, in every one of them.
-__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
-    uint32_t t;
-    t = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false);   // quad_perm [1, 0, 3, 2]
-    v = v > t ? v : t;
-    t = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false);   // quad_perm [2, 3, 0, 1]
-    v = v > t ? v : t;
-    t = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false);  // row_half_mirror
-    v = v > t ? v : t;
-    t = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false);  // row_mirror
-    return v > t ? v : t;
-}
-
 // The code by one division (subnormal scales, whose reciprocal may overflow).
 __device__ __forceinline__ int quant_code8_div(float v, float s) {
 #pragma clang fp contract(off)

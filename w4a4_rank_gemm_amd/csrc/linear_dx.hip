@@ -24,76 +24,130 @@ constexpr int kDxStages = 3;
 
 // ---- G and T in fp16 -------------------------------------------------------------------
 
-// One CTA a token row. Eight consecutive channels are stored in the order 0 4 1 5 2 6 3 7,
-// the order in which expanded codes come (dequant8).
+// The largest |dY s_W| of each row (without a low-rank pair; otherwise the shrink kernel finds
+// it while it reads dY). One CTA a row.
 template <class T>
-__global__ __launch_bounds__(256) void dx_scale_kernel(DxArgs a, int64_t npad) {
-    __shared__ float red[8];
-    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+__global__ __launch_bounds__(256) void dx_max_kernel(DxArgs a) {
+    __shared__ uint32_t red[4];
+    const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
-    const uint16_t *src = a.dy + row * a.n;
-    auto row_max = [&](float v, int slot) {  // of the CTA, NaN dropped
-        v = wave_max_f32(v);
-        if (lane == 0) red[slot + wave] = v;
-        __syncthreads();
-        return __builtin_fmaxf(__builtin_fmaxf(red[slot], red[slot + 1]), __builtin_fmaxf(red[slot + 2], red[slot + 3]));
-    };
-    float mx = 0.f;
+    uint32_t mx = 0;
     for (int64_t c = tid * 8; c < a.n; c += 2048) {
-        const v4i v = load16(src + c);
+        const v4i v = load16(a.dy + row * a.n + c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            mx = __builtin_fmaxf(mx, __builtin_fabsf(T::to_f32(half_of(v[e / 2], e % 2)) * a.sw[c + e]));
-    }
-    mx = row_max(mx, 0);
-    int ge = exponent_or_zero(mx);
-    ge = ge < -100 ? -100 : ge;
-    const float gf = pow2(14 - ge);
-    uint16_t *dst = a.g + row * npad;
-    for (int64_t c = tid * 8; c < npad; c += 2048) {
-        v4i o = {0, 0, 0, 0};
-        if (c < a.n) {
-            const v4i v = load16(src + c);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint16_t lo = half_of(v[e / 2], e % 2), hi = half_of(v[(e + 4) / 2], e % 2);
-                const uint16_t f0 = F16::from_f32(T::to_f32(lo) * a.sw[c + e] * gf);
-                const uint16_t f1 = F16::from_f32(T::to_f32(hi) * a.sw[c + e + 4] * gf);
-                o[e] = (int)((uint32_t)f0 | (uint32_t)f1 << 16);
-            }
+        for (int e = 0; e < 8; ++e) {
+            const float f = T::to_f32(half_of(v[e / 2], e % 2)) * a.sw[c + e];
+            const uint32_t m = __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu;
+            mx = mx > m ? mx : m;
         }
-        *reinterpret_cast<v4i *>(dst + c) = o;
     }
-    int te = 0;
-    if (a.r > 0) {
-        const int r32 = (a.r + 31) / 32 * 32;
-        float v = 0.f;  // thread t < r holds T[row][t]
-        if (tid < a.r)
-            for (int s = 0; s < a.tks; ++s) v += a.t[(s * a.b + row) * a.r + tid];
-        const float tm = row_max(__builtin_fabsf(v), 4);
-        te = tm > 0.f ? exponent_or_zero(tm) : ge;
-        // the two exponents meet in one accumulator: far apart, T keeps fewer bits
-        te = te < ge - 40 ? ge - 40 : te;
-        te = te < -100 ? -100 : te;
-        if (tid < r32) {
-            const float s = v * pow2(14 - te);
-            const uint16_t hi = F16::from_f32(s), lo = F16::from_f32(s - F16::to_f32(hi));
-            uint16_t *p = a.t16 + (row * r32 + tid / 8 * 8) * 2 + tid % 8;
+    mx = wave_max_u32(mx);
+    if (tid % kWave == 0) red[tid / kWave] = mx;
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < 4; ++w) mx = mx > red[w] ? mx : red[w];
+        a.rowmax[row] = __builtin_bit_cast(float, mx);
+    }
+}
+
+hipError_t launch_dx_max(const DxArgs &a, hipStream_t stream) {
+    if (a.bf16)
+        dx_max_kernel<BF16><<<(unsigned)a.b, 256, 0, stream>>>(a);
+    else
+        dx_max_kernel<F16><<<(unsigned)a.b, 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+constexpr int kScaleRows = 16, kScaleCols = 2048;
+
+// Exponent of a row of G: from the largest |dY s_W| of its slices.
+__device__ __forceinline__ int g_exponent(const DxArgs &a, int64_t row) {
+    float mx = 0.f;
+    for (int s = 0; s < a.rks; ++s) {
+        const float m = a.rowmax[s * a.b + row];
+        mx = m > mx || m != m ? m : mx;
+    }
+    const int e = exponent_or_zero(mx);
+    return e < -100 ? -100 : e;
+}
+
+// T = dY L2 of 16 rows, 16 threads a row: the slices' sum, its largest magnitude, two fp16 parts.
+__device__ __forceinline__ void t_parts(const DxArgs &a, int64_t row0, int nrows) {
+    const int i = threadIdx.x / 16, q = threadIdx.x % 16, r32 = (a.r + 31) / 32 * 32;
+    const int64_t row = row0 + (i < nrows ? i : 0);
+    float t[16], mx = 0.f;  // ranks q, q + 16, ..
+#pragma unroll
+    for (int u = 0; u < 16; ++u) t[u] = 0.f;
+    for (int s = 0; s < a.tks; ++s) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+            if (u * 16 < a.r) t[u] += a.t[(s * a.b + row) * a.r + u * 16 + q];
+    }
+#pragma unroll
+    for (int u = 0; u < 16; ++u) mx = __builtin_fmaxf(mx, __builtin_fabsf(t[u]));
+    for (int off = 8; off > 0; off >>= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, off, kWave));
+    const int ge = g_exponent(a, row);
+    // the two exponents meet in one accumulator: far apart, T keeps fewer bits
+    int te = mx > 0.f ? exponent_or_zero(mx) : ge;
+    te = te < ge - 40 ? ge - 40 : te;
+    te = te < -100 ? -100 : te;
+    if (i >= nrows) return;
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+        if (u * 16 < r32) {  // r is a multiple of 16: the last half step is zero
+            const float f = t[u] * pow2(14 - te);
+            const uint16_t hi = F16::from_f32(f), lo = F16::from_f32(f - F16::to_f32(hi));
+            const int k = u * 16 + q;
+            uint16_t *p = a.t16 + (row * r32 + k / 8 * 8) * 2 + k % 8;
             p[0] = hi;
             p[8] = lo;
         }
-    }
-    if (tid == 0) {
+    if (q == 0) {
         a.ge[row * 2] = ge - 14;
         a.ge[row * 2 + 1] = te - 14;
     }
 }
 
+// 16 token rows x 2048 channels a CTA, eight channels a thread with their scales in
+// registers; bound by the read of dY and the write of G. Eight consecutive channels are stored
+// in the order 0 4 1 5 2 6 3 7, in which expanded codes come (dequant8). One more CTA per 16
+// rows brings T to fp16 and stores the exponents.
+template <class T>
+__global__ __launch_bounds__(256) void dx_scale_kernel(DxArgs a, int64_t npad) {
+    __shared__ int exps[kScaleRows];
+    const int tid = threadIdx.x;
+    const int64_t row0 = (int64_t)blockIdx.x * kScaleRows;
+    const int nrows = (int)(a.b - row0 < kScaleRows ? a.b - row0 : kScaleRows);
+    if (blockIdx.y + 1 == gridDim.y) return t_parts(a, row0, nrows);
+    const int64_t c = (int64_t)blockIdx.y * kScaleCols + tid * 8;
+    const bool on = c < a.n;
+    v4i v[kScaleRows];
+#pragma unroll
+    for (int i = 0; i < kScaleRows; ++i) v[i] = load16(a.dy + (row0 + (i < nrows ? i : 0)) * a.n + (on ? c : 0));
+    const float *swp = a.sw + (on ? c : 0);
+    const v4f s0 = *reinterpret_cast<const v4f *>(swp), s1 = *reinterpret_cast<const v4f *>(swp + 4);
+    if (tid < kScaleRows) exps[tid] = g_exponent(a, row0 + (tid < nrows ? tid : 0));
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kScaleRows; ++i) {
+        const float gf = pow2(14 - exps[i]);
+        v4i o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint16_t f0 = F16::from_f32(T::to_f32(half_of(v[i][e / 2], e % 2)) * s0[e] * gf);
+            const uint16_t f1 = F16::from_f32(T::to_f32(half_of(v[i][(e + 4) / 2], e % 2)) * s1[e] * gf);
+            o[e] = (int)((uint32_t)f0 | (uint32_t)f1 << 16);
+        }
+        if (i < nrows && c < npad) *reinterpret_cast<v4i *>(a.g + (row0 + i) * npad + c) = on ? o : v4i{0, 0, 0, 0};
+    }
+}
+
 hipError_t launch_dx_scale(const DxArgs &a, const DxPlan &p, hipStream_t stream) {
+    const dim3 grid((unsigned)((a.b + kScaleRows - 1) / kScaleRows), (unsigned)((p.npad + kScaleCols - 1) / kScaleCols + 1));
     if (a.bf16)
-        dx_scale_kernel<BF16><<<(unsigned)a.b, 256, 0, stream>>>(a, p.npad);
+        dx_scale_kernel<BF16><<<grid, 256, 0, stream>>>(a, p.npad);
     else
-        dx_scale_kernel<F16><<<(unsigned)a.b, 256, 0, stream>>>(a, p.npad);
+        dx_scale_kernel<F16><<<grid, 256, 0, stream>>>(a, p.npad);
     return hipGetLastError();
 }
 
@@ -365,7 +419,8 @@ DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
     p.tks = r > 0 ? shrink_slices(b, n, r, (b + tile_rows(b) - 1) / tile_rows(b)) : 0;
     p.g = 0;
     p.ge = up((size_t)b * p.npad * 2);
-    p.t = p.ge + up((size_t)b * 8);
+    p.rowmax = p.ge + up((size_t)b * 8);
+    p.t = p.rowmax + up((size_t)(r > 0 ? p.tks : 1) * b * 4);
     p.t16 = p.t + up((size_t)p.tks * b * r * 4);
     p.part = p.t16 + up((size_t)b * ((r + 31) / 32 * 32) * 4);
     p.total = p.part + (p.ks > 1 ? up((size_t)p.ks * b * m * 4) : 0);

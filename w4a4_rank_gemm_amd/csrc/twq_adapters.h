@@ -84,9 +84,10 @@ struct ShrinkArgs {
     const uint16_t *w;   // per adapter [r][k], or [k][r] (kmajor)
     int64_t b, k;
     int r;
-    int bf16;            // type of v
-    int wbf16;           // type of w
+    int bf16;            // type of v and w (rowmax: w is fp16)
     int kmajor;
+    const float *sw;     // with rowmax: [k]
+    float *rowmax;       // [ks][b]: largest |v sw| of a row over a slice, or NULL (the plain products)
     PlanView plan;       // rows == NULL: one adapter, positions are rows
     int64_t tiles;       // grid bound
     int ks;              // K slices
@@ -163,6 +164,8 @@ struct DxArgs {
     int bf16;            // type of dy and dx
     uint16_t *g;         // [b][npad] fp16: dY s_W 2^-e, permuted along n
     int32_t *ge;         // [b][2] exponents of g and of t16
+    float *rowmax;       // [rks][b] largest |dY s_W| of a row over a slice
+    int rks;
     const float *t;      // [tks][b][r] partial sums of dY L2
     int tks;
     uint16_t *t16;       // [b][r rounded up to 32][2]: dY L2 2^-e in two fp16 parts, 8 hi, 8 lo
@@ -175,9 +178,10 @@ struct DxPlan {
     int ks;          // slices of n
     int64_t npad;    // n rounded up to a K stage
     int tks;         // K slices of dY L2
-    size_t g, ge, t, t16, part, total;
+    size_t g, ge, rowmax, t, t16, part, total;
 };
 DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r);
+hipError_t launch_dx_max(const DxArgs &a, hipStream_t stream);  // r == 0: rowmax, one slice
 hipError_t launch_dx_scale(const DxArgs &a, const DxPlan &p, hipStream_t stream);
 hipError_t launch_dx(const DxArgs &a, const DxPlan &p, hipStream_t stream);
 

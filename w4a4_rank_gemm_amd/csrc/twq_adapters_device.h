@@ -80,4 +80,17 @@ __device__ __forceinline__ int exponent_or_zero(float v) {
     return e == 0 || e == 255 ? 0 : e - 127;
 }
 
+// Maximum over the 16 lanes of a row of lanes, in every one of them.
+__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
+    uint32_t t;
+    t = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false);   // quad_perm [1, 0, 3, 2]
+    v = v > t ? v : t;
+    t = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false);   // quad_perm [2, 3, 0, 1]
+    v = v > t ? v : t;
+    t = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false);  // row_half_mirror
+    v = v > t ? v : t;
+    t = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false);  // row_mirror
+    return v > t ? v : t;
+}
+
 }  // namespace twq
