@@ -13,6 +13,7 @@ GPU is present, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -621,19 +622,44 @@ def _type(t, name: str) -> int:
     return TYPES[t.dtype]
 
 
-def _want(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device):
+def _want(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, index: int):
+    """t is a contiguous GPU tensor of this type and shape on GPU `index`. One comparison in the
+    usual case: these calls are short enough for their checks to be seen."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        return
     _need(t, name, dtype, len(shape))
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    raise ValueError(f"{name} is on {t.device}, not on GPU {index}")
 
 
-def _scratch(dev: torch.device, nbytes: int):
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(index: int, where: str, fn, *args):
+    """fn(*args, stream) on GPU `index`'s current stream, with that GPU current."""
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != TWQ_OK:
+        _check(status, where)
+
+
+@functools.lru_cache(maxsize=4096)
+def _sizes(name: str, *sizes) -> int:
+    return getattr(lib(), name)(*sizes)
+
+
+def _scratch(like: torch.Tensor, nbytes: int):
     """Workspace of one call, from torch's allocator: its memory belongs to the call's place in
     the stream (or to the graph that captures it), so neither other calls nor other captured
     graphs share it."""
-    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
 
 
 def _apart(out: torch.Tensor, name: str, *others):
@@ -655,29 +681,28 @@ def adapter_plan(index: torch.Tensor, count: int) -> AdapterPlan:
     """index int32 [b], each token row's adapter (outside [0, count): none) -> the plan that
     adapters and adapters_grad take; made once for all layers that see the same rows."""
     _need(index, "index", torch.int32, 1)
-    b, dev = index.shape[0], index.device
+    b, gpu = index.shape[0], index.get_device()
     L = lib()
     if not 0 <= count <= 4096:
         raise ValueError(f"count must lie in [0, 4096] (got {count})")
-    data = torch.empty(L.twq_adapter_plan_bytes(b, count), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        _check(L.twq_adapter_plan(_ptr(index), b, count, _ptr(data), data.numel(), _stream(dev)), "twq_adapter_plan")
+    data = torch.empty(L.twq_adapter_plan_bytes(b, count), dtype=torch.uint8, device=index.device)
+    _launch(gpu, "twq_adapter_plan", L.twq_adapter_plan, _addr(index), b, count, _addr(data), data.numel())
     return AdapterPlan(data, b, count)
 
 
-def _adapter_shapes(at, bt, plan: AdapterPlan, scale, b: int, dtype: torch.dtype, dev: torch.device):
+def _adapter_shapes(at, bt, plan: AdapterPlan, scale, b: int, dtype: torch.dtype, gpu: int):
     if not isinstance(plan, AdapterPlan):
         raise TypeError("plan must come from adapter_plan")
-    if plan.b != b or plan.data.device != dev:
-        raise ValueError(f"plan is for {plan.b} rows on {plan.data.device}, not {b} on {dev}")
-    _need(at, "at", dtype, 3)
-    _need(bt, "bt", dtype, 3)
-    count, r, m = at.shape
+    if plan.b != b or plan.data.get_device() != gpu:
+        raise ValueError(f"plan is for {plan.b} rows on {plan.data.device}, not {b} on GPU {gpu}")
+    if at.dim() != 3 or bt.dim() != 3:
+        raise ValueError(f"at and bt must have 3 dims (got {tuple(at.shape)}, {tuple(bt.shape)})")
+    _, r, m = at.shape
     n = bt.shape[1]
-    _want(at, "at", dtype, (plan.count, r, m), dev)
-    _want(bt, "bt", dtype, (count, n, r), dev)
+    _want(at, "at", dtype, (plan.count, r, m), gpu)
+    _want(bt, "bt", dtype, (plan.count, n, r), gpu)
     if scale is not None:
-        _want(scale, "scale", torch.float32, (count,), dev)
+        _want(scale, "scale", torch.float32, (plan.count,), gpu)
     return m, n, r
 
 
@@ -689,25 +714,23 @@ def adapters(x: torch.Tensor, at: torch.Tensor, bt: torch.Tensor, plan: AdapterP
     x [b][m], y [b][n] (None: zeros), at [count][r][m], bt [count][n][r]: all fp16 or all bf16.
     out may be y. keep_h: also returns x at^T, f32 [b][r], which adapters_grad needs."""
     ty = _type(x, "x")
-    _need(x, "x", x.dtype, 2)
-    b, dev = x.shape[0], x.device
-    m, n, r = _adapter_shapes(at, bt, plan, scale, b, x.dtype, dev)
-    _want(x, "x", x.dtype, (b, m), dev)
+    dt, gpu, b = x.dtype, x.get_device(), x.shape[0]
+    m, n, r = _adapter_shapes(at, bt, plan, scale, b, dt, gpu)
+    _want(x, "x", dt, (b, m), gpu)
     if y is not None:
-        _want(y, "y", x.dtype, (b, n), dev)
+        _want(y, "y", dt, (b, n), gpu)
     if out is None:
-        out = torch.empty((b, n), dtype=x.dtype, device=dev)
+        out = x.new_empty((b, n))
     else:
-        _want(out, "out", x.dtype, (b, n), dev)
+        _want(out, "out", dt, (b, n), gpu)
         _apart(out, "out", x, at, bt, scale, None if y is None or y.data_ptr() == out.data_ptr() else y)
-    h = torch.empty((b, r), dtype=torch.float32, device=dev) if keep_h else None
+    h = x.new_empty((b, r), dtype=torch.float32) if keep_h else None
     L = lib()
-    with torch.cuda.device(dev):
-        wsb = L.twq_adapters_workspace_bytes(b, m, n, r, plan.count)
-        ws = _scratch(dev, wsb)
-        _check(L.twq_adapters(_ptr(x), _ptr(at), _ptr(bt), _ptr(scale), _ptr(plan.data), plan.data.numel(), _ptr(y),
-                              _ptr(out), _ptr(h), b, m, n, r, plan.count, ty, _ptr(ws), wsb, _stream(dev)),
-               "twq_adapters")
+    wsb = _sizes("twq_adapters_workspace_bytes", b, m, n, r, plan.count)
+    ws = _scratch(x, wsb)
+    _launch(gpu, "twq_adapters", L.twq_adapters, x.data_ptr(), at.data_ptr(), bt.data_ptr(), _addr(scale),
+            plan.data.data_ptr(), plan.data.numel(), _addr(y), out.data_ptr(), _addr(h), b, m, n, r, plan.count, ty,
+            _addr(ws), wsb)
     return (out, h) if keep_h else out
 
 
@@ -719,34 +742,32 @@ def adapters_grad(dy: torch.Tensor, x, h: torch.Tensor, at: torch.Tensor, bt: to
     adapters(keep_h=True). dX = dx + the adapters' share (dx None: zeros), written to out if
     given (out may be dx). Adapters without rows get zero gradients."""
     ty = _type(dy, "dy")
-    _need(dy, "dy", dy.dtype, 2)
-    b, dev, dt = dy.shape[0], dy.device, dy.dtype
-    m, n, r = _adapter_shapes(at, bt, plan, scale, b, dt, dev)
-    _want(dy, "dy", dt, (b, n), dev)
-    _want(h, "h", torch.float32, (b, r), dev)
+    dt, gpu, b = dy.dtype, dy.get_device(), dy.shape[0]
+    m, n, r = _adapter_shapes(at, bt, plan, scale, b, dt, gpu)
+    _want(dy, "dy", dt, (b, n), gpu)
+    _want(h, "h", torch.float32, (b, r), gpu)
     qc = sc = None
     if isinstance(x, tuple):
         qc, sc = x
         x = None
-        _want(qc, "qc", torch.int8, (b, m), dev)
-        _want(sc, "sc", torch.float32, (m // GROUP, b), dev)
+        _want(qc, "qc", torch.int8, (b, m), gpu)
+        _want(sc, "sc", torch.float32, (m // GROUP, b), gpu)
     else:
-        _want(x, "x", dt, (b, m), dev)
+        _want(x, "x", dt, (b, m), gpu)
     if dx is not None:
-        _want(dx, "dx", dt, (b, m), dev)
+        _want(dx, "dx", dt, (b, m), gpu)
     if out is None:
-        out = torch.empty((b, m), dtype=dt, device=dev)
+        out = dy.new_empty((b, m))
     else:
-        _want(out, "out", dt, (b, m), dev)
+        _want(out, "out", dt, (b, m), gpu)
         _apart(out, "out", dy, x, qc, sc, h, at, bt, scale, None if dx is None or dx.data_ptr() == out.data_ptr() else dx)
     dat, dbt = torch.empty_like(at), torch.empty_like(bt)
     L = lib()
-    with torch.cuda.device(dev):
-        wsb = L.twq_adapters_grad_workspace_bytes(b, m, n, r, plan.count)
-        ws = _scratch(dev, wsb)
-        _check(L.twq_adapters_grad(_ptr(dy), _ptr(x), _ptr(qc), _ptr(sc), _ptr(h), _ptr(at), _ptr(bt), _ptr(scale),
-                                   _ptr(plan.data), plan.data.numel(), _ptr(dx), _ptr(out), _ptr(dat), _ptr(dbt), b, m, n,
-                                   r, plan.count, ty, _ptr(ws), wsb, _stream(dev)), "twq_adapters_grad")
+    wsb = _sizes("twq_adapters_grad_workspace_bytes", b, m, n, r, plan.count)
+    ws = _scratch(dy, wsb)
+    _launch(gpu, "twq_adapters_grad", L.twq_adapters_grad, dy.data_ptr(), _addr(x), _addr(qc), _addr(sc), h.data_ptr(),
+            at.data_ptr(), bt.data_ptr(), _addr(scale), plan.data.data_ptr(), plan.data.numel(), _addr(dx), out.data_ptr(),
+            dat.data_ptr(), dbt.data_ptr(), b, m, n, r, plan.count, ty, _addr(ws), wsb)
     return dat, dbt, out
 
 
@@ -755,11 +776,11 @@ def checkpoint_act(x: torch.Tensor):
     8 bits, one scale per token and 128 elements."""
     ty = _type(x, "x")
     _need(x, "x", x.dtype, 2)
-    (b, m), dev = x.shape, x.device
-    qc = torch.empty((b, m), dtype=torch.int8, device=dev)
-    sc = torch.empty((m // GROUP, b), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().twq_checkpoint_act(_ptr(x), b, m, ty, _ptr(qc), _ptr(sc), _stream(dev)), "twq_checkpoint_act")
+    b, m = x.shape
+    qc = x.new_empty((b, m), dtype=torch.int8)
+    sc = x.new_empty((m // GROUP, b), dtype=torch.float32)
+    _launch(x.get_device(), "twq_checkpoint_act", lib().twq_checkpoint_act, x.data_ptr(), b, m, ty, qc.data_ptr(),
+            sc.data_ptr())
     return qc, sc
 
 
@@ -767,15 +788,15 @@ def restore_act(qc: torch.Tensor, sc: torch.Tensor, dtype: torch.dtype = torch.f
                 out: torch.Tensor | None = None) -> torch.Tensor:
     """The activations of checkpoint_act again, codes times scales, in fp16 or bf16."""
     _need(qc, "qc", torch.int8, 2)
-    (b, m), dev = qc.shape, qc.device
-    _want(sc, "sc", torch.float32, (m // GROUP, b), dev)
+    (b, m), gpu = qc.shape, qc.get_device()
+    _want(sc, "sc", torch.float32, (m // GROUP, b), gpu)
     if out is None:
-        out = torch.empty((b, m), dtype=dtype, device=dev)
-    ty = _type(out, "out")
-    _want(out, "out", dtype, (b, m), dev)
-    _apart(out, "out", qc, sc)
-    with torch.cuda.device(dev):
-        _check(lib().twq_restore_act(_ptr(qc), _ptr(sc), b, m, ty, _ptr(out), _stream(dev)), "twq_restore_act")
+        out = qc.new_empty((b, m), dtype=dtype)
+    else:
+        _want(out, "out", dtype, (b, m), gpu)
+        _apart(out, "out", qc, sc)
+    _launch(gpu, "twq_restore_act", lib().twq_restore_act, qc.data_ptr(), sc.data_ptr(), b, m, _type(out, "out"),
+            out.data_ptr())
     return out
 
 
@@ -784,30 +805,28 @@ def linear_dx(dy: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor, l1t=None, l2
     """The layer's input gradient: dX [b][m] = dY (s_W Q_W)^T + (dY L2^T) L1^T, with the packed
     weight of pack_weight and the low-rank pair of linear; dY and dX fp16 or bf16."""
     ty = _type(dy, "dy")
-    _need(dy, "dy", dy.dtype, 2)
     _need(qw, "qw", torch.uint8, 2)
-    b, dev, dt = dy.shape[0], dy.device, dy.dtype
+    b, gpu, dt = dy.shape[0], dy.get_device(), dy.dtype
     n, m = qw.shape[0], 2 * qw.shape[1]
-    _want(dy, "dy", dt, (b, n), dev)
-    _want(qw, "qw", torch.uint8, (n, m // 2), dev)
-    _want(sw, "sw", torch.float32, (n,), dev)
+    _want(dy, "dy", dt, (b, n), gpu)
+    _want(qw, "qw", torch.uint8, (n, m // 2), gpu)
+    _want(sw, "sw", torch.float32, (n,), gpu)
     r = 0
     if l1t is not None or l2t is not None:
         _need(l1t, "l1t", torch.float16, 2)
         r = l1t.shape[0]
-        _want(l1t, "l1t", torch.float16, (r, m), dev)
-        _want(l2t, "l2t", torch.float16, (n, r), dev)
+        _want(l1t, "l1t", torch.float16, (r, m), gpu)
+        _want(l2t, "l2t", torch.float16, (n, r), gpu)
     if out is None:
-        out = torch.empty((b, m), dtype=dt, device=dev)
+        out = dy.new_empty((b, m))
     else:
-        _want(out, "out", dt, (b, m), dev)
+        _want(out, "out", dt, (b, m), gpu)
         _apart(out, "out", dy, qw, sw, l1t, l2t)
     L = lib()
-    with torch.cuda.device(dev):
-        wsb = L.twq_linear_dx_workspace_bytes(b, m, n, r)
-        ws = _scratch(dev, wsb)
-        _check(L.twq_linear_dx(_ptr(dy), _ptr(qw), _ptr(sw), _ptr(l1t), _ptr(l2t), r, _ptr(out), b, m, n, ty, _ptr(ws),
-                               wsb, _stream(dev)), "twq_linear_dx")
+    wsb = _sizes("twq_linear_dx_workspace_bytes", b, m, n, r)
+    ws = _scratch(dy, wsb)
+    _launch(gpu, "twq_linear_dx", L.twq_linear_dx, dy.data_ptr(), qw.data_ptr(), sw.data_ptr(), _addr(l1t), _addr(l2t), r,
+            out.data_ptr(), b, m, n, ty, _addr(ws), wsb)
     return out
 
 
