@@ -405,7 +405,8 @@ __global__ __launch_bounds__(256) void dx_join_kernel(const float *part, int ks,
 }
 
 // Token rows a CTA: as many as the batch fills, up to 128. Channel slices: with fewer CTAs
-// than two a compute unit, at least four stages each and at most 16.
+// than two a compute unit, at least four stages each and at most 16; below 16 stages in all
+// the joining launch costs more than the slices save.
 DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     DxPlan p{};
@@ -413,7 +414,7 @@ DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
     p.npad = (n + kDxK - 1) / kDxK * kDxK;
     const int64_t ctas = (b + p.bt - 1) / p.bt * ((m + kDxM - 1) / kDxM), stages = p.npad / kDxK;
     int64_t ks = ctas >= 512 ? 1 : 512 / ctas;
-    if (ks > stages / 4) ks = stages / 4;
+    if (ks > stages / 4) ks = stages < 16 ? 1 : stages / 4;
     if (ks > 16) ks = 16;
     p.ks = ks < 1 ? 1 : (int)ks;
     p.tks = r > 0 ? shrink_slices(b, n, r, (b + tile_rows(b) - 1) / tile_rows(b)) : 0;
