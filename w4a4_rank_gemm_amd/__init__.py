@@ -619,6 +619,8 @@ def _type(t, name: str) -> int:
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in TYPES:
         raise TypeError(f"{name} must be torch.float16 or torch.bfloat16 (got {t.dtype})")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU (got {t.device})")
     return TYPES[t.dtype]
 
 
@@ -747,7 +749,7 @@ def adapters_grad(dy: torch.Tensor, x, h: torch.Tensor, at: torch.Tensor, bt: to
     _want(dy, "dy", dt, (b, n), gpu)
     _want(h, "h", torch.float32, (b, r), gpu)
     qc = sc = None
-    if isinstance(x, tuple):
+    if isinstance(x, (tuple, list)):
         qc, sc = x
         x = None
         _want(qc, "qc", torch.int8, (b, m), gpu)
@@ -842,3 +844,13 @@ class DualLinear:
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
         return linear(x, self.qw, self.sw, self.l1t if self.r else None, self.l2t if self.r else None, out=out)
+
+    def adapted(self, x: torch.Tensor, at: torch.Tensor, bt: torch.Tensor, plan: AdapterPlan,
+                scale: torch.Tensor | None = None, out: torch.Tensor | None = None, keep_h: bool = False):
+        """The layer with each token row's adapter on top (adapters, in place on the layer's output)."""
+        y = self(x, out=out)
+        return adapters(x, at, bt, plan, y, scale, out=y, keep_h=keep_h)
+
+    def grad_input(self, dy: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+        """The frozen layer's input gradient (linear_dx)."""
+        return linear_dx(dy, self.qw, self.sw, self.l1t if self.r else None, self.l2t if self.r else None, out=out)

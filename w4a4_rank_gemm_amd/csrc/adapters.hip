@@ -189,7 +189,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
     const uint16_t *xp[NG], *wp[RB];
     const uint16_t *w = a.w + (int64_t)t.adapter * a.r * a.k;
 #pragma unroll
-    for (int j = 0; j < NG; ++j) xp[j] = a.v + at[j] * a.k + tid % 16 * 8;
+    for (int j = 0; j < NG; ++j) xp[j] = a.v + at[j] * a.k;
 #pragma unroll
     for (int j = 0; j < RB; ++j) {
         if constexpr (KMAJOR) {
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
             wp[j] = w + (rr < a.r ? rr : a.r - 8);
         } else {
             const int rr = rank0 + j * 16 + tid / 16;
-            wp[j] = w + (int64_t)(rr < a.r ? rr : a.r - 1) * a.k + tid % 16 * 8;
+            wp[j] = w + (int64_t)(rr < a.r ? rr : a.r - 1) * a.k;
         }
     }
     v4i xr[NG], wr[RB];
@@ -207,19 +207,20 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
         const int64_t k0 = st * SK;
         const int left = (int)(a.k - k0 < SK ? a.k - k0 : SK);  // elements of this stage
         const bool in = tid % 16 * 8 < left;
+        const int64_t kx = in ? k0 + tid % 16 * 8 : 0;  // K may be shorter than a stage
 #pragma unroll
-        for (int j = 0; j < NG; ++j) xr[j] = load16(xp[j] + (in ? k0 : 0));
+        for (int j = 0; j < NG; ++j) xr[j] = load16(xp[j] + kx);
 #pragma unroll
         for (int j = 0; j < RB; ++j) {
             if constexpr (KMAJOR) {
                 const int kk = (j * 256 + tid) / WCH;
                 wr[j] = load16(wp[j] + (k0 + (kk < left ? kk : 0)) * a.r);
             } else {
-                wr[j] = load16(wp[j] + (in ? k0 : 0));
+                wr[j] = load16(wp[j] + kx);
             }
         }
         if constexpr (DX) {
-            const float *s = a.sw + (in ? k0 : 0) + tid % 16 * 8;
+            const float *s = a.sw + kx;
             sr[0] = *reinterpret_cast<const v4f *>(s);
             sr[1] = *reinterpret_cast<const v4f *>(s + 4);
         }
@@ -313,17 +314,6 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
             if (i < t.rows && rank < a.r) *reinterpret_cast<v4f *>(a.p + ((slice * a.b + t.first + i) * a.r + rank)) = s;
         }
     }
-}
-
-// K slices: enough CTAs to fill the 256 compute units twice, at least two stages of 128
-// each, at most 16 (the partial sums are read again).
-int shrink_slices(int64_t b, int64_t k, int64_t r, int64_t tiles) {
-    (void)b;
-    const int64_t rt = r <= 16 ? 1 : r <= 32 ? 1 : (r + 63) / 64, steps = (k + 127) / 128;
-    int64_t ks = 512 / (tiles * rt);
-    if (ks > steps / 2) ks = steps / 2;
-    if (ks > 16) ks = 16;
-    return ks < 1 ? 1 : (int)ks;
 }
 
 template <class T, int NG, bool KMAJOR, bool DX>

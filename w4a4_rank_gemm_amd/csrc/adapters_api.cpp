@@ -13,12 +13,13 @@ namespace {
 
 using namespace twq;
 
-constexpr int64_t kMaxAdapterN = int64_t(1) << 22;  // 32-bit tile offsets and grid sizes
+constexpr int64_t kMaxAdapterN = int64_t(1) << 22;  // 32-bit offsets inside a tile
+constexpr int64_t kMaxOutput = int64_t(1) << 40;    // elements of Y: grid sizes below 2^31
 
 bool valid_type(int t) { return t == TWQ_F16 || t == TWQ_BF16; }
 bool valid_count(int64_t c) { return c >= 0 && c <= kMaxAdapters; }
 bool valid_shape(int64_t b, int64_t m, int64_t n, int64_t r) {
-    return valid_b(b) && valid_m(m) && n > 0 && n % 16 == 0 && n <= kMaxAdapterN && valid_r(r);
+    return valid_b(b) && valid_m(m) && n > 0 && n % 16 == 0 && n <= kMaxAdapterN && b * n <= kMaxOutput && valid_r(r);
 }
 
 twq_status done(hipError_t e, const char *name) { return e == hipSuccess ? TWQ_OK : (twq_status)hip_error(e, name); }
@@ -37,7 +38,7 @@ struct GradLayout {
 
 ForwardLayout forward_layout(int64_t b, int64_t k, int64_t r, int64_t count) {
     ForwardLayout L{};
-    L.ks = shrink_slices(b, k, r, plan_layout(b, count).max_tiles);
+    L.ks = shrink_slices(k, r, plan_layout(b, count).max_tiles);
     L.p = 0;
     L.parts = align256((size_t)L.ks * b * r * 4);
     L.total = L.parts + align256(expand_parts_bytes(b, r));
@@ -53,7 +54,7 @@ void set_parts(ExpandArgs &a, uint8_t *at) {
 GradLayout grad_layout(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count) {
     const PlanLayout pl = plan_layout(b, count);
     GradLayout L{};
-    L.ks = b > 0 ? shrink_slices(b, n, r, pl.max_tiles) : 1;
+    L.ks = b > 0 ? shrink_slices(n, r, pl.max_tiles) : 1;
     L.p = 0;
     L.parts = align256((size_t)L.ks * b * r * 4);
     L.g = L.parts + align256(expand_parts_bytes(b, r));

@@ -270,19 +270,21 @@ __global__ __launch_bounds__(256) void outer_join_kernel(OuterArgs a) {
 
 template <class T, bool CODES>
 static hipError_t outer_ranks(const OuterArgs &a, hipStream_t stream) {
-    const int rb = a.r <= 16 ? 1 : a.r <= 32 ? 2 : a.r <= 64 ? 4 : 8;
-    const dim3 grid((unsigned)(a.chunks * (a.m / kCols + (a.n + kCols - 1) / kCols)),
-                    (unsigned)((a.r + 16 * rb - 1) / (16 * rb)));
-    if (rb == 1)
-        outer_kernel<T, 1, CODES><<<grid, 256, 0, stream>>>(a);
-    else if (rb == 2)
-        outer_kernel<T, 2, CODES><<<grid, 256, 0, stream>>>(a);
-    else if (rb == 4)
-        outer_kernel<T, 4, CODES><<<grid, 256, 0, stream>>>(a);
-    else
-        outer_kernel<T, 8, CODES><<<grid, 256, 0, stream>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (a.chunks > 0) {
+        const int rb = a.r <= 16 ? 1 : a.r <= 32 ? 2 : a.r <= 64 ? 4 : 8;
+        const dim3 grid((unsigned)(a.chunks * (a.m / kCols + (a.n + kCols - 1) / kCols)),
+                        (unsigned)((a.r + 16 * rb - 1) / (16 * rb)));
+        if (rb == 1)
+            outer_kernel<T, 1, CODES><<<grid, 256, 0, stream>>>(a);
+        else if (rb == 2)
+            outer_kernel<T, 2, CODES><<<grid, 256, 0, stream>>>(a);
+        else if (rb == 4)
+            outer_kernel<T, 4, CODES><<<grid, 256, 0, stream>>>(a);
+        else
+            outer_kernel<T, 8, CODES><<<grid, 256, 0, stream>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     const int64_t per4 = (int64_t)a.r * (a.m + a.n) / 4;
     outer_join_kernel<T><<<dim3((unsigned)((per4 + 255) / 256), (unsigned)a.count), 256, 0, stream>>>(a);
     return hipGetLastError();

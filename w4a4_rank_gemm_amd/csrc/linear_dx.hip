@@ -18,8 +18,6 @@
 
 namespace twq {
 
-constexpr int kDxM = 256;      // input columns of a CTA: 64 a wave
-constexpr int kDxK = 64;       // output channels of a stage: four panels
 constexpr int kDxStages = 3;
 
 // ---- G and T in fp16 -------------------------------------------------------------------
@@ -402,30 +400,6 @@ __global__ __launch_bounds__(256) void dx_join_kernel(const float *part, int ks,
     }
     *reinterpret_cast<uint2 *>(dx + at) = make_uint2((uint32_t)T::from_f32(s[0]) | (uint32_t)T::from_f32(s[1]) << 16,
                                                      (uint32_t)T::from_f32(s[2]) | (uint32_t)T::from_f32(s[3]) << 16);
-}
-
-// Token rows a CTA: as many as the batch fills, up to 128. Channel slices: with fewer CTAs
-// than two a compute unit, at least four stages each and at most 16; below 16 stages in all
-// the joining launch costs more than the slices save.
-DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
-    auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
-    DxPlan p{};
-    p.bt = b <= 32 ? 32 : b <= 64 ? 64 : 128;
-    p.npad = (n + kDxK - 1) / kDxK * kDxK;
-    const int64_t ctas = (b + p.bt - 1) / p.bt * ((m + kDxM - 1) / kDxM), stages = p.npad / kDxK;
-    int64_t ks = ctas >= 512 ? 1 : 512 / ctas;
-    if (ks > stages / 4) ks = stages < 16 ? 1 : stages / 4;
-    if (ks > 16) ks = 16;
-    p.ks = ks < 1 ? 1 : (int)ks;
-    p.tks = r > 0 ? shrink_slices(b, n, r, (b + tile_rows(b) - 1) / tile_rows(b)) : 0;
-    p.g = 0;
-    p.ge = up((size_t)b * p.npad * 2);
-    p.rowmax = p.ge + up((size_t)b * 8);
-    p.t = p.rowmax + up((size_t)(r > 0 ? p.tks : 1) * b * 4);
-    p.t16 = p.t + up((size_t)p.tks * b * r * 4);
-    p.part = p.t16 + up((size_t)b * ((r + 31) / 32 * 32) * 4);
-    p.total = p.part + (p.ks > 1 ? up((size_t)p.ks * b * m * 4) : 0);
-    return p;
 }
 
 template <class T>

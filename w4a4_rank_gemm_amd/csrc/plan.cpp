@@ -5,6 +5,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "twq_adapters.h"
 #include "twq_kernels.h"
 
 namespace twq {
@@ -96,6 +97,42 @@ FoldLayout fold_layout(int64_t m, int64_t n, int64_t r) {
     L.ginv = L.aug + al((size_t)(2 * r * r) * 8);
     L.total = L.ginv + al((size_t)(r * r) * 8);
     return L;
+}
+
+// ---- adapters and the input gradient ----
+
+// K slices: enough CTAs to fill the 256 compute units twice, at least two stages of 128
+// each, at most 16 (the partial sums are read again).
+int shrink_slices(int64_t k, int64_t r, int64_t tiles) {
+    const int64_t rt = r <= 32 ? 1 : (r + 63) / 64, steps = (k + 127) / 128;
+    int64_t ks = 512 / (tiles * rt);
+    if (ks > steps / 2) ks = steps / 2;
+    if (ks > 16) ks = 16;
+    return ks < 1 ? 1 : (int)ks;
+}
+
+// Token rows a CTA: as many as the batch fills, up to 128. Channel slices: with fewer CTAs
+// than two a compute unit, at least four stages each and at most 16; below 16 stages in all
+// the joining launch costs more than the slices save.
+DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
+    auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+    DxPlan p{};
+    p.bt = b <= 32 ? 32 : b <= 64 ? 64 : 128;
+    p.npad = (n + kDxK - 1) / kDxK * kDxK;
+    const int64_t ctas = (b + p.bt - 1) / p.bt * ((m + kDxM - 1) / kDxM), stages = p.npad / kDxK;
+    int64_t ks = ctas >= 512 ? 1 : 512 / ctas;
+    if (ks > stages / 4) ks = stages < 16 ? 1 : stages / 4;
+    if (ks > 16) ks = 16;
+    p.ks = ks < 1 ? 1 : (int)ks;
+    p.tks = r > 0 ? shrink_slices(n, r, (b + tile_rows(b) - 1) / tile_rows(b)) : 0;
+    p.g = 0;
+    p.ge = up((size_t)b * p.npad * 2);
+    p.rowmax = p.ge + up((size_t)b * 8);
+    p.t = p.rowmax + up((size_t)(r > 0 ? p.tks : 1) * b * 4);
+    p.t16 = p.t + up((size_t)p.tks * b * r * 4);
+    p.part = p.t16 + up((size_t)b * ((r + 31) / 32 * 32) * 4);
+    p.total = p.part + (p.ks > 1 ? up((size_t)p.ks * b * m * 4) : 0);
+    return p;
 }
 
 }  // namespace twq

@@ -93,7 +93,7 @@ struct ShrinkArgs {
     int ks;              // K slices
     float *p;            // [ks][b][r]
 };
-int shrink_slices(int64_t b, int64_t k, int64_t r, int64_t tiles);
+int shrink_slices(int64_t k, int64_t r, int64_t tiles);  // plan.cpp
 hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t stream);
 
 // ---- second product: out[row] = base[row] + c (sum_s P[s][pos]) W ---------------------
@@ -173,6 +173,9 @@ struct DxArgs {
     float *part;         // [ks][b][m] fp32 when ks > 1
     uint16_t *dx;        // [b][m]
 };
+constexpr int kDxM = 256;  // input columns of a CTA: 64 a wave
+constexpr int kDxK = 64;   // output channels of a stage: four panels
+
 struct DxPlan {
     int bt;          // token rows a CTA
     int ks;          // slices of n
@@ -180,7 +183,7 @@ struct DxPlan {
     int tks;         // K slices of dY L2
     size_t g, ge, rowmax, t, t16, part, total;
 };
-DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r);
+DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r);  // plan.cpp
 hipError_t launch_dx_max(const DxArgs &a, hipStream_t stream);  // r == 0: rowmax, one slice
 hipError_t launch_dx_scale(const DxArgs &a, const DxPlan &p, hipStream_t stream);
 hipError_t launch_dx(const DxArgs &a, const DxPlan &p, hipStream_t stream);
