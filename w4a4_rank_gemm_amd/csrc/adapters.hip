@@ -161,59 +161,60 @@ __device__ __forceinline__ Tile tile_of(const PlanView &p, int64_t t, int64_t b)
 // layer's input gradient): fp16 weights whatever the rows, split exactly into two bf16 parts
 // for bf16 rows; and the rows' largest |v sw| on the way.
 template <class T, int NG, int RB, bool KMAJOR, bool DX>
-__global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
+__global__ __launch_bounds__(NG == 8 ? 512 : 256) void shrink_kernel(ShrinkArgs a) {
+    constexpr int NT = NG == 8 ? 512 : 256, XN = 256 * NG / NT, WN = (256 * RB + NT - 1) / NT;  // threads; chunks a thread
     constexpr int SK = 128, XS = SK * 2 + 16;                         // elements of a stage; padded LDS row of X
     constexpr int WROWS = KMAJOR ? SK : 16 * RB, WCH = KMAJOR ? 2 * RB : SK / 8;  // rows and 16-byte chunks a row of W
     constexpr int WS = WCH * 16 + 16;
     constexpr int XB = 16 * NG * XS, BUF = XB + WROWS * WS;
     constexpr int RED = NG == 1 ? 4 * RB * kWave * 16 : 0;
     __shared__ __align__(16) uint8_t smem[2 * BUF > RED ? 2 * BUF : RED];
-    const int64_t id = xcd_order(blockIdx.x, gridDim.x);  // tiles of one slice, and so of one adapter's weights, on one XCD
-    const Tile t = tile_of<16 * NG>(a.plan, id % a.tiles, a.b);
+    // Tiles of one slice, and so of one adapter's weights, on one XCD. With many rows the plan's
+    // own number of tiles is dealt out, not the grid's bound on it, so that no XCD gets only
+    // empty ones; with few that would be one more load to wait for.
+    const int rtiles = (a.r + 16 * RB - 1) / (16 * RB);
+    const int64_t tiles = NG > 1 && a.plan.rows ? a.plan.head[0] : a.tiles, ctas = tiles * rtiles * a.ks;
+    if (blockIdx.x >= ctas) return;
+    const int64_t id = xcd_order(blockIdx.x, ctas);
+    const Tile t = tile_of<16 * NG>(a.plan, id % tiles, a.b);
     if (t.rows == 0 || t.adapter < 0) return;
     const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave, li = lane & 15, g = lane >> 4;
-    const int rtiles = (a.r + 16 * RB - 1) / (16 * RB);
-    const int rank0 = (int)(id / a.tiles % rtiles) * 16 * RB;
-    const int64_t slice = id / a.tiles / rtiles, nst = (a.k + SK - 1) / SK;
+    const int rank0 = (int)(id / tiles % rtiles) * 16 * RB;
+    const int64_t slice = id / tiles / rtiles, nst = (a.k + SK - 1) / SK;
     const int64_t s0 = slice * nst / a.ks, s1 = (slice + 1) * nst / a.ks;
 
-    // chunk j of this thread: row 16 j + tid / 16, elements 8 (tid % 16) of a stage
-    int64_t at[NG];
+    // chunk j of this thread: row (NT j + tid) / 16, elements 8 (tid % 16) of a stage
+    int64_t at[XN];
     if (t.row) {
 #pragma unroll
-        for (int j = 0; j < NG; ++j) at[j] = t.row[j * 16 + tid / 16];
+        for (int j = 0; j < XN; ++j) at[j] = t.row[(j * NT + tid) / 16];
     } else {
 #pragma unroll
-        for (int j = 0; j < NG; ++j) at[j] = t.token(j * 16 + tid / 16);
+        for (int j = 0; j < XN; ++j) at[j] = t.token((j * NT + tid) / 16);
     }
-    const uint16_t *xp[NG], *wp[RB];
+    const uint16_t *xp[XN], *wp[WN];
     const uint16_t *w = a.w + (int64_t)t.adapter * a.r * a.k;
 #pragma unroll
-    for (int j = 0; j < NG; ++j) xp[j] = a.v + at[j] * a.k;
+    for (int j = 0; j < XN; ++j) xp[j] = a.v + at[j] * a.k;
 #pragma unroll
-    for (int j = 0; j < RB; ++j) {
-        if constexpr (KMAJOR) {
-            const int rr = rank0 + (j * 256 + tid) % WCH * 8;
-            wp[j] = w + (rr < a.r ? rr : a.r - 8);
-        } else {
-            const int rr = rank0 + j * 16 + tid / 16;
-            wp[j] = w + (int64_t)(rr < a.r ? rr : a.r - 1) * a.k;
-        }
+    for (int j = 0; j < WN; ++j) {
+        const int c = (j * NT + tid) % (256 * RB);
+        const int rr = rank0 + (KMAJOR ? c % WCH * 8 : c / WCH);
+        wp[j] = w + (KMAJOR ? (rr < a.r ? rr : a.r - 8) : (int64_t)(rr < a.r ? rr : a.r - 1) * a.k);
     }
-    v4i xr[NG], wr[RB];
+    v4i xr[XN], wr[WN];
     v4f sr[2];
-    uint32_t mx[NG] = {};
+    uint32_t mx[XN] = {};
     auto load = [&](int64_t st) {
         const int64_t k0 = st * SK;
         const int left = (int)(a.k - k0 < SK ? a.k - k0 : SK);  // elements of this stage
-        const bool in = tid % 16 * 8 < left;
-        const int64_t kx = in ? k0 + tid % 16 * 8 : 0;  // K may be shorter than a stage
+        const int64_t kx = tid % 16 * 8 < left ? k0 + tid % 16 * 8 : 0;  // past K: re-read, cleared when stored
 #pragma unroll
-        for (int j = 0; j < NG; ++j) xr[j] = load16(xp[j] + kx);
+        for (int j = 0; j < XN; ++j) xr[j] = load16(xp[j] + kx);
 #pragma unroll
-        for (int j = 0; j < RB; ++j) {
+        for (int j = 0; j < WN; ++j) {
             if constexpr (KMAJOR) {
-                const int kk = (j * 256 + tid) / WCH;
+                const int kk = (j * NT + tid) % (256 * RB) / WCH;
                 wr[j] = load16(wp[j] + (k0 + (kk < left ? kk : 0)) * a.r);
             } else {
                 wr[j] = load16(wp[j] + kx);
@@ -224,20 +225,20 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
             sr[0] = *reinterpret_cast<const v4f *>(s);
             sr[1] = *reinterpret_cast<const v4f *>(s + 4);
         }
-        if (!in) {  // past K: re-read elements, against zero rows
-#pragma unroll
-            for (int j = 0; j < NG; ++j) xr[j] = v4i{0, 0, 0, 0};
-        }
     };
     v4f acc[RB] = {};
     if (s0 < s1) load(s0);
     for (int64_t st = s0; st < s1; ++st) {
         uint8_t *buf = smem + (st & 1) * BUF;  // last read two stages ago, before the previous barrier
+        if (KMAJOR && st * SK + tid % 16 * 8 >= a.k) {
 #pragma unroll
-        for (int j = 0; j < NG; ++j) *reinterpret_cast<v4i *>(buf + (j * 16 + tid / 16) * XS + tid % 16 * 16) = xr[j];
+            for (int j = 0; j < XN; ++j) xr[j] = v4i{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int j = 0; j < XN; ++j) *reinterpret_cast<v4i *>(buf + (j * NT + tid) / 16 * XS + tid % 16 * 16) = xr[j];
         if constexpr (DX) {  // magnitudes in the order of their bit patterns, NaN above all
 #pragma unroll
-            for (int j = 0; j < NG; ++j)
+            for (int j = 0; j < XN; ++j)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float v = T::to_f32(half_of(xr[j][e / 2], e % 2)) * sr[e / 4][e % 4];
@@ -246,9 +247,9 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
                 }
         }
 #pragma unroll
-        for (int j = 0; j < RB; ++j) {
-            const int c = j * 256 + tid;
-            *reinterpret_cast<v4i *>(buf + XB + c / WCH * WS + c % WCH * 16) = wr[j];
+        for (int j = 0; j < WN; ++j) {
+            const int c = j * NT + tid;
+            if (256 * RB % NT == 0 || c < 256 * RB) *reinterpret_cast<v4i *>(buf + XB + c / WCH * WS + c % WCH * 16) = wr[j];
         }
         if (st + 1 < s1) load(st + 1);
         __syncthreads();
@@ -281,10 +282,10 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
     if constexpr (DX) {
         if (rank0 == 0) {
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
+            for (int j = 0; j < XN; ++j) {
                 const uint32_t m = row16_max(mx[j]);
-                if (tid % 16 == 0 && j * 16 + tid / 16 < t.rows)
-                    a.rowmax[slice * a.b + t.first + j * 16 + tid / 16] = __builtin_bit_cast(float, m);
+                const int i = (j * NT + tid) / 16;
+                if (tid % 16 == 0 && i < t.rows) a.rowmax[slice * a.b + t.first + i] = __builtin_bit_cast(float, m);
             }
         }
     }
@@ -318,20 +319,24 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
 
 template <class T, int NG, bool KMAJOR, bool DX>
 static hipError_t shrink_ranks(const ShrinkArgs &a, hipStream_t stream) {
-    const int rb = a.r <= 16 ? 1 : a.r <= 32 ? 2 : 4;
+    const int rb = a.r <= 16 ? 1 : a.r <= 32 ? 2 : a.r <= 64 || NG < 8 ? 4 : 8;
     const unsigned grid = (unsigned)(a.tiles * ((a.r + 16 * rb - 1) / (16 * rb)) * a.ks);
+    constexpr int NT = NG == 8 ? 512 : 256;
     if (rb == 1)
-        shrink_kernel<T, NG, 1, KMAJOR, DX><<<grid, 256, 0, stream>>>(a);
+        shrink_kernel<T, NG, 1, KMAJOR, DX><<<grid, NT, 0, stream>>>(a);
     else if (rb == 2)
-        shrink_kernel<T, NG, 2, KMAJOR, DX><<<grid, 256, 0, stream>>>(a);
-    else
-        shrink_kernel<T, NG, 4, KMAJOR, DX><<<grid, 256, 0, stream>>>(a);
+        shrink_kernel<T, NG, 2, KMAJOR, DX><<<grid, NT, 0, stream>>>(a);
+    else if (rb == 4)
+        shrink_kernel<T, NG, 4, KMAJOR, DX><<<grid, NT, 0, stream>>>(a);
+    else if constexpr (NG == 8)
+        shrink_kernel<T, NG, 8, KMAJOR, DX><<<grid, NT, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 template <class T, bool KMAJOR, bool DX>
 static hipError_t shrink_rows(const ShrinkArgs &a, hipStream_t stream) {
-    return a.b <= kFewRows ? shrink_ranks<T, 1, KMAJOR, DX>(a, stream) : shrink_ranks<T, 4, KMAJOR, DX>(a, stream);
+    if (a.b <= kFewRows) return shrink_ranks<T, 1, KMAJOR, DX>(a, stream);
+    return a.b <= kManyRows ? shrink_ranks<T, 4, KMAJOR, DX>(a, stream) : shrink_ranks<T, 8, KMAJOR, DX>(a, stream);
 }
 
 hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t stream) {
@@ -443,10 +448,11 @@ __host__ __device__ inline int parts_bytes(int r) { return (r + 31) / 32 * 128; 
 
 // Many rows: every column block of expand needs the rows' parts, so one launch forms them
 // once, 16 threads a row. (With few rows expand forms them itself and saves the launch.)
-template <class T>
+template <class T, int R>
 __global__ __launch_bounds__(256) void split_kernel(ExpandArgs a) {
-    const Tile t = tile_of<64>(a.plan, blockIdx.x / 4, a.b);
-    const int i = (blockIdx.x % 4) * 16 + threadIdx.x / 16, q = threadIdx.x % 16;
+    constexpr int G = R / 16;
+    const Tile t = tile_of<R>(a.plan, blockIdx.x / G, a.b);
+    const int i = (blockIdx.x % G) * 16 + threadIdx.x / 16, q = threadIdx.x % 16;
     if (i >= t.rows) return;
     const int64_t pos = t.first + i, row = t.row[i];
     if (t.adapter < 0) {
@@ -601,10 +607,10 @@ __device__ __forceinline__ void expand_base(const ExpandArgs &a, const int64_t (
 
 constexpr int kTurnBytes = 16 * (64 * 4 + 16);
 
-// Many rows: a tile of 64 x 256 columns, 64 a wave. Row numbers, bases, weights and the rows'
+// Many rows: 64 rows (a tile of the plan or half of one) x 256 columns, 64 a wave. Row numbers, bases, weights and the rows'
 // parts (split_kernel's, to LDS) are all requested before the first is used, and nothing is
 // loaded after the first store (loads and stores share a counter).
-template <class T, int KS, bool KMAJOR>
+template <class T, int KS, bool KMAJOR, int TR>
 __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int ncol) {
     using W = Weights<KS, KMAJOR>;
     constexpr int R = 64, STRIDE = KS * 128 + 16, NQ = R / 16;  // padded LDS row of parts
@@ -612,8 +618,16 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int ncol) {
     __shared__ __align__(16) uint8_t parts[R * STRIDE];
     __shared__ float undo[R];
     __shared__ __align__(16) uint8_t wlds[4][WB];
-    const int64_t id = xcd_order(blockIdx.x, gridDim.x);  // a tile's columns, and one adapter's weights, on one XCD
-    const Tile t = tile_of<R>(a.plan, id / ncol, a.b);
+    const int64_t ctas = (int64_t)a.plan.head[0] * (TR / R) * ncol;
+    if (blockIdx.x >= ctas) return;
+    const int64_t id = xcd_order(blockIdx.x, ctas);  // a tile's columns, and one adapter's weights, on one XCD
+    Tile t = tile_of<TR>(a.plan, id / ncol / (TR / R), a.b);
+    if constexpr (TR > R) {
+        const int i0 = (int)(id / ncol % (TR / R)) * R, left = t.rows - i0;
+        t.rows = left < 0 ? 0 : left < R ? left : R;
+        t.first += i0;
+        t.row += i0;
+    }
     if (t.rows == 0) return;
     const int64_t c0 = id % ncol * 256, c1 = c0 + 256 < a.n ? c0 + 256 : a.n;
     if (t.adapter < 0) return expand_plain(a, t, c0, c1, false);
@@ -696,10 +710,17 @@ template <class T, int KS, bool KMAJOR>
 static hipError_t expand_launch(const ExpandArgs &a, hipStream_t stream) {
     if (a.b > kFewRows) {
         const int ncol = (int)((a.n + 255) / 256);
-        split_kernel<T><<<(unsigned)(a.tiles * 4), 256, 0, stream>>>(a);
+        const bool many = a.b > kManyRows;
+        if (many)
+            split_kernel<T, 128><<<(unsigned)(a.tiles * 8), 256, 0, stream>>>(a);
+        else
+            split_kernel<T, 64><<<(unsigned)(a.tiles * 4), 256, 0, stream>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        expand_kernel<T, KS, KMAJOR><<<(unsigned)(a.tiles * ncol), 256, 0, stream>>>(a, ncol);
+        if (many)
+            expand_kernel<T, KS, KMAJOR, 128><<<(unsigned)(a.tiles * 2 * ncol), 256, 0, stream>>>(a, ncol);
+        else
+            expand_kernel<T, KS, KMAJOR, 64><<<(unsigned)(a.tiles * ncol), 256, 0, stream>>>(a, ncol);
         return hipGetLastError();
     }
     // runs a CTA: more where that still leaves four CTAs a compute unit

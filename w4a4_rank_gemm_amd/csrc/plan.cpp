@@ -101,11 +101,13 @@ FoldLayout fold_layout(int64_t m, int64_t n, int64_t r) {
 
 // ---- adapters and the input gradient ----
 
-// K slices: enough CTAs to fill the 256 compute units twice, at least two stages of 128
-// each, at most 16 (the partial sums are read again).
-int shrink_slices(int64_t k, int64_t r, int64_t tiles) {
-    const int64_t rt = r <= 32 ? 1 : (r + 63) / 64, steps = (k + 127) / 128;
-    int64_t ks = 512 / (tiles * rt);
+// K slices: enough CTAs to fill the 256 compute units twice (once with 128-row tiles, whose
+// CTAs are twice as large), at least two stages of 128 each, at most 16 (the partial sums are
+// read again).
+int shrink_slices(int64_t b, int64_t k, int64_t r, int64_t tiles) {
+    const bool many = b > kManyRows;
+    const int64_t rt = r <= 32 ? 1 : many ? (r + 127) / 128 : (r + 63) / 64, steps = (k + 127) / 128;
+    int64_t ks = (many ? 256 : 512) / (tiles * rt);
     if (ks > steps / 2) ks = steps / 2;
     if (ks > 16) ks = 16;
     return ks < 1 ? 1 : (int)ks;
@@ -124,7 +126,7 @@ DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
     if (ks > stages / 4) ks = stages < 16 ? 1 : stages / 4;
     if (ks > 16) ks = 16;
     p.ks = ks < 1 ? 1 : (int)ks;
-    p.tks = r > 0 ? shrink_slices(n, r, (b + tile_rows(b) - 1) / tile_rows(b)) : 0;
+    p.tks = r > 0 ? shrink_slices(b, n, r, (b + tile_rows(b) - 1) / tile_rows(b)) : 0;
     p.g = 0;
     p.ge = up((size_t)b * p.npad * 2);
     p.rowmax = p.ge + up((size_t)b * 8);

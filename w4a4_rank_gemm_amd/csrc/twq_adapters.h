@@ -11,9 +11,9 @@ namespace twq {
 // ---- the plan of a batch: its token rows sorted by adapter ---------------------------
 
 // Token rows of one tile (never two adapters in one): 16 up to 256 rows, which the kernels
-// for few rows take, 64 above.
-constexpr int kFewRows = 256;
-inline int tile_rows(int64_t b) { return b <= kFewRows ? 16 : 64; }
+// for few rows take, 64 above, 128 for many (the weights of a tile are read once a tile).
+constexpr int kFewRows = 256, kManyRows = 2048;
+inline int tile_rows(int64_t b) { return b <= kFewRows ? 16 : b <= kManyRows ? 64 : 128; }
 constexpr int64_t kMaxAdapters = 4096;
 
 // Rows of one piece of an adapter's tokens in the weight-gradient kernel. Longer pieces
@@ -93,7 +93,7 @@ struct ShrinkArgs {
     int ks;              // K slices
     float *p;            // [ks][b][r]
 };
-int shrink_slices(int64_t k, int64_t r, int64_t tiles);  // plan.cpp
+int shrink_slices(int64_t b, int64_t k, int64_t r, int64_t tiles);  // plan.cpp
 hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t stream);
 
 // ---- second product: out[row] = base[row] + c (sum_s P[s][pos]) W ---------------------
