@@ -213,21 +213,111 @@ __device__ __forceinline__ void dx_read(uint32_t w0, uint32_t w1, uint32_t g0, u
             : "memory");
 }
 
+// The low-rank term and the stores of TB token blocks of a wave, its sums in acc: lane holds
+// token lane % 32 of each block, columns 8 (v / 4) + 4 half + v % 4. All NT threads of the CTA
+// call it (L1 goes through their LDS).
+template <class T, int TB, int NT>
+__device__ __forceinline__ void dx_finish(const DxArgs &a, v16f (&acc)[2][TB], uint8_t *ring, int64_t tok0, int64_t m0,
+                                          int64_t slice, int wave) {
+    const int tid = threadIdx.x, lane = tid % kWave, li = lane & 15, half = lane >> 5;
+    float fin[TB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+        const int64_t tok = tok0 + t * 32 + lane % 32, tc = tok < a.b ? tok : a.b - 1;
+        int e = a.ge[tc * 2];
+        if (a.r > 0 && slice == 0) {
+            const int te = a.ge[tc * 2 + 1], d = e - te;
+            const float f = pow2(d < -126 ? -126 : d > 127 ? 127 : d);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[q][t][v] *= f;
+            e = te;
+        }
+        fin[t] = pow2(e);
+    }
+    if (a.r > 0 && slice == 0) {
+        const int r32 = (a.r + 31) / 32 * 32;
+        uint16_t *const l1 = reinterpret_cast<uint16_t *>(ring);  // [32 ranks][256 columns]
+        for (int k0 = 0; k0 < a.r; k0 += 32) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 1024 / NT; ++j) {
+                const int c = j * NT + tid, k = k0 + c / 32;
+                const int64_t col = m0 + c % 32 * 8;
+                *reinterpret_cast<v4i *>(l1 + c * 8) =
+                    load16(a.l1t + (int64_t)(k < a.r ? k : a.r - 1) * a.m + (col < a.m ? col : a.m - 8));
+            }
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // ranks 16 h + 8 half .. + 7
+                v4i wf[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const uint16_t *p = l1 + (h * 16 + half * 8 + li / 4) * 256 + wave * 64 + q * 32 + ((lane >> 4) & 1) * 16 + (li % 4) * 4;
+                    const v4s p0 = read_tr16(p), p1 = read_tr16(p + 4 * 256);
+                    wf[q] = join(p0, p1);
+                }
+#pragma unroll
+                for (int t = 0; t < TB; ++t) {
+                    const int64_t tok = tok0 + t * 32 + lane % 32, tc = tok < a.b ? tok : a.b - 1;
+                    const uint16_t *tp = a.t16 + (tc * r32 + k0 + h * 16 + half * 8) * 2;
+                    const v4i hi = load16(tp), lo = load16(tp + 8);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        acc[q][t] = mfma_f16_32(__builtin_bit_cast(v8h, wf[q]), __builtin_bit_cast(v8h, lo), acc[q][t]);
+                        acc[q][t] = mfma_f16_32(__builtin_bit_cast(v8h, wf[q]), __builtin_bit_cast(v8h, hi), acc[q][t]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+        const int64_t tok = tok0 + t * 32 + lane % 32;
+        if (tok >= a.b) continue;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int64_t col = m0 + wave * 64 + q * 32 + v * 8 + half * 4;
+                if (col >= a.m) continue;
+                v4f o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = acc[q][t][v * 4 + e] * fin[t];
+                if (a.ks > 1)
+                    *reinterpret_cast<v4f *>(a.part + (slice * a.b + tok) * a.m + col) = o;
+                else
+                    *reinterpret_cast<uint2 *>(a.dx + tok * a.m + col) =
+                        make_uint2((uint32_t)T::from_f32(o[0]) | (uint32_t)T::from_f32(o[1]) << 16,
+                                   (uint32_t)T::from_f32(o[2]) | (uint32_t)T::from_f32(o[3]) << 16);
+            }
+    }
+}
+
 // A CTA owns 32 TB tokens x 256 input columns over a slice of the channels; its four waves
 // take 64 columns each and share the tokens' operands. A stage of 64 channels is 8 KB of
 // codes and 4 TB KB of G, by direct-to-LDS loads into a ring of three stages (two in
 // flight). G rows are 128-byte lines with the 16-byte chunk index XORed by row % 8, code
 // rows 64 bytes with the chunk XORed by (row / 4) % 4, so both reads touch every bank once.
-template <class T, int TB>
-__global__ __launch_bounds__(256, 2) void dx_kernel(DxArgs a, int64_t npad, int64_t mtiles) {
+//
+// KG = 2: eight waves in two groups, each with its own ring and half of the channels; their
+// sums meet in LDS. That fills a compute unit with one CTA where the tiles are too few for two,
+// without sums in memory and a launch to join them (b=2048, 4096 x 14336: 271 to 261 us).
+template <class T, int TB, int KG>
+__global__ __launch_bounds__(256 * KG, 2 / KG) void dx_kernel(DxArgs a, int64_t npad, int64_t mtiles) {
     constexpr int BT = 32 * TB, WBYTES = kDxK / 16 * 2048, GBYTES = BT * 128, STAGE = WBYTES + GBYTES;
     constexpr int GL = GBYTES / 4096, LOADS = 2 + GL;  // direct-to-LDS loads of a wave per stage
-    __shared__ __align__(1024) uint8_t ring[kDxStages * STAGE];
-    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    constexpr int RING = kDxStages * STAGE;
+    __shared__ __align__(1024) uint8_t ring_lds[KG * RING];
+    const int tid = threadIdx.x, lane = tid % kWave, wave_id = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wave = wave_id % 4, grp = KG == 1 ? 0 : wave_id / 4;
+    uint8_t *const ring = ring_lds + grp * RING;
     const int li = lane & 15, half = lane >> 5;
     const int64_t mt = blockIdx.x % mtiles, tt = blockIdx.x / mtiles, slice = blockIdx.y;
     const int64_t tok0 = tt * BT, m0 = mt * kDxM, pieces = a.m / 128, panels = a.n / 16;
-    const int64_t nst = npad / kDxK, s0 = slice * nst / a.ks, s1 = (slice + 1) * nst / a.ks;
+    const int64_t nst = npad / kDxK, parts = (int64_t)a.ks * KG, part = slice * KG + grp;
+    const int64_t s0 = part * nst / parts, s1 = (part + 1) * nst / parts;
 
     // direct-to-LDS: lane l of a 1 KB block fetches row l / 8, chunk (l % 8) ^ row of G (8
     // rows), or row l / 4, chunk (l % 4) ^ (row / 4) of a panel piece (16 rows)
@@ -280,19 +370,20 @@ __global__ __launch_bounds__(256, 2) void dx_kernel(DxArgs a, int64_t npad, int6
         for (int h = 0; h < 2; ++h)
             ga[pr][h] = ring0 + WBYTES + (lane % 32) * 128 + ((pr * 4 + half * 2 + h) ^ (lane % 8)) * 16;
 
-    const int64_t n_st = s1 - s0;
+    const int64_t n_st = s1 - s0, rounds = KG == 1 ? n_st : (nst + parts - 1) / parts;  // the groups meet at barriers
     if (n_st > 0) issue(s0, 0);
     if (n_st > 1) issue(s0 + 1, 1);
-    for (int64_t c0 = 0; c0 < n_st; c0 += kDxStages) {
+    for (int64_t c0 = 0; c0 < rounds; c0 += kDxStages) {
         static_for(std::make_integer_sequence<int, kDxStages>{}, [&](auto u) {
             constexpr int U = decltype(u)::value, OFF = U * STAGE;
             const int64_t c = c0 + U;
-            if (c >= n_st) return;
+            if (c >= rounds) return;
             if (c + 1 < n_st)
                 wait_vmcnt<LOADS>();
             else
                 wait_vmcnt<0>();
             stage_barrier();  // stage c has landed for every wave, and stage c - 1 is read
+            if (KG > 1 && c >= n_st) return;
             if (c + 2 < n_st) issue(s0 + c + 2, (U + 2) % kDxStages);
             static_for(std::make_integer_sequence<int, 2>{}, [&](auto pv) {
                 constexpr int PR = decltype(pv)::value;
@@ -311,79 +402,44 @@ __global__ __launch_bounds__(256, 2) void dx_kernel(DxArgs a, int64_t npad, int6
         });
     }
 
-    // epilogue: lane holds token lane % 32 of each token block, columns 8 (v / 4) + 4 half + v % 4
-    float fin[TB];
-#pragma unroll
-    for (int t = 0; t < TB; ++t) {
-        const int64_t tok = tok0 + t * 32 + lane % 32, tc = tok < a.b ? tok : a.b - 1;
-        int e = a.ge[tc * 2];
-        if (a.r > 0 && slice == 0) {
-            const int te = a.ge[tc * 2 + 1], d = e - te;
-            const float f = pow2(d < -126 ? -126 : d > 127 ? 127 : d);
+    if constexpr (KG == 2) {
+        // group 0 finishes the first half of the token blocks, group 1 the second: each puts its
+        // sums of the other's half in LDS, [4 waves][2 column blocks][TB / 2][4][64 lanes] a group
+        constexpr int H = TB / 2;
+        v4f *const swap = reinterpret_cast<v4f *>(ring_lds);
+        auto slot = [&](int g, int q, int t, int v) { return swap + (((g * 4 + wave) * 2 + q) * H + t) * 4 * kWave + v * kWave + lane; };
+        auto put = [&](auto first) {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int v = 0; v < 16; ++v) acc[q][t][v] *= f;
-            e = te;
-        }
-        fin[t] = pow2(e);
-    }
-    if (a.r > 0 && slice == 0) {
-        const int r32 = (a.r + 31) / 32 * 32;
-        uint16_t *const l1 = reinterpret_cast<uint16_t *>(ring);  // [32 ranks][256 columns]
-        for (int k0 = 0; k0 < a.r; k0 += 32) {
-            __syncthreads();
+                for (int t = 0; t < H; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = j * 256 + tid, k = k0 + c / 32;
-                const int64_t col = m0 + c % 32 * 8;
-                *reinterpret_cast<v4i *>(l1 + c * 8) =
-                    load16(a.l1t + (int64_t)(k < a.r ? k : a.r - 1) * a.m + (col < a.m ? col : a.m - 8));
-            }
-            __syncthreads();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {  // ranks 16 h + 8 half .. + 7
-                v4i wf[2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint16_t *p = l1 + (h * 16 + half * 8 + li / 4) * 256 + wave * 64 + q * 32 + ((lane >> 4) & 1) * 16 + (li % 4) * 4;
-                    const v4s p0 = read_tr16(p), p1 = read_tr16(p + 4 * 256);
-                    wf[q] = join(p0, p1);
-                }
-#pragma unroll
-                for (int t = 0; t < TB; ++t) {
-                    const int64_t tok = tok0 + t * 32 + lane % 32, tc = tok < a.b ? tok : a.b - 1;
-                    const uint16_t *tp = a.t16 + (tc * r32 + k0 + h * 16 + half * 8) * 2;
-                    const v4i hi = load16(tp), lo = load16(tp + 8);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        acc[q][t] = mfma_f16_32(__builtin_bit_cast(v8h, wf[q]), __builtin_bit_cast(v8h, lo), acc[q][t]);
-                        acc[q][t] = mfma_f16_32(__builtin_bit_cast(v8h, wf[q]), __builtin_bit_cast(v8h, hi), acc[q][t]);
+                    for (int v = 0; v < 4; ++v) {
+                        const v16f &s = acc[q][decltype(first)::value + t];
+                        *slot(grp, q, t, v) = v4f{s[4 * v], s[4 * v + 1], s[4 * v + 2], s[4 * v + 3]};
                     }
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < TB; ++t) {
-        const int64_t tok = tok0 + t * 32 + lane % 32;
-        if (tok >= a.b) continue;
+        };
+        __syncthreads();  // every wave is done with the rings
+        if (grp == 0)
+            put(std::integral_constant<int, H>{});
+        else
+            put(std::integral_constant<int, 0>{});
+        __syncthreads();
+        v16f fold[2][H];
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int64_t col = m0 + wave * 64 + q * 32 + v * 8 + half * 4;
-                if (col >= a.m) continue;
-                v4f o;
+            for (int t = 0; t < H; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = acc[q][t][v * 4 + e] * fin[t];
-                if (a.ks > 1)
-                    *reinterpret_cast<v4f *>(a.part + (slice * a.b + tok) * a.m + col) = o;
-                else
-                    *reinterpret_cast<uint2 *>(a.dx + tok * a.m + col) =
-                        make_uint2((uint32_t)T::from_f32(o[0]) | (uint32_t)T::from_f32(o[1]) << 16,
-                                   (uint32_t)T::from_f32(o[2]) | (uint32_t)T::from_f32(o[3]) << 16);
-            }
+                for (int v = 0; v < 4; ++v) {
+                    const v4f o = *slot(1 - grp, q, t, v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)  // group 0's sum first, whichever group adds
+                        fold[q][t][4 * v + e] = (grp == 0 ? acc[q][t][4 * v + e] : o[e]) + (grp == 0 ? o[e] : acc[q][H + t][4 * v + e]);
+                }
+        dx_finish<T, H, 512>(a, fold, ring_lds, tok0 + grp * H * 32, m0, slice, wave);
+    } else {
+        dx_finish<T, TB, 256>(a, acc, ring_lds, tok0, m0, slice, wave);
     }
 }
 
@@ -407,11 +463,13 @@ static hipError_t dx_typed(const DxArgs &a, const DxPlan &p, hipStream_t stream)
     const int64_t mtiles = (a.m + kDxM - 1) / kDxM;
     const dim3 grid((unsigned)(mtiles * ((a.b + p.bt - 1) / p.bt)), (unsigned)p.ks);
     if (p.bt == 32)
-        dx_kernel<T, 1><<<grid, 256, 0, stream>>>(a, p.npad, mtiles);
+        dx_kernel<T, 1, 1><<<grid, 256, 0, stream>>>(a, p.npad, mtiles);
     else if (p.bt == 64)
-        dx_kernel<T, 2><<<grid, 256, 0, stream>>>(a, p.npad, mtiles);
+        dx_kernel<T, 2, 1><<<grid, 256, 0, stream>>>(a, p.npad, mtiles);
+    else if (p.kg == 1)
+        dx_kernel<T, 4, 1><<<grid, 256, 0, stream>>>(a, p.npad, mtiles);
     else
-        dx_kernel<T, 4><<<grid, 256, 0, stream>>>(a, p.npad, mtiles);
+        dx_kernel<T, 4, 2><<<grid, 512, 0, stream>>>(a, p.npad, mtiles);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.ks == 1) return e;
     const int64_t total = a.b * a.m;

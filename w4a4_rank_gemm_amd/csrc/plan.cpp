@@ -113,17 +113,19 @@ int shrink_slices(int64_t b, int64_t k, int64_t r, int64_t tiles) {
     return ks < 1 ? 1 : (int)ks;
 }
 
-// Token rows a CTA: as many as the batch fills, up to 128. Channel slices: with fewer CTAs
-// than two a compute unit, at least four stages each and at most 16; below 16 stages in all
-// the joining launch costs more than the slices save.
+// Token rows a CTA: as many as the batch fills, up to 128. Up to one 128-row tile a compute
+// unit, two groups of waves share its channels. Channel slices where the compute units are not
+// full (two CTAs of one group each, or one of two), at least four stages each and at most 16;
+// below 16 stages in all the joining launch costs more than the slices save.
 DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     DxPlan p{};
     p.bt = b <= 32 ? 32 : b <= 64 ? 64 : 128;
     p.npad = (n + kDxK - 1) / kDxK * kDxK;
     const int64_t ctas = (b + p.bt - 1) / p.bt * ((m + kDxM - 1) / kDxM), stages = p.npad / kDxK;
-    int64_t ks = ctas >= 512 ? 1 : 512 / ctas;
-    if (ks > stages / 4) ks = stages < 16 ? 1 : stages / 4;
+    p.kg = p.bt == 128 && ctas <= 256 && stages >= 16 ? 2 : 1;
+    int64_t ks = (p.kg == 2 ? 256 : 512) / ctas;
+    if (ks > stages / 4 / p.kg) ks = stages < 16 ? 1 : stages / 4 / p.kg;
     if (ks > 16) ks = 16;
     p.ks = ks < 1 ? 1 : (int)ks;
     p.tks = r > 0 ? shrink_slices(b, n, r, (b + tile_rows(b) - 1) / tile_rows(b)) : 0;

@@ -178,6 +178,7 @@ constexpr int kDxK = 64;   // output channels of a stage: four panels
 
 struct DxPlan {
     int bt;          // token rows a CTA
+    int kg;          // groups of four waves that share the channels of a CTA (2: bt = 128 only)
     int ks;          // slices of n
     int64_t npad;    // n rounded up to a K stage
     int tks;         // K slices of dY L2
