@@ -723,9 +723,12 @@ static hipError_t expand_launch(const ExpandArgs &a, hipStream_t stream) {
             expand_kernel<T, KS, KMAJOR, 64><<<(unsigned)(a.tiles * ncol), 256, 0, stream>>>(a, ncol);
         return hipGetLastError();
     }
-    // runs a CTA: more where that still leaves four CTAs a compute unit
-    int blocks = 1;
-    while (blocks < 8 && a.tiles * ((a.n + 511 * blocks) / (512 * blocks)) >= 1024) blocks *= 2;
+    // Runs a CTA: as many as leave the CTAs all resident at once (the registers allow 4, 3, 2
+    // or 1 a compute unit). 32 tiles of 28672 columns, 64 ranks: 1, 2, 4, 5 and 8 runs took 36, 32,
+    // 33, 27 and 29 us.
+    constexpr int resident = 256 * (KS == 1 ? 4 : KS == 2 ? 3 : KS == 4 ? 2 : 1);
+    const int64_t runs = (a.n + 255) / 256, blocks64 = (a.tiles * runs + resident - 1) / resident;
+    const int blocks = (int)(blocks64 < runs ? blocks64 : runs);
     const int ncol = (int)((a.n + 256 * blocks - 1) / (256 * blocks));
     expand_few_kernel<T, KS, KMAJOR><<<(unsigned)(a.tiles * ncol), 256, 0, stream>>>(a, ncol, blocks);
     return hipGetLastError();
