@@ -298,8 +298,9 @@ __device__ __forceinline__ void dx_finish(const DxArgs &a, v16f (&acc)[2][TB], u
 // A CTA owns 32 TB tokens x 256 input columns over a slice of the channels; its four waves
 // take 64 columns each and share the tokens' operands. A stage of 64 channels is 8 KB of
 // codes and 4 TB KB of G, by direct-to-LDS loads into a ring of three stages (two in
-// flight). G rows are 128-byte lines with the 16-byte chunk index XORed by row % 8, code
-// rows 64 bytes with the chunk XORed by (row / 4) % 4, so both reads touch every bank once.
+// flight). G rows are 128-byte lines with the 16-byte chunk index XORed by row % 8 and by
+// (row / 16) % 2 (one 16-byte read serves lanes 0-7 with 16-23 in a pass), code rows 64 bytes
+// with the chunk XORed by (row / 4) % 4.
 //
 // KG = 2: eight waves in two groups, each with its own ring and half of the channels; their
 // sums meet in LDS. That fills a compute unit with one CTA where the tiles are too few for two,
@@ -319,13 +320,13 @@ __global__ __launch_bounds__(256 * KG, 2 / KG) void dx_kernel(DxArgs a, int64_t 
     const int64_t nst = npad / kDxK, parts = (int64_t)a.ks * KG, part = slice * KG + grp;
     const int64_t s0 = part * nst / parts, s1 = (part + 1) * nst / parts;
 
-    // direct-to-LDS: lane l of a 1 KB block fetches row l / 8, chunk (l % 8) ^ row of G (8
+    // direct-to-LDS: lane l of a 1 KB block fetches row l / 8, chunk (l % 8) ^ row ^ (block / 2) of G (8
     // rows), or row l / 4, chunk (l % 4) ^ (row / 4) of a panel piece (16 rows)
     uint32_t goff[GL];
 #pragma unroll
     for (int j = 0; j < GL; ++j) {
         const int64_t row = (j * 4 + wave) * 8 + lane / 8, rel = tok0 + row < a.b ? row : a.b - 1 - tok0;
-        goff[j] = (uint32_t)(rel * npad * 2 + ((lane % 8) ^ (lane / 8)) * 16);
+        goff[j] = (uint32_t)(rel * npad * 2 + ((lane % 8) ^ (lane / 8) ^ ((j * 4 + wave) / 2 % 2)) * 16);
     }
     const uint32_t woff = (lane / 4) * 64 + ((lane % 4) ^ (lane / 16)) * 16;
     const uint8_t *gbase = reinterpret_cast<const uint8_t *>(a.g + tok0 * npad);
@@ -368,7 +369,7 @@ __global__ __launch_bounds__(256 * KG, 2 / KG) void dx_kernel(DxArgs a, int64_t 
     for (int pr = 0; pr < 2; ++pr)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            ga[pr][h] = ring0 + WBYTES + (lane % 32) * 128 + ((pr * 4 + half * 2 + h) ^ (lane % 8)) * 16;
+            ga[pr][h] = ring0 + WBYTES + (lane % 32) * 128 + ((pr * 4 + half * 2 + h) ^ (lane % 8) ^ (lane / 16 % 2)) * 16;
 
     const int64_t n_st = s1 - s0, rounds = KG == 1 ? n_st : (nst + parts - 1) / parts;  // the groups meet at barriers
     if (n_st > 0) issue(s0, 0);
