@@ -415,9 +415,10 @@ twq_status twq_fold_lowrank(const double *w, const double *u, const double *s, c
  *   at    [count][r][m], bt [count][n][r]   the adapters (layouts of l1t and l2t). Smaller
  *                                           ranks are padded with zeros.
  *   scale f32 [count]                       c_a, or NULL (1)
- * Shapes: as above, n and r positive, n at most 2^22, count 0..4096. Non-finite values in
- * rows without an adapter are not read; elsewhere they make the row (or the adapter's
- * gradient) non-finite.
+ * Shapes: as above, n and r positive, n at most 2^22, count 0..4096, and
+ * (b / 64 + min(b, count + 1)) ((m + n) / 128 + 2) below 2^24. Non-finite values in rows
+ * without an adapter are not read; elsewhere they make the row (or the adapter's gradient)
+ * non-finite.
  */
 #define TWQ_F16 0
 #define TWQ_BF16 1

@@ -89,6 +89,19 @@ def test_workspaces_and_plan_sizes():
     assert L.twq_linear_dx_workspace_bytes(16, 4096, 4100, 32) == 0
 
 
+def test_refused_launch_sizes():
+    """(b / 64 + min(b, count + 1)) ((m + n) / 128 + 2) stays below 2^24."""
+    L = twq.lib()
+    n = 128 * (2 ** 24 // 4161 - 2) // 16 * 16 - 256  # 4096 rows of 4096 adapters: 4160 tiles
+    assert L.twq_adapters_workspace_bytes(4096, 256, n, 16, 4096) > 0
+    assert L.twq_adapters_grad_workspace_bytes(4096, 256, n, 16, 4096) > 0
+    n += 2048
+    assert L.twq_adapters_workspace_bytes(4096, 256, n, 16, 4096) == 0
+    assert L.twq_adapters_grad_workspace_bytes(4096, 256, n, 16, 4096) == 0
+    assert _forward(4096, 256, n, 16, 4096) == SHAPE and _grad(4096, 256, n, 16, 4096) == SHAPE
+    assert L.twq_adapters_workspace_bytes(4096, 256, n, 16, 4000) > 0  # fewer adapters
+
+
 def test_empty_calls_launch_nothing():
     nothing = dict(x=None, at=None, bt=None, scale=None, plan=None, pb=0, y=None, out=None, h=None, ws=None, wsb=0)
     assert _forward(b=0, **nothing) == OK

@@ -365,3 +365,16 @@ def test_offsets_past_32_bits():
     q, s = ref.checkpoint(x[-3:])
     assert torch.equal(qc[-3:], q) and torch.equal(sc[:, -3:], s)
     assert torch.equal(twq.restore_act(qc, sc)[-3:], (q.float() * s.T.repeat_interleave(128, dim=1)).half())
+
+
+def test_most_token_rows():
+    """2^24 token rows, the limit, without a low-rank pair: the rows' maxima are found by a launch
+    of a CTA a row."""
+    b, m, n = 1 << 24, 128, 16
+    _say(f"linear_dx b={b} m={m} n={n} r=0")
+    g = _gen(24)
+    qw, sw, codes = _packed(n, m, g)
+    dy = (torch.randn(b, n, generator=g, device="cuda") * 2.0 ** -5).half()
+    dx = twq.linear_dx(dy, qw, sw)
+    for rows in (slice(0, 3), slice(b // 2 - 2, b // 2 + 2), slice(b - 3, b)):
+        ref.check(dx[rows], ref.linear_dx(dy[rows], codes, sw, None, None), f"rows {rows}")

@@ -175,7 +175,7 @@ __global__ __launch_bounds__(NG == 8 ? 512 : 256) void shrink_kernel(ShrinkArgs 
     const int rtiles = (a.r + 16 * RB - 1) / (16 * RB);
     const int64_t tiles = NG > 1 && a.plan.rows ? a.plan.head[0] : a.tiles, ctas = tiles * rtiles * a.ks;
     if (blockIdx.x >= ctas) return;
-    const int64_t id = xcd_order(blockIdx.x, ctas);
+    const int64_t id = xcd_range(blockIdx.x, ctas);
     const Tile t = tile_of<16 * NG>(a.plan, id % tiles, a.b);
     if (t.rows == 0 || t.adapter < 0) return;
     const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave, li = lane & 15, g = lane >> 4;
@@ -620,7 +620,7 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int ncol) {
     __shared__ __align__(16) uint8_t wlds[4][WB];
     const int64_t ctas = (int64_t)a.plan.head[0] * (TR / R) * ncol;
     if (blockIdx.x >= ctas) return;
-    const int64_t id = xcd_order(blockIdx.x, ctas);  // a tile's columns, and one adapter's weights, on one XCD
+    const int64_t id = xcd_range(blockIdx.x, ctas);  // a tile's columns, and one adapter's weights, on one XCD
     Tile t = tile_of<TR>(a.plan, id / ncol / (TR / R), a.b);
     if constexpr (TR > R) {
         const int i0 = (int)(id / ncol % (TR / R)) * R, left = t.rows - i0;

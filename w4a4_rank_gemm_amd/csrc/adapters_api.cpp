@@ -21,6 +21,12 @@ bool valid_count(int64_t c) { return c >= 0 && c <= kMaxAdapters; }
 bool valid_shape(int64_t b, int64_t m, int64_t n, int64_t r) {
     return valid_b(b) && valid_m(m) && n > 0 && n % 16 == 0 && n <= kMaxAdapterN && b * n <= kMaxOutput && valid_r(r);
 }
+// The largest launches: a tile's 256-column blocks, a piece's 128-column blocks. A grid
+// dimension holds fewer than 2^32 threads, 2^24 CTAs of 256.
+bool valid_grid(int64_t b, int64_t m, int64_t n, int64_t count) {
+    const int64_t groups = count + 1 < b ? count + 1 : b;
+    return (b / 64 + groups) * ((m + n) / 128 + 2) < int64_t(1) << 24;
+}
 
 twq_status done(hipError_t e, const char *name) { return e == hipSuccess ? TWQ_OK : (twq_status)hip_error(e, name); }
 
@@ -82,7 +88,7 @@ twq_status twq_adapter_plan(const int32_t *index, int64_t b, int64_t count, void
 }
 
 size_t twq_adapters_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count) {
-    if (!valid_shape(b, m, n, r) || r == 0 || !valid_count(count) || b == 0) return 0;
+    if (!valid_shape(b, m, n, r) || r == 0 || !valid_count(count) || !valid_grid(b, m, n, count) || b == 0) return 0;
     return forward_layout(b, m, r, count).total;
 }
 
@@ -90,7 +96,7 @@ twq_status twq_adapters(const void *x, const void *at, const void *bt, const flo
                         size_t plan_bytes, const void *y, void *out, float *h, int64_t b, int64_t m, int64_t n,
                         int64_t r, int64_t count, int type, void *workspace, size_t workspace_bytes, void *stream) {
     if (!valid_type(type)) return TWQ_ERR_UNSUPPORTED;
-    if (!valid_shape(b, m, n, r) || r == 0 || !valid_count(count)) return TWQ_ERR_SHAPE;
+    if (!valid_shape(b, m, n, r) || r == 0 || !valid_count(count) || !valid_grid(b, m, n, count)) return TWQ_ERR_SHAPE;
     if (b == 0) return TWQ_OK;
     if (!x || !plan || !out || (count > 0 && (!at || !bt))) return TWQ_ERR_NULL;
     if (!aligned16(x) || !aligned16(at) || !aligned16(bt) || !aligned16(scale) || !aligned16(plan) || !aligned16(y) ||
@@ -135,7 +141,7 @@ twq_status twq_adapters(const void *x, const void *at, const void *bt, const flo
 }
 
 size_t twq_adapters_grad_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count) {
-    if (!valid_shape(b, m, n, r) || r == 0 || !valid_count(count)) return 0;
+    if (!valid_shape(b, m, n, r) || r == 0 || !valid_count(count) || !valid_grid(b, m, n, count)) return 0;
     return grad_layout(b, m, n, r, count).total;
 }
 
@@ -144,7 +150,7 @@ twq_status twq_adapters_grad(const void *dy, const void *x, const void *qc, cons
                              const void *dx, void *dx_out, void *dat, void *dbt, int64_t b, int64_t m, int64_t n,
                              int64_t r, int64_t count, int type, void *workspace, size_t workspace_bytes, void *stream) {
     if (!valid_type(type)) return TWQ_ERR_UNSUPPORTED;
-    if (!valid_shape(b, m, n, r) || r == 0 || !valid_count(count)) return TWQ_ERR_SHAPE;
+    if (!valid_shape(b, m, n, r) || r == 0 || !valid_count(count) || !valid_grid(b, m, n, count)) return TWQ_ERR_SHAPE;
     if (b == 0 && count == 0) return TWQ_OK;
     if (!plan || (count > 0 && (!at || !bt || !dat || !dbt))) return TWQ_ERR_NULL;
     if (b > 0 && (!dy || !h || !dx_out || (!x && (!qc || !sc)))) return TWQ_ERR_NULL;

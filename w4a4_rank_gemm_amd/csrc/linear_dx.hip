@@ -23,12 +23,14 @@ constexpr int kDxStages = 3;
 // ---- G and T in fp16 -------------------------------------------------------------------
 
 // The largest |dY s_W| of each row (without a low-rank pair; otherwise the shrink kernel finds
-// it while it reads dY). One CTA a row.
+// it while it reads dY). One CTA a row, 2^23 along a grid dimension (it holds fewer than 2^32
+// threads).
 template <class T>
 __global__ __launch_bounds__(256) void dx_max_kernel(DxArgs a) {
     __shared__ uint32_t red[4];
     const int tid = threadIdx.x;
-    const int64_t row = blockIdx.x;
+    const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (row >= a.b) return;
     uint32_t mx = 0;
     for (int64_t c = tid * 8; c < a.n; c += 2048) {
         const v4i v = load16(a.dy + row * a.n + c);
@@ -49,10 +51,12 @@ __global__ __launch_bounds__(256) void dx_max_kernel(DxArgs a) {
 }
 
 hipError_t launch_dx_max(const DxArgs &a, hipStream_t stream) {
+    const int64_t most = int64_t(1) << 23;
+    const dim3 grid((unsigned)(a.b < most ? a.b : most), (unsigned)((a.b + most - 1) / most));
     if (a.bf16)
-        dx_max_kernel<BF16><<<(unsigned)a.b, 256, 0, stream>>>(a);
+        dx_max_kernel<BF16><<<grid, 256, 0, stream>>>(a);
     else
-        dx_max_kernel<F16><<<(unsigned)a.b, 256, 0, stream>>>(a);
+        dx_max_kernel<F16><<<grid, 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 

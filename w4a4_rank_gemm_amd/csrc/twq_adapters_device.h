@@ -70,6 +70,14 @@ __device__ __forceinline__ v4i join(v4s a, v4s b) {
     return __builtin_bit_cast(v4i, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// CTA b runs on XCD b % 8 (they are dealt out in turn). XCD x gets a contiguous range of `ctas`
+// ids, the first ctas % 8 XCDs one more: a bijection of [0, ctas), in which neighbours, which
+// share operands, share an L2.
+__device__ __forceinline__ int64_t xcd_range(int64_t b, int64_t ctas) {
+    const int64_t x = b % 8, more = ctas % 8;
+    return ctas / 8 * x + (x < more ? x : more) + b / 8;
+}
+
 // Power of two 2^e, e in [-126, 127].
 __device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
 

@@ -395,12 +395,4 @@ __device__ __forceinline__ void lds_read_scales32(uint32_t w, uint32_t x, v4f (&
         : "memory");
 }
 
-// Block b runs on XCD b % 8 (the hardware deals CTAs out in turn). Give XCD x the
-// contiguous range of q + (x < rem) tiles starting at x q + min(x, rem), q = tiles / 8,
-// rem = tiles % 8: a bijection of [0, tiles) for any tile count.
-__host__ __device__ __forceinline__ int64_t xcd_order(int64_t bid, int64_t ntiles) {
-    const int64_t q = ntiles / 8, rem = ntiles % 8, x = bid % 8, j = bid / 8;
-    return x * q + (x < rem ? x : rem) + j;
-}
-
 }  // namespace twq
