@@ -44,7 +44,7 @@ struct GradLayout {
 
 ForwardLayout forward_layout(int64_t b, int64_t k, int64_t r, int64_t count) {
     ForwardLayout L{};
-    L.ks = shrink_slices(b, k, r, plan_layout(b, count).max_tiles);
+    L.ks = shrink_slices(b, k, r, plan_layout(b, count).max_tiles, 4);
     L.p = 0;
     L.parts = align256((size_t)L.ks * b * r * 4);
     L.total = L.parts + align256(expand_parts_bytes(b, r));
@@ -60,7 +60,7 @@ void set_parts(ExpandArgs &a, uint8_t *at) {
 GradLayout grad_layout(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count) {
     const PlanLayout pl = plan_layout(b, count);
     GradLayout L{};
-    L.ks = b > 0 ? shrink_slices(b, n, r, pl.max_tiles) : 1;
+    L.ks = b > 0 ? shrink_slices(b, n, r, pl.max_tiles, 4) : 1;
     L.p = 0;
     L.parts = align256((size_t)L.ks * b * r * 4);
     L.g = L.parts + align256(expand_parts_bytes(b, r));

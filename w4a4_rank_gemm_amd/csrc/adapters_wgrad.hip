@@ -255,12 +255,7 @@ __global__ __launch_bounds__(256) void outer_join_kernel(OuterArgs a) {
     const int64_t per = (int64_t)a.r * (a.m + a.n), e4 = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (e4 * 4 >= per) return;
     v4f s = {0.f, 0.f, 0.f, 0.f};
-    const float *src = a.part + (parts ? (int64_t)a.plan.slot0[ad] * per : 0) + e4 * 4;
-    for (int p = 0; p < parts; ++p) {
-        const v4f v = *reinterpret_cast<const v4f *>(src + p * per);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] += v[e];
-    }
+    if (parts > 1) s = sum_slices(a.part + (int64_t)a.plan.slot0[ad] * per + e4 * 4, per, parts);
     const int64_t at = e4 * 4, na = (int64_t)a.r * a.m;
     if (at < na)
         outer_put<T>(a, a.dat + ad * na, nullptr, at, s);

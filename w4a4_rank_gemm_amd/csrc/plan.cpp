@@ -102,33 +102,48 @@ FoldLayout fold_layout(int64_t m, int64_t n, int64_t r) {
 // ---- adapters and the input gradient ----
 
 // K slices: enough CTAs to fill the 256 compute units twice (once with 128-row tiles, whose
-// CTAs are twice as large), at least two stages of 128 each, at most 16 (the partial sums are
-// read again).
-int shrink_slices(int64_t b, int64_t k, int64_t r, int64_t tiles) {
+// CTAs are twice as large), at least `least` stages of 128 each, at most 16 (the partial sums are
+// read again). Half and twice as many CTAs: b=8192, 4096 -> 14336, 64 ranks, gradients 272 and
+// 215 us against 210; b=4096, 4096 -> 4096, 32 ranks, 63 and 64 against 60. At most 8 instead of
+// 16: one row, 14336 -> 4096, 64 ranks, 12.5 against 11.2 us; at most 32: 12.0.
+// `least`: 4 for adapters (b=256, 4096 -> 4096: 2, 3, 4 and 8 stages took 11.9, 12.0, 10.3 and
+// 12.4 us), 2 for the input gradient, whose slices also find the rows' maxima (b=512, 1024 x 4096,
+// 64 ranks: 2, 4 and 8 stages 34, 37 and 44 us).
+int shrink_slices(int64_t b, int64_t k, int64_t r, int64_t tiles, int64_t least) {
     const bool many = b > kManyRows;
     const int64_t rt = r <= 32 ? 1 : many ? (r + 127) / 128 : (r + 63) / 64, steps = (k + 127) / 128;
     int64_t ks = (many ? 256 : 512) / (tiles * rt);
-    if (ks > steps / 2) ks = steps / 2;
+    if (ks > steps / least) ks = steps / least;
     if (ks > 16) ks = 16;
     return ks < 1 ? 1 : (int)ks;
 }
 
-// Token rows a CTA: as many as the batch fills, up to 128. Up to one 128-row tile a compute
-// unit, two groups of waves share its channels. Channel slices where the compute units are not
-// full (two CTAs of one group each, or one of two), at least four stages each and at most 16;
-// below 16 stages in all the joining launch costs more than the slices save.
+// Token rows a CTA, by the work in 128-row tiles x stages: small tiles fill the chip, large ones
+// expand each code for more rows. With 32, 64 and 128 rows (us):
+//   b=128,  512 x 512     17, 20, 27       b=256,  4096 x 14336  62, 58, 62
+//   b=512,  1024 x 4096   34, 42, 43       b=2048, 1024 x 4096   57, 58, 62
+//   b=64,   8192 x 28672  78, 85, 98       b=1024, 4096 x 14336  177, 153, 143
+//   b=128,  8192 x 28672  118, 104, 112    b=4096, 8192 x 28672  2242, 1871, 1792
+// Up to one 128-row tile a compute unit, two groups of waves share its channels (4096 x 4096, one
+// group and two: b=2048 104 and 90 us; b=4096, 512 tiles, 155 and 170).
+// Channel slices where the compute units are not full (two CTAs of one group each, or one of
+// two), at least four stages each and at most 16 (b=16, 4096 x 14336: at most 4 and 16 took 47 and
+// 29 us; at most 32, as 16); below 16 stages in all the joining launch costs more than the slices
+// save.
 DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     DxPlan p{};
-    p.bt = b <= 32 ? 32 : b <= 64 ? 64 : 128;
+    const int64_t mtiles = (m + kDxM - 1) / kDxM;
     p.npad = (n + kDxK - 1) / kDxK * kDxK;
-    const int64_t ctas = (b + p.bt - 1) / p.bt * ((m + kDxM - 1) / kDxM), stages = p.npad / kDxK;
+    const int64_t stages = p.npad / kDxK, work = (b + 127) / 128 * mtiles * stages;
+    p.bt = b <= 64 || work < 4096 ? 32 : b <= 128 || work < 8192 ? 64 : 128;
+    const int64_t ctas = (b + p.bt - 1) / p.bt * mtiles;
     p.kg = p.bt == 128 && ctas <= 256 && stages >= 16 ? 2 : 1;
     int64_t ks = (p.kg == 2 ? 256 : 512) / ctas;
     if (ks > stages / 4 / p.kg) ks = stages < 16 ? 1 : stages / 4 / p.kg;
     if (ks > 16) ks = 16;
     p.ks = ks < 1 ? 1 : (int)ks;
-    p.tks = r > 0 ? shrink_slices(b, n, r, (b + tile_rows(b) - 1) / tile_rows(b)) : 0;
+    p.tks = r > 0 ? shrink_slices(b, n, r, (b + tile_rows(b) - 1) / tile_rows(b), 2) : 0;
     p.g = 0;
     p.ge = up((size_t)b * p.npad * 2);
     p.rowmax = p.ge + up((size_t)b * 8);

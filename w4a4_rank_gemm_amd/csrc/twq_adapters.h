@@ -11,7 +11,12 @@ namespace twq {
 // ---- the plan of a batch: its token rows sorted by adapter ---------------------------
 
 // Token rows of one tile (never two adapters in one): 16 up to 256 rows, which the kernels
-// for few rows take, 64 above, 128 for many (the weights of a tile are read once a tile).
+// for few rows take (no launch that splits the rows' sums); 64 above; 128 for many (the weights of
+// a tile are read once a tile). Measured, forward (8 adapters):
+//   b=256, 4096 -> 4096, 32 ranks      16-row tiles 12.0 us, 64-row 14.7
+//   b=512, 4096 -> 4096, 32 ranks      14.5, 17.7;  8192 -> 28672, 128 ranks 67, 55
+//   b=2048, 4096 -> 14336, 64 ranks    64-row tiles 55.6 us, 128-row 60.4
+//   b=4096, the same                   89 and 92; its gradients 129 and 124
 constexpr int kFewRows = 256, kManyRows = 2048;
 inline int tile_rows(int64_t b) { return b <= kFewRows ? 16 : b <= kManyRows ? 64 : 128; }
 constexpr int64_t kMaxAdapters = 4096;
@@ -93,7 +98,7 @@ struct ShrinkArgs {
     int ks;              // K slices
     float *p;            // [ks][b][r]
 };
-int shrink_slices(int64_t b, int64_t k, int64_t r, int64_t tiles);  // plan.cpp
+int shrink_slices(int64_t b, int64_t k, int64_t r, int64_t tiles, int64_t least);  // plan.cpp
 hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t stream);
 
 // ---- second product: out[row] = base[row] + c (sum_s P[s][pos]) W ---------------------

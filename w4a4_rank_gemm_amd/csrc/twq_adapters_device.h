@@ -70,6 +70,21 @@ __device__ __forceinline__ v4i join(v4s a, v4s b) {
     return __builtin_bit_cast(v4i, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// Sum of `count` slices, `stride` floats apart, in order, eight in flight.
+__device__ __forceinline__ v4f sum_slices(const float *p, int64_t stride, int count) {
+    v4f s = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < count; i += 8) {
+        v4f v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const v4f *>(p + (i + j < count ? i + j : i) * stride);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] += i + j < count ? v[j][e] : 0.f;
+    }
+    return s;
+}
+
 // CTA b runs on XCD b % 8 (they are dealt out in turn). XCD x gets a contiguous range of `ctas`
 // ids, the first ctas % 8 XCDs one more: a bijection of [0, ctas), in which neighbours, which
 // share operands, share an L2.
