@@ -60,20 +60,34 @@ hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t) {
     return hipSuccess;
 }
 
-hipError_t launch_expand(const ExpandArgs &a, hipStream_t) {
-    plan_read(a.plan, a.b, a.tiles);
+static void split(const ExpandArgs &a) {
     rd(a.p, (size_t)a.ks * a.b * a.r * 4);
-    rd(a.base, a.b * a.n * 2);
-    wr(a.out, a.b * a.n * 2);
     wr(a.sum, a.b * a.r * 4);
     if (a.planes) {
         rd(a.h, a.b * a.r * 4);
         wr(a.planes, a.b * a.r * 8);
     }
-    if (a.b > kFewRows) {
-        wr(a.parts, a.b * ((a.r + 31) / 32 * 128));
-        wr(a.undo, a.b * 4);
+}
+
+hipError_t launch_split(const ExpandArgs &a, hipStream_t) {
+    if (a.b <= kFewRows) return hipErrorInvalidValue;
+    plan_read(a.plan, a.b, a.tiles);
+    split(a);
+    wr(a.parts, a.b * ((a.r + 31) / 32 * 128));
+    wr(a.undo, a.b * 4);
+    return hipSuccess;
+}
+
+hipError_t launch_expand(const ExpandArgs &a, hipStream_t) {
+    plan_read(a.plan, a.b, a.tiles);
+    if (a.b <= kFewRows) {
+        split(a);
+    } else {
+        rd(a.parts, a.b * ((a.r + 31) / 32 * 128));
+        rd(a.undo, a.b * 4);
     }
+    rd(a.base, a.b * a.n * 2);
+    wr(a.out, a.b * a.n * 2);
     return hipSuccess;
 }
 

@@ -710,14 +710,7 @@ template <class T, int KS, bool KMAJOR>
 static hipError_t expand_launch(const ExpandArgs &a, hipStream_t stream) {
     if (a.b > kFewRows) {
         const int ncol = (int)((a.n + 255) / 256);
-        const bool many = a.b > kManyRows;
-        if (many)
-            split_kernel<T, 128><<<(unsigned)(a.tiles * 8), 256, 0, stream>>>(a);
-        else
-            split_kernel<T, 64><<<(unsigned)(a.tiles * 4), 256, 0, stream>>>(a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        if (many)
+        if (a.b > kManyRows)
             expand_kernel<T, KS, KMAJOR, 128><<<(unsigned)(a.tiles * 2 * ncol), 256, 0, stream>>>(a, ncol);
         else
             expand_kernel<T, KS, KMAJOR, 64><<<(unsigned)(a.tiles * ncol), 256, 0, stream>>>(a, ncol);
@@ -740,6 +733,19 @@ static hipError_t expand_ranks(const ExpandArgs &a, hipStream_t stream) {
     if (a.r <= 64) return expand_launch<T, 2, KMAJOR>(a, stream);
     if (a.r <= 128) return expand_launch<T, 4, KMAJOR>(a, stream);
     return expand_launch<T, 8, KMAJOR>(a, stream);
+}
+
+template <class T>
+static hipError_t split_typed(const ExpandArgs &a, hipStream_t stream) {
+    if (a.b > kManyRows)
+        split_kernel<T, 128><<<(unsigned)(a.tiles * 8), 256, 0, stream>>>(a);
+    else
+        split_kernel<T, 64><<<(unsigned)(a.tiles * 4), 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_split(const ExpandArgs &a, hipStream_t stream) {
+    return a.bf16 ? split_typed<BF16>(a, stream) : split_typed<F16>(a, stream);
 }
 
 hipError_t launch_expand(const ExpandArgs &a, hipStream_t stream) {

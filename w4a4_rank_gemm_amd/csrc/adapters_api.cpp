@@ -137,7 +137,9 @@ twq_status twq_adapters(const void *x, const void *at, const void *bt, const flo
     x2.out = static_cast<uint16_t *>(out);
     x2.sum = h;
     set_parts(x2, static_cast<uint8_t *>(workspace) + L.parts);
-    return done(launch_expand(x2, st), "twq_adapters");
+    if (b > kFewRows) e = launch_split(x2, st);
+    if (e == hipSuccess) e = launch_expand(x2, st);
+    return done(e, "twq_adapters");
 }
 
 size_t twq_adapters_grad_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r, int64_t count) {
@@ -201,8 +203,13 @@ twq_status twq_adapters_grad(const void *dy, const void *x, const void *qc, cons
     x2.planes = reinterpret_cast<uint16_t *>(ws + L.planes);
     x2.h = h;
     set_parts(x2, ws + L.parts);
-    if (b > 0) e = launch_expand(x2, st);
-    if (e != hipSuccess || count == 0) return done(e, "twq_adapters_grad");
+    // The weight gradients come before the expand where it does not form their factors: their
+    // read of dY then finds what the shrink's left in the caches.
+    if (b > kFewRows)
+        e = launch_split(x2, st);
+    else if (b > 0)
+        e = launch_expand(x2, st);
+    if (e != hipSuccess) return done(e, "twq_adapters_grad");
 
     OuterArgs o{};
     o.g = x2.sum;
@@ -224,7 +231,9 @@ twq_status twq_adapters_grad(const void *dy, const void *x, const void *qc, cons
     o.part = reinterpret_cast<float *>(ws + L.part);
     o.dat = static_cast<uint16_t *>(dat);
     o.dbt = static_cast<uint16_t *>(dbt);
-    return done(launch_outer(o, st), "twq_adapters_grad");
+    if (count > 0) e = launch_outer(o, st);
+    if (e == hipSuccess && b > kFewRows) e = launch_expand(x2, st);
+    return done(e, "twq_adapters_grad");
 }
 
 twq_status twq_checkpoint_act(const void *x, int64_t b, int64_t m, int type, void *qc, float *sc, void *stream) {

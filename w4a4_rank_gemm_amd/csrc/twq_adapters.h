@@ -126,6 +126,9 @@ struct ExpandArgs {
 inline size_t expand_parts_bytes(int64_t b, int64_t r) {
     return b > kFewRows ? (size_t)b * ((size_t)(r + 31) / 32 * 128 + 4) : 0;
 }
+// More than kFewRows rows: the split forms the sums' parts (and planes and sums), the expand uses
+// them. Up to kFewRows rows the expand does both.
+hipError_t launch_split(const ExpandArgs &a, hipStream_t stream);
 hipError_t launch_expand(const ExpandArgs &a, hipStream_t stream);
 
 // ---- weight gradients -------------------------------------------------------------------
