@@ -6,12 +6,12 @@
 //
 //   G[i] = B_a^T dy_i,   dX[i] = dx_i + c_a A_a^T G[i].
 //
-// Token rows are grouped by adapter (the plan), so a tile of 16 or 64 rows shares one
+// Token rows are grouped by adapter (the plan), so a tile of 16, 64 or 128 rows shares one
 // adapter's weights, whatever the order of the requests in the batch; no row is moved.
-// Each product is a pair of launches: shrink (K = the long axis, partial sums over K
-// slices) and expand (K = the rank). Both are bound by memory: shrink by the rows and the
-// adapters' first factors, expand by the read and write of the output rows. All sums
-// are in binary32 and in a fixed order, so equal calls give equal bits.
+// A product is two launches, shrink (K = the long axis, partial sums over K slices) and expand
+// (K = the rank), with a split of the sums between them for many rows. All are bound by memory:
+// shrink by the rows and the adapters' first factors, expand by the read and write of the
+// output rows. All sums are in binary32 and in a fixed order, so equal calls give equal bits.
 #include "twq_adapters.h"
 #include "twq_adapters_device.h"
 
@@ -23,7 +23,9 @@ constexpr int kPlanThreads = 1024;
 
 // CTA a owns adapter a (CTA `count`: the rows without one). It counts every adapter's
 // rows, from which its own first position, first tile and first piece follow, then
-// scans the index again and writes its rows in token order.
+// scans the index again and writes its rows in token order. Every CTA repeats the count, so that
+// one launch does without a sum across CTAs; bound by the second scan's steps of 1024 rows
+// (one row 6 us, 4096 rows of 6 adapters 14, 8192 of 16 21; made once for all layers of a batch).
 __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_t *index, int64_t b, int count, uint8_t *plan,
                                                            PlanLayout L, int chunk, int trows) {
     __shared__ int hist[kMaxAdapters + 1];
@@ -153,10 +155,15 @@ __device__ __forceinline__ Tile tile_of(const PlanView &p, int64_t t, int64_t b)
 
 // A tile of 16 NG rows x 16 RB ranks over a slice of K, in stages of 128 elements through
 // LDS. Global loads run along the rows (sixteen lanes to a row's 256 bytes): matrix operands
-// loaded straight to registers would put neighbouring lanes on different rows, which reads
-// L2 at about half the rate (2.9 against 4.4 TB/s of X at 4096 x 14336, 64 ranks). The next
-// stage is in registers while this one is used. With 64 rows (NG = 4) a wave owns 16 rows;
-// with 16 (NG = 1) a quarter of each stage, and the waves' sums are added in wave order.
+// loaded straight to registers put neighbouring lanes on different rows (4096 x 14336, 64 ranks:
+// 40 us against 33). The next stage is on its way to registers while this one is used; two
+// stages ahead, or one LDS buffer and two or three CTAs a compute unit, gained nothing. With 64
+// or 128 rows (NG = 4, 8) a wave owns 16 rows; with 16 (NG = 1) a quarter of each stage, and the
+// waves' sums are added in wave order. More rows read the weights less often, and all ranks up to
+// 128 in one pass the rows once.
+// Bound by the read of V: 4096 x 14336, 64 ranks, 31 us (3.8 TB/s of X; a 1 GiB copy moves 5.1);
+// 8192 x 14336 by 64 ranks 66 us (3.6), by 16 ranks 52 us (4.5); 32 rows of 32 adapters,
+// 8192 x 64 each, 9.4 us (3.6 TB/s of weights).
 // KMAJOR weights ([k][r], ranks contiguous) are read back from LDS transposed. DX (the frozen
 // layer's input gradient): fp16 weights whatever the rows, split exactly into two bf16 parts
 // for bf16 rows; and the rows' largest |v sw| on the way.
@@ -447,7 +454,9 @@ __device__ __forceinline__ float split_row(const ExpandArgs &a, int64_t pos, int
 __host__ __device__ inline int parts_bytes(int r) { return (r + 31) / 32 * 128; }
 
 // Many rows: every column block of expand needs the rows' parts, so one launch forms them
-// once, 16 threads a row. (With few rows expand forms them itself and saves the launch.)
+// once, 16 threads a row. (With few rows expand forms them itself and saves the launch.) Bound by
+// its start and two dependent reads: 4096 rows of 64 ranks, 6 slices, 5.3 us; 8192 rows with the
+// weight gradients' parts 8.3 us.
 template <class T, int R>
 __global__ __launch_bounds__(256) void split_kernel(ExpandArgs a) {
     constexpr int G = R / 16;
@@ -467,11 +476,10 @@ __global__ __launch_bounds__(256) void split_kernel(ExpandArgs a) {
 
 // The weights of 64 output columns from col0, for one wave: KS steps of 32 ranks x four
 // sub-tiles of 16 columns. Memory is read along its rows ([n][r], or [r][n] if KMAJOR) into
-// registers (fetch); then, 32 KP ranks at a time, through this wave's LDS into matrix operands
+// registers (fetch); then, 32 KP ranks a pass, through this wave's LDS into matrix operands
 // (place), transposed if KMAJOR.
-template <int KS, bool KMAJOR>
+template <int KS, bool KMAJOR, int KP>
 struct Weights {
-    static constexpr int KP = KMAJOR || KS < 2 ? 1 : 2;             // steps of 32 ranks a pass
     static constexpr int STRIDE = KMAJOR ? 64 * 2 + 16 : KP * 64 + 16;  // padded LDS row
     static constexpr int BYTES = (KMAJOR ? 32 : 64) * STRIDE;
     v4i in[KS / KP][KP * 4];
@@ -607,12 +615,16 @@ __device__ __forceinline__ void expand_base(const ExpandArgs &a, const int64_t (
 
 constexpr int kTurnBytes = 16 * (64 * 4 + 16);
 
-// Many rows: 64 rows (a tile of the plan or half of one) x 256 columns, 64 a wave. Row numbers, bases, weights and the rows'
-// parts (split_kernel's, to LDS) are all requested before the first is used, and nothing is
-// loaded after the first store (loads and stores share a counter).
+// Many rows: 64 rows (a tile of the plan or half of one) x 256 columns, 64 a wave. Row numbers,
+// bases, weights and the rows' parts (split_kernel's, to LDS) are all requested before the first
+// is used, and nothing is loaded after the first store (loads and stores share a counter).
+// Weights pass through LDS 32 ranks at a time: up to 64 ranks that leaves room for four CTAs a
+// compute unit (with 64 ranks a pass, three: 4096 x 4096, 64 ranks, 26.6 against 22.9 us).
+// Bound by the base and output rows: that case moves 76 MB, 3.3 TB/s; 8192 x 4096, 64 ranks,
+// 36.8 us (4.1 TB/s).
 template <class T, int KS, bool KMAJOR, int TR>
-__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int ncol) {
-    using W = Weights<KS, KMAJOR>;
+__global__ __launch_bounds__(256, KS <= 2 ? 4 : 1) void expand_kernel(ExpandArgs a, int ncol) {
+    using W = Weights<KS, KMAJOR, 1>;
     constexpr int R = 64, STRIDE = KS * 128 + 16, NQ = R / 16;  // padded LDS row of parts
     constexpr int WB = W::BYTES > kTurnBytes ? W::BYTES : kTurnBytes;
     __shared__ __align__(16) uint8_t parts[R * STRIDE];
@@ -669,10 +681,12 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int ncol) {
 
 // Few rows: a tile of 16 x `blocks` runs of 256 columns, 64 a wave. The rows' parts are
 // formed here, once for all the runs, while the first run's weights are on their way; the
-// next run's weights are requested before this one's are used.
+// next run's weights are requested before this one's are used. Bound by the weights: 32 rows of
+// 32 adapters, 28672 x 64 each, 26 us (4.6 TB/s). Up to 64 ranks a pass through LDS here: the
+// registers allow no fourth CTA, and 32 ranks a pass took 28 us.
 template <class T, int KS, bool KMAJOR>
-__global__ __launch_bounds__(256) void expand_few_kernel(ExpandArgs a, int ncol, int blocks) {
-    using W = Weights<KS, KMAJOR>;
+__global__ __launch_bounds__(256, KS == 1 ? 4 : 1) void expand_few_kernel(ExpandArgs a, int ncol, int blocks) {
+    using W = Weights<KS, KMAJOR, KMAJOR || KS < 2 ? 1 : 2>;
     constexpr int STRIDE = KS * 128 + 16;
     constexpr int WB = W::BYTES > kTurnBytes ? W::BYTES : kTurnBytes;
     __shared__ __align__(16) uint8_t parts[16 * STRIDE];

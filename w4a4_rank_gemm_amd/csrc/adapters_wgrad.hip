@@ -5,8 +5,12 @@
 // over the token rows i of adapter a: products whose long axis K is the tokens, so both
 // operands lie with K as the slow index. They are staged in LDS row by row and read
 // transposed. One CTA takes a piece of one adapter's rows and 128 columns of X or dY;
-// both gradients are one launch. Each element of X and dY is read once; X may come as an
-// 8-bit checkpoint, whose codes feed the matrix cores as they are.
+// both gradients are one launch. Each element of X and dY is read once (up to 128 ranks); X may
+// come as an 8-bit checkpoint, whose codes are made bf16 in registers.
+//
+// Bound by memory: 8192 rows, 4096 (codes) + 14336 columns, 64 ranks 71 us (268 MB of rows, 3.8
+// TB/s; 305 MB with the factors' repeated reads); 2048 rows, 32 ranks 19 us. Wider tiles read the
+// factor less often but are fewer: 256 and 512 columns a CTA were equal to 45% slower.
 //
 // The binary32 factor, c_a G or c_a H, comes as two bf16 parts, 16 significant bits together
 // (expand's planes); with a checkpoint c_a G still takes the group's scale of the token and is
@@ -245,8 +249,9 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a) {
     }
 }
 
-// Gradients of adapters whose rows were several pieces: the pieces' sums in order. Adapters
-// without rows get zeros; those of one piece were written whole.
+// Gradients of adapters whose rows were several pieces: the pieces' sums in order (no atomics).
+// Adapters without rows get zeros; those of one piece were written whole. 16 adapters, 64 x
+// (4096 + 14336) each, 8.8 us.
 template <class T>
 __global__ __launch_bounds__(256) void outer_join_kernel(OuterArgs a) {
     const int ad = blockIdx.y;
