@@ -416,7 +416,7 @@ twq_status twq_fold_lowrank(const double *w, const double *u, const double *s, c
  *                                           ranks are padded with zeros.
  *   scale f32 [count]                       c_a, or NULL (1)
  * Shapes: as above, n and r positive, n at most 2^22, count 0..4096, and
- * (b / 64 + min(b, count + 1)) ((m + n) / 128 + 2) below 2^24. Non-finite values in rows
+ * (b / 64 + count + 1) ((m + n) / 128 + 2) below 2^24. Non-finite values in rows
  * without an adapter are not read; elsewhere they make the row (or the adapter's gradient)
  * non-finite.
  */

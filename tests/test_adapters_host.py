@@ -90,7 +90,7 @@ def test_workspaces_and_plan_sizes():
 
 
 def test_refused_launch_sizes():
-    """(b / 64 + min(b, count + 1)) ((m + n) / 128 + 2) stays below 2^24."""
+    """(b / 64 + count + 1) ((m + n) / 128 + 2) stays below 2^24."""
     L = twq.lib()
     n = 128 * (2 ** 24 // 4161 - 2) // 16 * 16 - 256  # 4096 rows of 4096 adapters: 4160 tiles
     assert L.twq_adapters_workspace_bytes(4096, 256, n, 16, 4096) > 0

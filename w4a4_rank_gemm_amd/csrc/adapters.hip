@@ -29,7 +29,7 @@ constexpr int kPlanThreads = 1024;
 __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_t *index, int64_t b, int count, uint8_t *plan,
                                                            PlanLayout L, int chunk, int trows) {
     __shared__ int hist[kMaxAdapters + 1];
-    __shared__ int red[7][kPlanThreads / kWave];
+    __shared__ int red[9][kPlanThreads / kWave];
     __shared__ int wsum[kPlanThreads / kWave];
     const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
     const int a = blockIdx.x;
@@ -42,9 +42,10 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_
     __syncthreads();
     const int rows = hist[a], rest = rows % chunk;
     // Rows, tiles, whole pieces and partial-sum slots before adapter a; all whole pieces; the
-    // shorter pieces before a's; all shorter pieces. Pieces lie longest first, so that no long
-    // one starts last.
-    int s[7] = {0, 0, 0, 0, 0, 0, 0};
+    // shorter pieces before a's; all shorter pieces; the adapters without rows before a; all of
+    // those. Pieces lie longest first, so that no long one starts last; an adapter without rows
+    // has one of no rows, for its zeros.
+    int s[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};
     for (int k = tid; k <= count; k += kPlanThreads) {
         const int c = hist[k];
         if (k < a) {
@@ -58,16 +59,18 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_
             const int other = c % chunk;
             s[5] += other > rest || (other == rest && k < a);
             s[6] += other > 0;
+            s[7] += c == 0 && k < a;
+            s[8] += c == 0;
         }
     }
 #pragma unroll
-    for (int q = 0; q < 7; ++q) {
+    for (int q = 0; q < 9; ++q) {
         for (int off = 32; off > 0; off >>= 1) s[q] += __shfl_xor(s[q], off, kWave);
         if (lane == 0) red[q][wave] = s[q];
     }
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 7; ++q) {
+    for (int q = 0; q < 9; ++q) {
         s[q] = 0;
         for (int w = 0; w < kPlanThreads / kWave; ++w) s[q] += red[q][w];
     }
@@ -81,7 +84,7 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_
         if (a == count) {
             offsets[count + 1] = s[0] + rows;
             head[0] = s[1] + ntiles;
-            head[1] = s[4] + s[6];
+            head[1] = s[4] + s[6] + s[8];
         }
     }
     for (int j = tid; j < ntiles; j += kPlanThreads) {
@@ -94,7 +97,10 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_
             chunks[left < chunk ? s[4] + s[5] : s[2] + j] =
                 PlanItem{a, s[0] + j * chunk, left < chunk ? left : chunk, nparts > 1 ? s[3] + j : -1};
         }
-    if (rows == 0) return;
+    if (rows == 0) {
+        if (a < count && tid == 0) chunks[s[4] + s[6] + s[7]] = PlanItem{a, s[0], 0, -1};
+        return;
+    }
     int pos = s[0];
     for (int64_t i0 = 0; i0 < b; i0 += kPlanThreads) {
         const int64_t i = i0 + tid;

@@ -24,8 +24,7 @@ bool valid_shape(int64_t b, int64_t m, int64_t n, int64_t r) {
 // The largest launches: a tile's 256-column blocks, a piece's 128-column blocks. A grid
 // dimension holds fewer than 2^32 threads, 2^24 CTAs of 256.
 bool valid_grid(int64_t b, int64_t m, int64_t n, int64_t count) {
-    const int64_t groups = count + 1 < b ? count + 1 : b;
-    return (b / 64 + groups) * ((m + n) / 128 + 2) < int64_t(1) << 24;
+    return (b / 64 + count + 1) * ((m + n) / 128 + 2) < int64_t(1) << 24;
 }
 
 twq_status done(hipError_t e, const char *name) { return e == hipSuccess ? TWQ_OK : (twq_status)hip_error(e, name); }

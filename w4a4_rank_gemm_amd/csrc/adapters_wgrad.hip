@@ -201,7 +201,7 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a) {
     const int64_t piece = blockIdx.x / ct;
     if (piece >= a.plan.head[1]) return;
     const PlanItem it = a.plan.chunks[piece];
-    {
+    if (it.rows > 0) {
         int in[kMaxChunk / 256];
 #pragma unroll
         for (int j = 0; j < kMaxChunk / 256; ++j) {
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a) {
     if (tile >= nt) {
         v4f acc[kBlocks][RB] = {};
         const int col0 = (tile - nt) * kCols;
-        outer_piece<RB, XS, false>(a, it, col0, rank0, rows, smem, acc);
+        if (it.rows > 0) outer_piece<RB, XS, false>(a, it, col0, rank0, rows, smem, acc);
         uint16_t *const out = a.dat + (int64_t)it.adapter * a.r * a.m;
 #pragma unroll
         for (int c = 0; c < RB; ++c) {
@@ -233,7 +233,7 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a) {
     } else {
         v4f acc[kBlocks][RB] = {};
         const int col0 = tile * kCols;
-        outer_piece<RB, ZS, true>(a, it, col0, rank0, rows, smem, acc);
+        if (it.rows > 0) outer_piece<RB, ZS, true>(a, it, col0, rank0, rows, smem, acc);
         uint16_t *const out = a.dbt + (int64_t)it.adapter * a.r * a.n;
         float *const bp = part ? part + (int64_t)a.r * a.m : nullptr;
 #pragma unroll
@@ -250,17 +250,15 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a) {
 }
 
 // Gradients of adapters whose rows were several pieces: the pieces' sums in order (no atomics).
-// Adapters without rows get zeros; those of one piece were written whole. 16 adapters, 64 x
-// (4096 + 14336) each, 8.8 us.
+// The others were written whole. 16 adapters, 64 x (4096 + 14336) each, 8.8 us.
 template <class T>
 __global__ __launch_bounds__(256) void outer_join_kernel(OuterArgs a) {
     const int ad = blockIdx.y;
     const int rows = a.plan.offsets[ad + 1] - a.plan.offsets[ad], parts = (rows + a.chunk - 1) / a.chunk;
-    if (parts == 1) return;
+    if (parts < 2) return;
     const int64_t per = (int64_t)a.r * (a.m + a.n), e4 = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (e4 * 4 >= per) return;
-    v4f s = {0.f, 0.f, 0.f, 0.f};
-    if (parts > 1) s = sum_slices(a.part + (int64_t)a.plan.slot0[ad] * per + e4 * 4, per, parts);
+    const v4f s = sum_slices(a.part + (int64_t)a.plan.slot0[ad] * per + e4 * 4, per, parts);
     const int64_t at = e4 * 4, na = (int64_t)a.r * a.m;
     if (at < na)
         outer_put<T>(a, a.dat + ad * na, nullptr, at, s);
@@ -270,21 +268,18 @@ __global__ __launch_bounds__(256) void outer_join_kernel(OuterArgs a) {
 
 template <class T, bool CODES>
 static hipError_t outer_ranks(const OuterArgs &a, hipStream_t stream) {
-    if (a.chunks > 0) {
-        const int rb = a.r <= 16 ? 1 : a.r <= 32 ? 2 : a.r <= 64 ? 4 : 8;
-        const dim3 grid((unsigned)(a.chunks * (a.m / kCols + (a.n + kCols - 1) / kCols)),
-                        (unsigned)((a.r + 16 * rb - 1) / (16 * rb)));
-        if (rb == 1)
-            outer_kernel<T, 1, CODES><<<grid, 256, 0, stream>>>(a);
-        else if (rb == 2)
-            outer_kernel<T, 2, CODES><<<grid, 256, 0, stream>>>(a);
-        else if (rb == 4)
-            outer_kernel<T, 4, CODES><<<grid, 256, 0, stream>>>(a);
-        else
-            outer_kernel<T, 8, CODES><<<grid, 256, 0, stream>>>(a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
+    const int rb = a.r <= 16 ? 1 : a.r <= 32 ? 2 : a.r <= 64 ? 4 : 8;
+    const dim3 grid((unsigned)(a.chunks * (a.m / kCols + (a.n + kCols - 1) / kCols)), (unsigned)((a.r + 16 * rb - 1) / (16 * rb)));
+    if (rb == 1)
+        outer_kernel<T, 1, CODES><<<grid, 256, 0, stream>>>(a);
+    else if (rb == 2)
+        outer_kernel<T, 2, CODES><<<grid, 256, 0, stream>>>(a);
+    else if (rb == 4)
+        outer_kernel<T, 4, CODES><<<grid, 256, 0, stream>>>(a);
+    else
+        outer_kernel<T, 8, CODES><<<grid, 256, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.b <= a.chunk) return e;  // no adapter has two pieces
     const int64_t per4 = (int64_t)a.r * (a.m + a.n) / 4;
     outer_join_kernel<T><<<dim3((unsigned)((per4 + 255) / 256), (unsigned)a.count), 256, 0, stream>>>(a);
     return hipGetLastError();

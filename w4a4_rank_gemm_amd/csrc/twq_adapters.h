@@ -28,8 +28,8 @@ constexpr int64_t kMaxAdapters = 4096;
 constexpr int kMaxChunk = 2048;
 inline int chunk_rows(int64_t b) { return b >= 8192 ? kMaxChunk : b >= 2048 ? 1024 : 512; }
 
-// One tile or piece: adapter (-1: the rows without one), first position in `order`, rows,
-// and for a piece the slot of its partial sums (-1: the only piece of its adapter, which
+// One tile or piece: adapter (-1: the rows without one), first position in `order`, rows (a
+// piece of none: the adapter has none), and for a piece the slot of its partial sums (-1: the only piece of its adapter, which
 // needs none).
 struct PlanItem {
     int32_t adapter, first, rows, slot;
@@ -53,7 +53,7 @@ inline PlanLayout plan_layout(int64_t b, int64_t count) {
     PlanLayout L{};
     // sum over adapters of ceil(n_a / T) <= b / T + the number of adapters with tokens
     L.max_tiles = b / tile_rows(b) + (count + 1 < b ? count + 1 : b);
-    L.max_chunks = b / chunk_rows(b) + (count < b ? count : b);
+    L.max_chunks = b / chunk_rows(b) + count;
     // adapters of several pieces only: ceil(n / T) < 2 n / T for n > T
     L.max_slots = 2 * b / chunk_rows(b);
     L.head = 0;
