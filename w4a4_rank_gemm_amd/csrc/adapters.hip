@@ -432,8 +432,7 @@ __device__ __forceinline__ float split_row(const ExpandArgs &a, int64_t pos, int
     float f = 1.f, undo = 1.f;
     if constexpr (!T::kBf16) {
         for (int off = TPR / 2; off > 0; off >>= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, off, kWave));
-        int e = exponent_or_zero(mx);
-        e = e < -100 ? -100 : e;  // 13 - e <= 113, inside the range of pow2
+        const int e = scale_exponent(mx);
         if (mx > 0.f && mx < __builtin_inff()) f = pow2(13 - e), undo = pow2(e - 13);
     }
     for (int c = q * 8; c < a.r; c += TPR * 8) {

@@ -8,8 +8,10 @@
 // transposed as nibbles: a lane gets 16 channels of one input column in 8 bytes, which are
 // expanded to fp16 in registers. Codes are exact in fp16; the per-channel scale is folded
 // into dY by a first kernel, G[i][j] = fp16(dY[i][j] s_W[j] 2^-e_i) with a power of two per
-// token that brings the row's largest element to [2^14, 2^15): one rounding, and no
-// gradient too small or too large for fp16. In an fp16 dX that rounding weighs as much as the
+// token that brings the row's largest element to [2^14, 2^15) (from 2^-112 up; a smaller row is
+// scaled by 2^126): one rounding, and no gradient too small or too large for fp16. Elements below
+// 2^-28 of the row's largest are subnormal there and off by up to 2^-39 of the largest; a T
+// below 2^-40 of G is off by up to 2^-79 of G's largest. In an fp16 dX that rounding weighs as much as the
 // output's own (the 2-norm off by 2.9e-4 instead of 2.1e-4 where the low-rank part is small), in
 // a bf16 one nothing; a second part of G would double the matrix work. T = dY L2 (the adapters' shrink kernel) is held
 // in binary32, then in two fp16 parts, and joins the same accumulator after the long sum.
@@ -71,8 +73,7 @@ constexpr int kScaleRows = 16, kScaleCols = 2048;
 // (b=16, 4096 x 14336, 16 slices here and in t_parts: 37 to 29 us for the whole call).
 __device__ __forceinline__ int g_exponent(const DxArgs &a, int64_t row, int q) {
     const uint32_t m = __builtin_bit_cast(uint32_t, a.rowmax[(q < a.rks ? q : a.rks - 1) * a.b + row]);
-    const int e = exponent_or_zero(__builtin_bit_cast(float, row16_max(m)));  // magnitudes: ordered as integers, NaN last
-    return e < -100 ? -100 : e;
+    return scale_exponent(__builtin_bit_cast(float, row16_max(m)));  // magnitudes: ordered as integers, NaN last
 }
 
 // T = dY L2 of 16 rows, 16 threads a row: the slices' sum, its largest magnitude, two fp16 parts.
@@ -97,10 +98,10 @@ __device__ __forceinline__ void t_parts(const DxArgs &a, int64_t row0, int nrows
     for (int u = 0; u < 16; ++u) mx = __builtin_fmaxf(mx, __builtin_fabsf(t[u]));
     for (int off = 8; off > 0; off >>= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, off, kWave));
     const int ge = g_exponent(a, row, q);
-    // the two exponents meet in one accumulator: far apart, T keeps fewer bits
-    int te = mx > 0.f ? exponent_or_zero(mx) : ge;
+    // the two exponents meet in one accumulator: far below G, T keeps fewer bits (a G of zeros has
+    // the least exponent, and T its own)
+    int te = mx > 0.f ? scale_exponent(mx) : ge;
     te = te < ge - 40 ? ge - 40 : te;
-    te = te < -100 ? -100 : te;
     if (i >= nrows) return;
 #pragma unroll
     for (int u = 0; u < 16; ++u)

@@ -96,11 +96,12 @@ __device__ __forceinline__ int64_t xcd_range(int64_t b, int64_t ctas) {
 // Power of two 2^e, e in [-126, 127].
 __device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
 
-// Exponent e with 2^e <= v < 2^(e + 1) for a positive normal v; 0 for 0 (and for
-// subnormals, infinities and NaN, which then pass unscaled).
-__device__ __forceinline__ int exponent_or_zero(float v) {
+// Exponent by which a row with the largest magnitude v is scaled: e with 2^e <= v < 2^(e + 1),
+// at least -112, so that 2^(14 - e) and 2^(e - 14) lie in the range of pow2 (subnormals and 0 are
+// scaled by 2^126 too); 0 for infinities and NaN, which pass unscaled.
+__device__ __forceinline__ int scale_exponent(float v) {
     const int e = (int)((__builtin_bit_cast(uint32_t, v) >> 23) & 0xFFu);
-    return e == 0 || e == 255 ? 0 : e - 127;
+    return e == 255 ? 0 : e < 15 ? -112 : e - 127;
 }
 
 // Maximum over the 16 lanes of a row of lanes, in every one of them.
