@@ -4,7 +4,7 @@ import shutil
 
 import pytest
 
-from tests import plan_rules, test_gpu_dx_kernels
+from tests import plan_rules, test_gpu_adapters_many, test_gpu_dx_kernels
 
 pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="g++ is not installed")
 
@@ -31,3 +31,18 @@ def test_input_gradient_variants(rules):
     grid = [(b, m, n, r) for b in (1, 16, 60, 65, 128, 200, 500, 1000, 2048, 2049, 4096, 8192, 40000)
             for m in (128, 512, 1152, 4096, 8192, 28672) for n in (16, 512, 1040, 4096, 14336, 65536) for r in (0, 64)]
     assert {(bt, kg, ks > 1) for bt, kg, ks, *_ in plan_rules.ask(rules, [("dx", *c) for c in grid])} == set(tiles)
+
+
+def test_adapter_variants(rules):
+    shapes = test_gpu_adapters_many.SHAPES
+    got = plan_rules.ask(rules, [("rows", b) for b, *_ in shapes])
+    # rows of a tile with the ranks' matrix blocks, in the first product (powers of two up to 64, or 128
+    # with the largest tiles) and in the second (up to 256)
+    first = {(t, next(k for k in (16, 32, 64, 128) if r <= k or k == (128 if t == 128 else 64)))
+             for (t, _), (_, _, _, r, *_) in zip(got, shapes)}
+    assert first == {(t, k) for t in (16, 64, 128) for k in (16, 32, 64, 128) if k < 128 or t == 128}
+    second = {(t, next(k for k in (32, 64, 128, 256) if r <= k)) for (t, _), (_, _, _, r, *_) in zip(got, shapes)}
+    assert second == {(t, k) for t in (16, 64, 128) for k in (32, 64, 128, 256)}
+    # an adapter of several weight-gradient pieces, at each length of a piece
+    assert {c for (_, c), (b, _, _, _, count, kind) in zip(got, shapes) if kind in ("one", "runs") and b > count * c} == \
+        {512, 1024, 2048}
