@@ -621,6 +621,8 @@ def _type(t, name: str) -> int:
         raise TypeError(f"{name} must be torch.float16 or torch.bfloat16 (got {t.dtype})")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU (got {t.device})")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims (got {tuple(t.shape)})")
     return TYPES[t.dtype]
 
 
@@ -697,8 +699,9 @@ def _adapter_shapes(at, bt, plan: AdapterPlan, scale, b: int, dtype: torch.dtype
         raise TypeError("plan must come from adapter_plan")
     if plan.b != b or plan.data.get_device() != gpu:
         raise ValueError(f"plan is for {plan.b} rows on {plan.data.device}, not {b} on GPU {gpu}")
-    if at.dim() != 3 or bt.dim() != 3:
-        raise ValueError(f"at and bt must have 3 dims (got {tuple(at.shape)}, {tuple(bt.shape)})")
+    for t, name in ((at, "at"), (bt, "bt")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            _need(t, name, dtype, 3)
     _, r, m = at.shape
     n = bt.shape[1]
     _want(at, "at", dtype, (plan.count, r, m), gpu)
@@ -714,7 +717,8 @@ def adapters(x: torch.Tensor, at: torch.Tensor, bt: torch.Tensor, plan: AdapterP
     the plan; out[i] = y[i] without one.
 
     x [b][m], y [b][n] (None: zeros), at [count][r][m], bt [count][n][r]: all fp16 or all bf16.
-    out may be y. keep_h: also returns x at^T, f32 [b][r], which adapters_grad needs."""
+    out may be y. keep_h: also returns x at^T, f32 [b][r], which adapters_grad needs. As with every
+    call here no autograd graph is recorded: the gradients are adapters_grad's and linear_dx's."""
     ty = _type(x, "x")
     dt, gpu, b = x.dtype, x.get_device(), x.shape[0]
     m, n, r = _adapter_shapes(at, bt, plan, scale, b, dt, gpu)
