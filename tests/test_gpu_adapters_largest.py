@@ -59,3 +59,55 @@ def test_every_adapter_and_many_rows():
     want[:, 0], want[:, 1] = (idx % 64).half(), (idx // 64).half()
     want[idx < 0] = 0
     assert torch.equal(out, want)
+
+
+WIDE = 1 << 22  # the largest n
+
+
+def _columns(g):
+    """Some columns of WIDE, the last among them."""
+    cols = torch.randint(0, WIDE, (1000,), generator=g, device="cuda")
+    cols[:24] = torch.arange(WIDE - 24, WIDE, device="cuda")
+    return cols.unique()
+
+
+@pytest.mark.parametrize("b", [40, 300])
+def test_widest_adapters(b):
+    m, r, count = 128, 16, 2
+    _say(f"adapters b={b} m={m} n={WIDE} r={r}")
+    g = _gen(27)
+    idx = torch.randint(-1, count, (b,), generator=g, device="cuda").to(torch.int32)
+    x = torch.randn(b, m, generator=g, device="cuda").half()
+    at = (torch.randn(count, r, m, generator=g, device="cuda") / m ** 0.5).half()
+    bt = torch.randn(count, WIDE, r, generator=g, device="cuda", dtype=torch.float16)
+    y = torch.randn(b, WIDE, generator=g, device="cuda", dtype=torch.float16)
+    cols = _columns(g)
+    plan = twq.adapter_plan(idx, count)
+    out, h = twq.adapters(x, at, bt, plan, y, keep_h=True)
+    ref.check(out[:, cols], ref.adapters(x, at, bt[:, cols], idx, y[:, cols], None)[0], "out")
+    del out, y
+    dy = torch.zeros(b, WIDE, dtype=torch.float16, device="cuda")
+    dy[:, cols] = torch.randn(b, len(cols), generator=g, device="cuda").half() * 2.0 ** -6
+    dat, dbt, dx = twq.adapters_grad(dy, x, h, at, bt, plan)
+    wants = ref.adapters_grad(dy[:, cols], x.double(), h, at, bt[:, cols], idx, None, None)
+    for name, o, w in zip(("dat", "dbt", "dx"), (dat, dbt[:, cols], dx), wants):
+        ref.check(o, w, name)
+    assert int(dbt.count_nonzero()) == int(dbt[:, cols].count_nonzero())
+
+
+@pytest.mark.parametrize("b,r", [(20, 16), (200, 0), (200, 32)])
+def test_widest_input_gradient(b, r):
+    m = 128
+    _say(f"linear_dx b={b} m={m} n={WIDE} r={r}")
+    g = _gen(28)
+    qw, sw = twq.pack_weight(torch.randn(WIDE, m, generator=g, device="cuda"))
+    rows = qw.view(WIDE // 16, 1, 16, 64).reshape(WIDE, m // 2)
+    l1t = torch.randn(r, m, generator=g, device="cuda").half() if r else None
+    l2t = torch.randn(WIDE, r, generator=g, device="cuda", dtype=torch.float16) if r else None
+    cols = _columns(g)
+    dy = torch.zeros(b, WIDE, dtype=torch.float16, device="cuda")
+    dy[:, cols] = torch.randn(b, len(cols), generator=g, device="cuda").half() * 2.0 ** -6
+    codes = torch.stack((rows[cols] & 15, rows[cols] >> 4), dim=2).view(len(cols), m).to(torch.int16)
+    codes = torch.where(codes > 7, codes - 16, codes)
+    got = twq.linear_dx(dy, qw, sw, l1t, l2t)
+    ref.check(got, ref.linear_dx(dy[:, cols], codes, sw[cols], l1t, l2t[cols] if r else None), "dx")
