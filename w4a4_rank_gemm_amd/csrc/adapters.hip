@@ -24,8 +24,9 @@ constexpr int kPlanThreads = 1024;
 // CTA a owns adapter a (CTA `count`: the rows without one). It counts every adapter's
 // rows, from which its own first position, first tile and first piece follow, then
 // scans the index again and writes its rows in token order. Every CTA repeats the count, so that
-// one launch does without a sum across CTAs; bound by the second scan's steps of 1024 rows
-// (one row 6 us, 4096 rows of 6 adapters 14, 8192 of 16 21; made once for all layers of a batch).
+// one launch does without a sum across CTAs; bound by the second scan's steps of 1024 rows, one
+// after the other (one row 6 us, 4096 rows of 6 adapters 12-14, 8192 of 16 16-21; 2^20 of 16 1.25 ms,
+// 2^24 of 3 21 ms, of 256 32 ms; made once for all layers of a batch).
 __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_t *index, int64_t b, int count, uint8_t *plan,
                                                            PlanLayout L, int chunk, int trows) {
     __shared__ int hist[kMaxAdapters + 1];
@@ -167,9 +168,11 @@ __device__ __forceinline__ Tile tile_of(const PlanView &p, int64_t t, int64_t b)
 // or 128 rows (NG = 4, 8) a wave owns 16 rows; with 16 (NG = 1) a quarter of each stage, and the
 // waves' sums are added in wave order. More rows read the weights less often, and all ranks up to
 // 128 in one pass the rows once.
-// Bound by the read of V: 4096 x 14336, 64 ranks, 31 us (3.8 TB/s of X; a 1 GiB copy moves 5.1);
-// 8192 x 14336 by 64 ranks 66 us (3.6), by 16 ranks 52 us (4.5); 32 rows of 32 adapters,
-// 8192 x 64 each, 9.4 us (3.6 TB/s of weights).
+// Bound by the read of V with few ranks, with more of them by LDS as well: every wave reads a stage's
+// whole weights from LDS for its 16 rows. 8192 x 14336 by 16, 32, 64 and 128 ranks takes 55, 59, 66 and
+// 87 us (4.3 to 2.7 TB/s of V; a 1 GiB copy moves 5.1), LDS active in 25, 32, 42 and 56% of the
+// compute units' busy cycles, 34 to 40% of that bank conflicts. 4096 x 14336, 64 ranks, 31 us; 32
+// rows of 32 adapters, 8192 x 64 each, 9.4 us (3.6 TB/s of weights).
 // KMAJOR weights ([k][r], ranks contiguous) are read back from LDS transposed. DX (the frozen
 // layer's input gradient): fp16 weights whatever the rows, split exactly into two bf16 parts
 // for bf16 rows; and the rows' largest |v sw| on the way.
@@ -737,7 +740,7 @@ static hipError_t expand_launch(const ExpandArgs &a, hipStream_t stream) {
     }
     // Runs a CTA: as many as leave the CTAs all resident at once (the registers allow 4, 3, 2
     // or 1 a compute unit). 32 tiles of 28672 columns, 64 ranks: 1, 2, 4, 5 and 8 runs took 36, 32,
-    // 33, 27 and 29 us.
+    // 33, 27 and 29 us (the one shape measured).
     constexpr int resident = 256 * (KS == 1 ? 4 : KS == 2 ? 3 : KS == 4 ? 2 : 1);
     const int64_t runs = (a.n + 255) / 256, blocks64 = (a.tiles * runs + resident - 1) / resident;
     const int blocks = (int)(blocks64 < runs ? blocks64 : runs);

@@ -8,9 +8,11 @@
 // both gradients are one launch. Each element of X and dY is read once (up to 128 ranks); X may
 // come as an 8-bit checkpoint, whose codes are made bf16 in registers.
 //
-// Bound by memory: 8192 rows, 4096 (codes) + 14336 columns, 64 ranks 71 us (268 MB of rows, 3.8
-// TB/s; 305 MB with the factors' repeated reads); 2048 rows, 32 ranks 19 us. Wider tiles read the
-// factor less often but are fewer: 256 and 512 columns a CTA were equal to 45% slower.
+// Bound by memory up to about 32 ranks, then by LDS and the matrix cores as well: 8192 rows, 4096
+// (codes) + 14336 columns with 16, 32, 64 and 128 ranks take 52, 55, 73 and 133 us (268 MB of rows:
+// 5.1 to 2.0 TB/s), LDS active in 38 to 53% of the compute units' busy cycles, a third of that bank
+// conflicts, matrix cores in 11, 21, 29 and 31%. 2048 rows, 32 ranks 18-21 us. Wider tiles read the factor
+// less often but are fewer: 256 and 512 columns a CTA were equal to 45% slower.
 //
 // The binary32 factor, c_a G or c_a H, comes as two bf16 parts, 16 significant bits together
 // (expand's planes); with a checkpoint c_a G still takes the group's scale of the token and is

@@ -3,8 +3,9 @@
 // Per token row and group of 128 elements: s = fl32(max|x| / 127), q = round-half-even
 // (fl32(x / s)); the restored value is s q. It is eq. (1) with k = 8 on groups: an outlier
 // channel coarsens its own group only. Both kernels read and write each byte once and are
-// bound by memory: 8192 x 14336 takes 85-97 us to keep (357 MB, 3.7-4.2 TB/s) and 56 us to
-// restore (6.4 TB/s, part of it from the last-level cache).
+// bound by memory: 8192 x 14336 takes 82-103 us to keep (357 MB, 3.5-4.4 TB/s) and to restore 56-58 us
+// right after (6.3 TB/s, part of it from the last-level cache), 55-64, median 62 (5.8), when five other
+// such tensors were kept in between.
 #include "twq_adapters.h"
 #include "twq_adapters_device.h"
 

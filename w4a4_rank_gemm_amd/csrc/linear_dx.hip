@@ -6,17 +6,18 @@
 // The long sum runs over the output channels j, the slow axis of the packed weight. Packed
 // 4-bit codes go to LDS as they lie (a 16-channel panel piece is 16 rows of K) and are read
 // transposed as nibbles: a lane gets 16 channels of one input column in 8 bytes, which are
-// expanded to fp16 in registers. Codes are exact in fp16; the per-channel scale is folded
-// into dY by a first kernel, G[i][j] = fp16(dY[i][j] s_W[j] 2^-e_i) with a power of two per
-// token that brings the row's largest element to [2^14, 2^15) (from 2^-112 up; a smaller row is
-// scaled by 2^126): one rounding, and no gradient too small or too large for fp16. Elements below
-// 2^-28 of the row's largest are subnormal there and off by up to 2^-39 of the largest; a T
-// below 2^-40 of G is off by up to 2^-79 of G's largest. In an fp16 dX that rounding weighs as much as the
-// output's own (the 2-norm off by 2.9e-4 instead of 2.1e-4 where the low-rank part is small), in
-// a bf16 one nothing; a second part of G would double the matrix work. T = dY L2 (the adapters' shrink kernel) is held
-// in binary32, then in two fp16 parts, and joins the same accumulator after the long sum.
-// Together: 4096 tokens, 8192 x 28672, 128 ranks 1.69 ms (1963 GFLOP, 1.16 PFLOP/s; a library
-// fp16 product of 8192^3 runs at 1.33); 2048 tokens, 4096 x 14336, 32 ranks 242 us.
+// expanded to fp16 in registers. Codes are exact in fp16; the per-channel scale is folded into dY by a
+// first kernel, G[i][j] = fp16(dY[i][j] s_W[j] 2^-e_i) with a power of two per token that brings the
+// row's largest element to [2^14, 2^15) (from 2^-112 up; a smaller row is scaled by 2^126): one
+// rounding, and no gradient too small or too large for fp16. Elements below 2^-28 of the row's largest
+// are subnormal there and off by up to 2^-39 of the largest; a T below 2^-40 of G is off by up to
+// 2^-79 of G's largest. In an fp16 dX that rounding weighs as much as the output's own (the 2-norm off
+// by 2.9e-4 instead of 2.1e-4 where the low-rank part is small), in a bf16 one nothing. It is the
+// error of a weight dequantized to fp16 (code times scale rounded to 11 bits); a second part of G
+// would double the matrix work. T = dY L2 (the adapters' shrink kernel) is held in binary32, then in
+// two fp16 parts, and joins the same accumulator after the long sum.
+// Together: 4096 tokens, 8192 x 28672, 128 ranks 1.67-1.76 ms (1963 GFLOP, 1.1-1.2
+// PFLOP/s; a library fp16 product of 8192^3 runs at 1.33); 2048 tokens, 4096 x 14336, 32 ranks 242-254 us.
 #include <utility>
 
 #include "twq_adapters.h"
@@ -330,9 +331,10 @@ __device__ __forceinline__ void dx_finish(const DxArgs &a, v16f (&acc)[2][TB], u
 // (row / 16) % 2 (one 16-byte read serves lanes 0-7 with 16-23 in a pass), code rows 64 bytes
 // with the chunk XORed by (row / 4) % 4. No bank conflicts to speak of (0.6% of LDS cycles).
 //
-// Bound by the matrix cores and the expansion of the codes, whose cycles add up: 4096 tokens,
-// 8192 x 28672: 1.60 ms, matrix cores busy 1.85 of 2.82 million cycles. 2048 tokens, 4096 x
-// 14336: 205-220 us.
+// Bound by the matrix cores and the expansion of the codes, whose cycles add up (a wave waits for
+// its LDS reads before its matrix instructions, with two waves a SIMD to fill in): 4096 tokens, 8192 x
+// 28672: 1.54-1.70 ms, matrix cores busy 1.85 of the kernel's 2.80 million cycles, 0.70 of those in which
+// their compute unit is. 2048 tokens, 4096 x 14336: 207-262 us, medians of runs 210 to 250; 0.60.
 //
 // KG = 2: eight waves in two groups, each with its own ring and half of the channels; their
 // sums meet in LDS. That fills a compute unit with one CTA where the tiles are too few for two,
