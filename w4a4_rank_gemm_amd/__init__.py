@@ -180,13 +180,17 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int):
 
 
 # One workspace per (device, stream): calls sharing a workspace must not overlap,
-# and calls enqueued on one stream never do. New workspaces start zeroed.
+# and eager calls enqueued on one stream never do. New workspaces start zeroed.
+# Captured calls take theirs from their graph's memory: a graph may be replayed on any
+# stream, and after the workspace of its capture stream was replaced by a larger one.
 _workspaces: dict = {}
 
 
 def _workspace(dev: torch.device, nbytes: int):
     if nbytes == 0:
         return None, 0
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
     key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
