@@ -480,7 +480,8 @@ twq_status twq_restore_act(const void *qc, const float *sc, int64_t b, int64_t m
  *   qw, sw from twq_pack_weight;  l1t, l2t fp16 as for twq_linear (NULL iff r == 0)
  *   workspace: at least twq_linear_dx_workspace_bytes(b, m, n, r) bytes, rules as above
  * dY s_W is rounded once to 11 bits for the matrix cores (elements below 2^-28 of their row's
- * largest: to steps of 2^-38 of it); sums are binary32. n is positive and at most 2^22. A non-finite element of dY makes its row of dX non-finite.
+ * largest: to steps of 2^-38 of it); sums are binary32. n is positive and at most 2^22. A
+ * non-finite element of dY makes its row of dX non-finite.
  */
 size_t twq_linear_dx_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r);
 twq_status twq_linear_dx(const void *dy, const void *qw, const float *sw, const void *l1t, const void *l2t, int64_t r,
