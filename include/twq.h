@@ -488,6 +488,73 @@ twq_status twq_linear_dx(const void *dy, const void *qw, const float *sw, const 
                          void *dx, int64_t b, int64_t m, int64_t n, int type, void *workspace, size_t workspace_bytes,
                          void *stream);
 
+/*
+ * ---- the layer with 16-bit activations (W4A16) ----
+ *
+ * The group-wise packed weight with X unquantized, fp16 or bf16:
+ *
+ *   Y[i][j] = sum_G s_W[G][j] sum_{k in G} X[i][k] Q_W[j][k] + sum_t T[i][t] L2[t][j],  T = X L1
+ *
+ * X and the codes enter the products as they are; sums are binary32, T is taken to 16 significant
+ * bits, Y is rounded once. A non-finite element of X makes its row of Y non-finite and no other.
+ *   x     [b][m], y [b][n] (out), both of `type`
+ *   qw, sw from twq_pack_weight_grouped;  l1t fp16 [r][m], l2t fp16 [n][r] (NULL iff r == 0)
+ *   workspace: at least twq_linear_a16_workspace_bytes(b, m, n, r, g) bytes (0 where r == 0 and b
+ *   is small: NULL is then allowed), rules as above
+ * g must be 128 (TWQ_ERR_UNSUPPORTED otherwise); n at most 2^22.
+ */
+size_t twq_linear_a16_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r, int64_t g);
+twq_status twq_linear_a16(const void *x, const void *qw, const float *sw, const void *l1t, const void *l2t, int64_t r,
+                          void *y, int64_t b, int64_t m, int64_t n, int64_t g, int type, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * ---- a routed layer (mixture of experts) of packed 4-bit experts, for a few tokens ----
+ *
+ * For each token i of at most 256, with experts e = e(i, j), j < k:
+ *
+ *   y_i = sum_j w_ij D_e (silu(G_e x_i) * (U_e x_i)),   silu(v) = v / (1 + exp(-v))
+ *
+ * G_e, U_e [f][m] and D_e [m][f] are packed by twq_pack_weight_grouped: q1, s1 from the array of
+ * all experts' [2 f][m] (f rows of G_e, then f of U_e) as one matrix of experts 2 f rows, q2, s2
+ * from that of all experts' [m][f] as one of experts m rows. X, Y fp16 or bf16 (`type`).
+ * Sums are binary32, the inner rows are taken to 16 significant bits, Y is rounded once. Every sum has a fixed
+ * order: equal calls give equal bits. A non-finite element of x_i makes y_i non-finite and no other row.
+ * m, f: multiples of 128 up to 131072. experts: 1..512, k: 1..16, experts 2 f and experts m at
+ * most 2^24. b == 0 is a valid empty call; more than 256 tokens are TWQ_ERR_SHAPE.
+ */
+#define TWQ_SOFTMAX 0
+#define TWQ_SIGMOID 1
+
+/*
+ * The router: logits l = x wr^T (binary64), scores p = softmax(l) over the experts or sigmoid(l)
+ * (`score`). A token's k experts are those with the largest l, or with a bias those with the
+ * largest p + bias; in that order, the lowest index first among equals. Weights are p, divided by
+ * the sum over the chosen if `norm` (all zero where that sum is), times `scale`.
+ *   x [b][m], wr [experts][m] of `type`;  bias f32 [experts] or NULL;  k <= experts
+ *   ids i32 [b][k] (out), weights f32 [b][k] (out)
+ * With non-finite logits the choice is unspecified (ids still name k different experts).
+ */
+size_t twq_moe_route_workspace_bytes(int64_t b, int64_t m, int64_t experts, int64_t k);
+twq_status twq_moe_route(const void *x, const void *wr, const float *bias, int64_t b, int64_t m, int64_t experts, int64_t k,
+                         int score, int norm, float scale, int type, int32_t *ids, float *weights, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * The experts' products for a given choice: ids outside [0, experts) mean none (a token without
+ * any gets zeros), an expert may be named more than once.
+ */
+size_t twq_moe_experts_workspace_bytes(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k);
+twq_status twq_moe_experts(const void *x, const int32_t *ids, const float *weights, const void *q1, const float *s1,
+                           const void *q2, const float *s2, void *y, int64_t b, int64_t m, int64_t f, int64_t experts,
+                           int64_t k, int64_t g, int type, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The whole layer: twq_moe_route, then twq_moe_experts on its choice (Y bitwise the same). */
+size_t twq_moe_workspace_bytes(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k);
+twq_status twq_moe(const void *x, const void *wr, const float *bias, const void *q1, const float *s1, const void *q2,
+                   const float *s2, void *y, int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k, int64_t g,
+                   int score, int norm, float scale, int type, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

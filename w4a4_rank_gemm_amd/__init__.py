@@ -39,7 +39,8 @@ EXPORTS = ("twq_status_string", "twq_last_error_string", "twq_last_hip_error", "
            "twq_linear_noalloc", "twq_fold_workspace_bytes", "twq_fold_lowrank", "twq_adapter_plan_bytes",
            "twq_adapter_plan", "twq_adapters_workspace_bytes", "twq_adapters", "twq_adapters_grad_workspace_bytes",
            "twq_adapters_grad", "twq_checkpoint_act", "twq_restore_act", "twq_linear_dx_workspace_bytes",
-           "twq_linear_dx")
+           "twq_linear_dx", "twq_linear_a16_workspace_bytes", "twq_linear_a16", "twq_moe_route_workspace_bytes",
+           "twq_moe_route", "twq_moe_experts_workspace_bytes", "twq_moe_experts", "twq_moe_workspace_bytes", "twq_moe")
 
 GROUP = 128  # group size of the group-wise entry points
 
@@ -55,7 +56,7 @@ class TwqError(RuntimeError):
 
 _lib = None
 _lock = threading.Lock()
-_P, _I, _S, _T = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+_P, _I, _S, _T, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
 
 
 def lib() -> ctypes.CDLL:
@@ -137,7 +138,9 @@ def lib() -> ctypes.CDLL:
                 L.twq_debug_linear_grouped_main.argtypes = [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _P, _S, _P]
                 for nm, args in (("twq_adapter_plan_bytes", [_I] * 2), ("twq_adapters_workspace_bytes", [_I] * 5),
                                  ("twq_adapters_grad_workspace_bytes", [_I] * 5),
-                                 ("twq_linear_dx_workspace_bytes", [_I] * 4)):
+                                 ("twq_linear_dx_workspace_bytes", [_I] * 4), ("twq_linear_a16_workspace_bytes", [_I] * 5),
+                                 ("twq_moe_route_workspace_bytes", [_I] * 4),
+                                 ("twq_moe_experts_workspace_bytes", [_I] * 5), ("twq_moe_workspace_bytes", [_I] * 5)):
                     getattr(L, nm).restype = _S
                     getattr(L, nm).argtypes = args
                 for nm, args in (("twq_adapter_plan", [_P, _I, _I, _P, _S, _P]),
@@ -145,7 +148,11 @@ def lib() -> ctypes.CDLL:
                                  ("twq_adapters_grad", [_P] * 9 + [_S] + [_P] * 4 + [_I] * 5 + [_T, _P, _S, _P]),
                                  ("twq_checkpoint_act", [_P, _I, _I, _T, _P, _P, _P]),
                                  ("twq_restore_act", [_P, _P, _I, _I, _T, _P, _P]),
-                                 ("twq_linear_dx", [_P] * 5 + [_I, _P, _I, _I, _I, _T, _P, _S, _P])):
+                                 ("twq_linear_dx", [_P] * 5 + [_I, _P, _I, _I, _I, _T, _P, _S, _P]),
+                                 ("twq_linear_a16", [_P] * 5 + [_I, _P, _I, _I, _I, _I, _T, _P, _S, _P]),
+                                 ("twq_moe_route", [_P] * 3 + [_I] * 4 + [_T, _T, _F, _T] + [_P] * 3 + [_S, _P]),
+                                 ("twq_moe_experts", [_P] * 8 + [_I] * 6 + [_T, _P, _S, _P]),
+                                 ("twq_moe", [_P] * 8 + [_I] * 6 + [_T, _T, _F, _T, _P, _S, _P])):
                     getattr(L, nm).restype = ctypes.c_int
                     getattr(L, nm).argtypes = args
                 _lib = L
@@ -838,6 +845,171 @@ def linear_dx(dy: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor, l1t=None, l2
     _launch(gpu, "twq_linear_dx", L.twq_linear_dx, dy.data_ptr(), qw.data_ptr(), sw.data_ptr(), _addr(l1t), _addr(l2t), r,
             out.data_ptr(), b, m, n, ty, _addr(ws), wsb)
     return out
+
+
+# ---- the packed weight with 16-bit activations, and routed layers of packed experts ----
+
+SCORES = {"softmax": 0, "sigmoid": 1}  # TWQ_SOFTMAX, TWQ_SIGMOID
+MOE_TOKENS = 256                       # tokens of one routed call
+
+
+def linear_a16(x: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor, l1t=None, l2t=None,
+               out: torch.Tensor | None = None, g: int = GROUP) -> torch.Tensor:
+    """The group-wise layer with unquantized activations (W4A16): Y [b][n] = X (s_W Q_W)^T +
+    (X L1) L2, with the packed weight of pack_weight_grouped and the fp16 pair of linear; X and Y
+    fp16 or bf16."""
+    ty = _type(x, "x")
+    _need(qw, "qw", torch.uint8, 2)
+    dt, gpu = x.dtype, x.get_device()
+    (b, m), n = x.shape, qw.shape[0]
+    _want(x, "x", dt, (b, m), gpu)
+    _want(qw, "qw", torch.uint8, (n, m // 2), gpu)
+    _want(sw, "sw", torch.float32, (m // g, n), gpu)
+    r = 0
+    if l1t is not None or l2t is not None:
+        _need(l1t, "l1t", torch.float16, 2)
+        r = l1t.shape[0]
+        _want(l1t, "l1t", torch.float16, (r, m), gpu)
+        _want(l2t, "l2t", torch.float16, (n, r), gpu)
+    if out is None:
+        out = x.new_empty((b, n))
+    else:
+        _want(out, "out", dt, (b, n), gpu)
+        _apart(out, "out", x, qw, sw, l1t, l2t)
+    L = lib()
+    wsb = _sizes("twq_linear_a16_workspace_bytes", b, m, n, r, g)
+    ws = _scratch(x, wsb)
+    _launch(gpu, "twq_linear_a16", L.twq_linear_a16, x.data_ptr(), qw.data_ptr(), sw.data_ptr(), _addr(l1t), _addr(l2t), r,
+            out.data_ptr(), b, m, n, g, ty, _addr(ws), wsb)
+    return out
+
+
+def pack_experts(w: torch.Tensor):
+    """W f32 [experts][n][m] -> (codes u8 [experts][n][m/2], scales f32 [m/128][experts * n]): each
+    expert's matrix as pack_weight_grouped packs it, the scales of all experts side by side."""
+    _need(w, "w", torch.float32, 3)
+    e, n, m = w.shape
+    if n % 16:
+        raise ValueError(f"n must be a multiple of 16 (got {n})")
+    with torch.cuda.device(w.device):
+        qw, sw = pack_weight_grouped(w.view(e * n, m))
+    return qw.view(e, n, m // 2), sw
+
+
+def _router(x, wr, k: int, bias, score: str, gpu: int):
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)} (got {score!r})")
+    if not isinstance(wr, torch.Tensor) or wr.dim() != 2:
+        _need(wr, "wr", x.dtype, 2)
+    b, m = x.shape
+    experts = wr.shape[0]
+    _want(x, "x", x.dtype, (b, m), gpu)
+    _want(wr, "wr", x.dtype, (experts, m), gpu)
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (experts,), gpu)
+    return b, m, experts
+
+
+def _experts(x, gate_up, down, gpu: int):
+    (q1, s1), (q2, s2) = gate_up, down
+    for t, name in ((q1, "gate_up codes"), (q2, "down codes")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            _need(t, name, torch.uint8, 3)
+    m, (experts, n1, _) = x.shape[1], q1.shape
+    f = n1 // 2
+    _want(q1, "gate_up codes", torch.uint8, (experts, 2 * f, m // 2), gpu)
+    _want(s1, "gate_up scales", torch.float32, (m // GROUP, experts * 2 * f), gpu)
+    _want(q2, "down codes", torch.uint8, (experts, m, f // 2), gpu)
+    _want(s2, "down scales", torch.float32, (f // GROUP, experts * m), gpu)
+    return q1, s1, q2, s2, experts, f
+
+
+def _routed_out(x, out, *inputs):
+    if out is None:
+        return torch.empty_like(x)
+    _want(out, "out", x.dtype, tuple(x.shape), x.get_device())
+    _apart(out, "out", x, *inputs)
+    return out
+
+
+def moe_route(x: torch.Tensor, wr: torch.Tensor, k: int, bias: torch.Tensor | None = None, score: str = "softmax",
+              norm: bool = True, scale: float = 1.0):
+    """The router of a routed layer, for up to MOE_TOKENS tokens: (ids int32 [b][k], weights f32 [b][k]).
+
+    Logits x wr^T (binary64; wr [experts][m] of x's type), scores p = softmax or sigmoid of
+    them. A token's experts are the k with the largest logits, or with a bias (f32 [experts]) the
+    largest p + bias, best first, the lowest index first among equals; weights are p, divided by
+    their sum if norm, times scale."""
+    ty, gpu = _type(x, "x"), x.get_device()
+    b, m, experts = _router(x, wr, k, bias, score, gpu)
+    ids, weights = x.new_empty((b, k), dtype=torch.int32), x.new_empty((b, k), dtype=torch.float32)
+    L = lib()
+    wsb = _sizes("twq_moe_route_workspace_bytes", b, m, experts, k)
+    ws = _scratch(x, wsb)
+    _launch(gpu, "twq_moe_route", L.twq_moe_route, x.data_ptr(), wr.data_ptr(), _addr(bias), b, m, experts, k, SCORES[score],
+            int(norm), scale, ty, ids.data_ptr(), weights.data_ptr(), _addr(ws), wsb)
+    return ids, weights
+
+
+def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up, down,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """The experts' part of a routed layer for a given choice (moe_route's, or any other router's):
+    Y [b][m], y_i = sum_j weights_ij D_e (silu(G_e x_i) * (U_e x_i)) with e = ids_ij.
+
+    x [b][m] fp16 or bf16, at most MOE_TOKENS rows; ids int32 [b][k] (outside [0, experts): none),
+    weights f32 [b][k]; gate_up = pack_experts([experts][2 f][m], f rows of G and then f of U an
+    expert), down = pack_experts([experts][m][f])."""
+    ty, gpu = _type(x, "x"), x.get_device()
+    b, m = x.shape
+    _want(x, "x", x.dtype, (b, m), gpu)
+    q1, s1, q2, s2, experts, f = _experts(x, gate_up, down, gpu)
+    _need(ids, "ids", torch.int32, 2)
+    k = ids.shape[1]
+    _want(ids, "ids", torch.int32, (b, k), gpu)
+    _want(weights, "weights", torch.float32, (b, k), gpu)
+    out = _routed_out(x, out, ids, weights, q1, s1, q2, s2)
+    L = lib()
+    wsb = _sizes("twq_moe_experts_workspace_bytes", b, m, f, experts, k)
+    ws = _scratch(x, wsb)
+    _launch(gpu, "twq_moe_experts", L.twq_moe_experts, x.data_ptr(), ids.data_ptr(), weights.data_ptr(), q1.data_ptr(),
+            s1.data_ptr(), q2.data_ptr(), s2.data_ptr(), out.data_ptr(), b, m, f, experts, k, GROUP, ty, _addr(ws), wsb)
+    return out
+
+
+def moe(x: torch.Tensor, wr: torch.Tensor, k: int, gate_up, down, bias: torch.Tensor | None = None, score: str = "softmax",
+        norm: bool = True, scale: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The whole routed layer in one call (twq_moe): moe_route, then moe_experts on its choice."""
+    ty, gpu = _type(x, "x"), x.get_device()
+    b, m, experts = _router(x, wr, k, bias, score, gpu)
+    q1, s1, q2, s2, held, f = _experts(x, gate_up, down, gpu)
+    if held != experts:
+        raise ValueError(f"wr routes to {experts} experts, gate_up holds {held}")
+    out = _routed_out(x, out, wr, bias, q1, s1, q2, s2)
+    L = lib()
+    wsb = _sizes("twq_moe_workspace_bytes", b, m, f, experts, k)
+    ws = _scratch(x, wsb)
+    _launch(gpu, "twq_moe", L.twq_moe, x.data_ptr(), wr.data_ptr(), _addr(bias), q1.data_ptr(), s1.data_ptr(), q2.data_ptr(),
+            s2.data_ptr(), out.data_ptr(), b, m, f, experts, k, GROUP, SCORES[score], int(norm), scale, ty, _addr(ws), wsb)
+    return out
+
+
+class RoutedLayer:
+    """A routed layer (mixture of experts) with packed experts, resident on one GPU: the router's
+    weight wr [experts][m], the experts' gate and up rows [experts][2 f][m] and down rows
+    [experts][m][f] in binary32."""
+
+    def __init__(self, wr: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, k: int, bias: torch.Tensor | None = None,
+                 score: str = "softmax", norm: bool = True, scale: float = 1.0):
+        self.wr, self.bias = wr, bias
+        self.gate_up, self.down = pack_experts(gate_up), pack_experts(down)
+        self.k, self.score, self.norm, self.scale = k, score, norm, scale
+
+    def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+        return moe(x, self.wr, self.k, self.gate_up, self.down, self.bias, self.score, self.norm, self.scale, out=out)
+
+    def route(self, x: torch.Tensor):
+        """The experts of each token and their weights (moe_route)."""
+        return moe_route(x, self.wr, self.k, self.bias, self.score, self.norm, self.scale)
 
 
 class DualLinear:

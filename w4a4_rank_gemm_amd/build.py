@@ -12,7 +12,8 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "lib", "libtwq.so")
 SOURCES = ["act_quant.hip", "pack_weight.hip", "dual_linear.hip", "lowrank_int4.hip", "noalloc.hip", "fold.hip", "adapters.hip",
-           "adapters_wgrad.hip", "checkpoint.hip", "linear_dx.hip", "plan.cpp", "twq_api.cpp", "adapters_api.cpp"]
+           "adapters_wgrad.hip", "checkpoint.hip", "linear_dx.hip", "linear_a16.hip", "moe.hip", "plan.cpp",
+           "twq_api.cpp", "adapters_api.cpp", "moe_api.cpp"]
 ARCH = "gfx950"
 
 

@@ -173,10 +173,10 @@ __device__ __forceinline__ Tile tile_of(const PlanView &p, int64_t t, int64_t b)
 // 87 us (4.3 to 2.7 TB/s of V; a 1 GiB copy moves 5.1), LDS active in 25, 32, 42 and 56% of the
 // compute units' busy cycles, 34 to 40% of that bank conflicts. 4096 x 14336, 64 ranks, 31 us; 32
 // rows of 32 adapters, 8192 x 64 each, 9.4 us (3.6 TB/s of weights).
-// KMAJOR weights ([k][r], ranks contiguous) are read back from LDS transposed. DX (the frozen
-// layer's input gradient): fp16 weights whatever the rows, split exactly into two bf16 parts
-// for bf16 rows; and the rows' largest |v sw| on the way.
-template <class T, int NG, int RB, bool KMAJOR, bool DX>
+// KMAJOR weights ([k][r], ranks contiguous) are read back from LDS transposed. W16 (the layer's own
+// pair): fp16 weights whatever the rows, split exactly into two bf16 parts for bf16 rows. DX (the
+// frozen layer's input gradient): the rows' largest |v sw| on the way.
+template <class T, int NG, int RB, bool KMAJOR, bool DX, bool W16>
 __global__ __launch_bounds__(NG == 8 ? 512 : 256) void shrink_kernel(ShrinkArgs a) {
     constexpr int NT = NG == 8 ? 512 : 256, XN = 256 * NG / NT, WN = (256 * RB + NT - 1) / NT;  // threads; chunks a thread
     constexpr int SK = 128, XS = SK * 2 + 16;                         // elements of a stage; padded LDS row of X
@@ -284,7 +284,7 @@ __global__ __launch_bounds__(NG == 8 ? 512 : 256) void shrink_kernel(ShrinkArgs 
                 } else {
                     wf = load16(buf + XB + (c * 16 + li) * WS + (e + g * 8) * 2);
                 }
-                if constexpr (DX && T::kBf16) {
+                if constexpr (W16 && T::kBf16) {
                     v4i hi, lo;
                     split_f16(wf, hi, lo);
                     acc[c] = T::mfma(lo, xf, acc[c]);
@@ -333,32 +333,33 @@ __global__ __launch_bounds__(NG == 8 ? 512 : 256) void shrink_kernel(ShrinkArgs 
     }
 }
 
-template <class T, int NG, bool KMAJOR, bool DX>
+template <class T, int NG, bool KMAJOR, bool DX, bool W16>
 static hipError_t shrink_ranks(const ShrinkArgs &a, hipStream_t stream) {
     const int rb = a.r <= 16 ? 1 : a.r <= 32 ? 2 : a.r <= 64 || NG < 8 ? 4 : 8;
     const unsigned grid = (unsigned)(a.tiles * ((a.r + 16 * rb - 1) / (16 * rb)) * a.ks);
     constexpr int NT = NG == 8 ? 512 : 256;
     if (rb == 1)
-        shrink_kernel<T, NG, 1, KMAJOR, DX><<<grid, NT, 0, stream>>>(a);
+        shrink_kernel<T, NG, 1, KMAJOR, DX, W16><<<grid, NT, 0, stream>>>(a);
     else if (rb == 2)
-        shrink_kernel<T, NG, 2, KMAJOR, DX><<<grid, NT, 0, stream>>>(a);
+        shrink_kernel<T, NG, 2, KMAJOR, DX, W16><<<grid, NT, 0, stream>>>(a);
     else if (rb == 4)
-        shrink_kernel<T, NG, 4, KMAJOR, DX><<<grid, NT, 0, stream>>>(a);
+        shrink_kernel<T, NG, 4, KMAJOR, DX, W16><<<grid, NT, 0, stream>>>(a);
     else if constexpr (NG == 8)
-        shrink_kernel<T, NG, 8, KMAJOR, DX><<<grid, NT, 0, stream>>>(a);
+        shrink_kernel<T, NG, 8, KMAJOR, DX, W16><<<grid, NT, 0, stream>>>(a);
     return hipGetLastError();
 }
 
-template <class T, bool KMAJOR, bool DX>
+template <class T, bool KMAJOR, bool DX, bool W16>
 static hipError_t shrink_rows(const ShrinkArgs &a, hipStream_t stream) {
-    if (a.b <= kFewRows) return shrink_ranks<T, 1, KMAJOR, DX>(a, stream);
-    return a.b <= kManyRows ? shrink_ranks<T, 4, KMAJOR, DX>(a, stream) : shrink_ranks<T, 8, KMAJOR, DX>(a, stream);
+    if (a.b <= kFewRows) return shrink_ranks<T, 1, KMAJOR, DX, W16>(a, stream);
+    return a.b <= kManyRows ? shrink_ranks<T, 4, KMAJOR, DX, W16>(a, stream) : shrink_ranks<T, 8, KMAJOR, DX, W16>(a, stream);
 }
 
 hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t stream) {
-    if (a.rowmax) return a.bf16 ? shrink_rows<BF16, true, true>(a, stream) : shrink_rows<F16, true, true>(a, stream);
-    if (a.bf16) return a.kmajor ? shrink_rows<BF16, true, false>(a, stream) : shrink_rows<BF16, false, false>(a, stream);
-    return a.kmajor ? shrink_rows<F16, true, false>(a, stream) : shrink_rows<F16, false, false>(a, stream);
+    if (a.rowmax) return a.bf16 ? shrink_rows<BF16, true, true, true>(a, stream) : shrink_rows<F16, true, true, true>(a, stream);
+    if (a.bf16 && a.w_f16) return shrink_rows<BF16, false, false, true>(a, stream);
+    if (a.bf16) return a.kmajor ? shrink_rows<BF16, true, false, false>(a, stream) : shrink_rows<BF16, false, false, false>(a, stream);
+    return a.kmajor ? shrink_rows<F16, true, false, false>(a, stream) : shrink_rows<F16, false, false, false>(a, stream);
 }
 
 // ---- expand --------------------------------------------------------------------------

@@ -1,0 +1,222 @@
+// moe_api.cpp -- the C ABI of the layer with 16-bit activations and of the routed layer: argument
+// validation, workspace layouts and launches. As in twq_api.cpp every check happens before
+// the first HIP call.
+#include "twq.h"
+
+#include <hip/hip_runtime.h>
+
+#include "twq_adapters.h"
+#include "twq_check.h"
+#include "twq_kernels.h"
+#include "twq_moe.h"
+
+namespace {
+
+using namespace twq;
+
+constexpr int64_t kMaxA16N = int64_t(1) << 22;
+constexpr int64_t kMaxOutput = int64_t(1) << 40;
+
+bool valid_type(int t) { return t == TWQ_F16 || t == TWQ_BF16; }
+bool valid_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
+    return valid_b(b) && valid_m(m) && n >= 0 && n % 16 == 0 && n <= kMaxA16N && b * n <= kMaxOutput && valid_r(r);
+}
+bool valid_route(int64_t b, int64_t m, int64_t experts, int64_t k) {
+    return b >= 0 && b <= kMaxMoeTokens && valid_m(m) && experts >= 1 && experts <= kMaxExperts && k >= 1 && k <= kMaxTopK && k <= experts;
+}
+bool valid_experts(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k) {
+    // a token may choose more often than there are experts here: its choices are given
+    return b >= 0 && b <= kMaxMoeTokens && valid_m(m) && valid_m(f) && experts >= 1 && experts <= kMaxExperts && k >= 1 &&
+           k <= kMaxTopK && experts * 2 * f <= kMaxN && experts * m <= kMaxN;
+}
+
+twq_status done(hipError_t e, const char *name) { return e == hipSuccess ? TWQ_OK : (twq_status)hip_error(e, name); }
+
+const uint16_t *u16(const void *p) { return static_cast<const uint16_t *>(p); }
+
+struct MoeLayout {
+    size_t h, part, experts;             // of twq_moe_experts
+    size_t logits, ids, weights, total;  // of twq_moe, behind it
+};
+
+size_t route_bytes(int64_t b, int64_t experts) { return align256((size_t)(b * experts) * 8); }
+
+MoeLayout moe_layout(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k) {
+    MoeLayout L{};
+    L.h = 0;
+    L.part = align256((size_t)(b * k * f) * 4);
+    L.experts = L.part + align256((size_t)(b * k * m) * 4);
+    L.logits = L.experts;
+    L.ids = L.logits + route_bytes(b, experts);
+    L.weights = L.ids + align256((size_t)(b * k) * 4);
+    L.total = L.weights + align256((size_t)(b * k) * 4);
+    return L;
+}
+
+hipError_t route(const void *x, const void *wr, const float *bias, int64_t b, int64_t m, int64_t experts, int64_t k, int score,
+                 int norm, float scale, int type, int32_t *ids, float *weights, void *logits, hipStream_t stream) {
+    RouteArgs a{};
+    a.x = u16(x);
+    a.wr = u16(wr);
+    a.bias = bias;
+    a.b = b;
+    a.m = m;
+    a.experts = (int)experts;
+    a.k = (int)k;
+    a.bf16 = type == TWQ_BF16;
+    a.sigmoid = score == TWQ_SIGMOID;
+    a.norm = norm != 0;
+    a.scale = scale;
+    a.logits = static_cast<double *>(logits);
+    a.ids = ids;
+    a.weights = weights;
+    return launch_route(a, stream);
+}
+
+hipError_t experts_of(const void *x, const int32_t *ids, const float *weights, const void *q1, const float *s1, const void *q2,
+                      const float *s2, void *y, int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k, int type,
+                      uint8_t *ws, const MoeLayout &L, hipStream_t stream) {
+    MoeArgs a{};
+    a.x = u16(x);
+    a.ids = ids;
+    a.weights = weights;
+    a.q1 = static_cast<const uint8_t *>(q1);
+    a.s1 = s1;
+    a.q2 = static_cast<const uint8_t *>(q2);
+    a.s2 = s2;
+    a.b = b;
+    a.m = m;
+    a.f = f;
+    a.experts = (int)experts;
+    a.k = (int)k;
+    a.bf16 = type == TWQ_BF16;
+    a.h = reinterpret_cast<uint16_t *>(ws + L.h);
+    a.part = reinterpret_cast<float *>(ws + L.part);
+    a.y = static_cast<uint16_t *>(y);
+    return launch_moe(a, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t twq_linear_a16_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r, int64_t g) {
+    if (g != 128 || !valid_a16(b, m, n, r) || b == 0 || n == 0) return 0;
+    return plan_a16(b, m, n, r).total;
+}
+
+twq_status twq_linear_a16(const void *x, const void *qw, const float *sw, const void *l1t, const void *l2t, int64_t r, void *y,
+                          int64_t b, int64_t m, int64_t n, int64_t g, int type, void *workspace, size_t workspace_bytes,
+                          void *stream) {
+    if (!valid_type(type) || g != 128) return TWQ_ERR_UNSUPPORTED;
+    if (!valid_a16(b, m, n, r)) return TWQ_ERR_SHAPE;
+    if (b == 0 || n == 0) return TWQ_OK;
+    if (!x || !qw || !sw || !y || (r > 0 && (!l1t || !l2t))) return TWQ_ERR_NULL;
+    if (!aligned16(x) || !aligned16(qw) || !aligned16(sw) || !aligned16(y) || (r > 0 && (!aligned16(l1t) || !aligned16(l2t))))
+        return TWQ_ERR_ALIGN;
+    const A16Plan p = plan_a16(b, m, n, r);
+    if (p.total > 0 && (!workspace || workspace_bytes < p.total)) return TWQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TWQ_ERR_ALIGN;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    uint8_t *const ws = static_cast<uint8_t *>(workspace);
+    hipError_t e = hipSuccess;
+    if (r > 0) {
+        ShrinkArgs s{};
+        s.v = u16(x);
+        s.w = u16(l1t);
+        s.b = b;
+        s.k = m;
+        s.r = (int)r;
+        s.bf16 = type == TWQ_BF16;
+        s.w_f16 = 1;
+        s.tiles = (b + tile_rows(b) - 1) / tile_rows(b);
+        s.ks = p.ks;
+        s.p = reinterpret_cast<float *>(ws + p.t);
+        e = launch_shrink(s, st);
+        if (e != hipSuccess) return done(e, "twq_linear_a16");
+    }
+    A16Args a{};
+    a.x = u16(x);
+    a.qw = static_cast<const uint8_t *>(qw);
+    a.sw = sw;
+    a.l2t = u16(l2t);
+    a.t = reinterpret_cast<const float *>(ws + p.t);
+    a.ks = p.ks;
+    a.y = static_cast<uint16_t *>(y);
+    a.b = b;
+    a.m = m;
+    a.n = n;
+    a.r = (int)r;
+    a.bf16 = type == TWQ_BF16;
+    return done(launch_a16(a, p, st), "twq_linear_a16");
+}
+
+size_t twq_moe_route_workspace_bytes(int64_t b, int64_t m, int64_t experts, int64_t k) {
+    if (!valid_route(b, m, experts, k)) return 0;
+    return route_bytes(b, experts);
+}
+
+twq_status twq_moe_route(const void *x, const void *wr, const float *bias, int64_t b, int64_t m, int64_t experts, int64_t k,
+                         int score, int norm, float scale, int type, int32_t *ids, float *weights, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+    if (!valid_type(type) || (score != TWQ_SOFTMAX && score != TWQ_SIGMOID)) return TWQ_ERR_UNSUPPORTED;
+    if (!valid_route(b, m, experts, k)) return TWQ_ERR_SHAPE;
+    if (b == 0) return TWQ_OK;
+    if (!x || !wr || !ids || !weights) return TWQ_ERR_NULL;
+    if (!aligned16(x) || !aligned16(wr) || !aligned16(bias) || !aligned16(ids) || !aligned16(weights)) return TWQ_ERR_ALIGN;
+    if (!workspace || workspace_bytes < route_bytes(b, experts)) return TWQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TWQ_ERR_ALIGN;
+    return done(route(x, wr, bias, b, m, experts, k, score, norm, scale, type, ids, weights, workspace,
+                      static_cast<hipStream_t>(stream)), "twq_moe_route");
+}
+
+size_t twq_moe_experts_workspace_bytes(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k) {
+    if (!valid_experts(b, m, f, experts, k)) return 0;
+    return moe_layout(b, m, f, experts, k).experts;
+}
+
+twq_status twq_moe_experts(const void *x, const int32_t *ids, const float *weights, const void *q1, const float *s1,
+                           const void *q2, const float *s2, void *y, int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k,
+                           int64_t g, int type, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!valid_type(type) || g != 128) return TWQ_ERR_UNSUPPORTED;
+    if (!valid_experts(b, m, f, experts, k)) return TWQ_ERR_SHAPE;
+    if (b == 0) return TWQ_OK;
+    if (!x || !ids || !weights || !q1 || !s1 || !q2 || !s2 || !y) return TWQ_ERR_NULL;
+    if (!aligned16(x) || !aligned16(ids) || !aligned16(weights) || !aligned16(q1) || !aligned16(s1) || !aligned16(q2) ||
+        !aligned16(s2) || !aligned16(y))
+        return TWQ_ERR_ALIGN;
+    const MoeLayout L = moe_layout(b, m, f, experts, k);
+    if (!workspace || workspace_bytes < L.experts) return TWQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TWQ_ERR_ALIGN;
+    return done(experts_of(x, ids, weights, q1, s1, q2, s2, y, b, m, f, experts, k, type, static_cast<uint8_t *>(workspace), L,
+                           static_cast<hipStream_t>(stream)), "twq_moe_experts");
+}
+
+size_t twq_moe_workspace_bytes(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k) {
+    if (!valid_experts(b, m, f, experts, k) || !valid_route(b, m, experts, k)) return 0;
+    return moe_layout(b, m, f, experts, k).total;
+}
+
+twq_status twq_moe(const void *x, const void *wr, const float *bias, const void *q1, const float *s1, const void *q2,
+                   const float *s2, void *y, int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k, int64_t g, int score,
+                   int norm, float scale, int type, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!valid_type(type) || g != 128 || (score != TWQ_SOFTMAX && score != TWQ_SIGMOID)) return TWQ_ERR_UNSUPPORTED;
+    if (!valid_experts(b, m, f, experts, k) || !valid_route(b, m, experts, k)) return TWQ_ERR_SHAPE;
+    if (b == 0) return TWQ_OK;
+    if (!x || !wr || !q1 || !s1 || !q2 || !s2 || !y) return TWQ_ERR_NULL;
+    if (!aligned16(x) || !aligned16(wr) || !aligned16(bias) || !aligned16(q1) || !aligned16(s1) || !aligned16(q2) ||
+        !aligned16(s2) || !aligned16(y))
+        return TWQ_ERR_ALIGN;
+    const MoeLayout L = moe_layout(b, m, f, experts, k);
+    if (!workspace || workspace_bytes < L.total) return TWQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TWQ_ERR_ALIGN;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    uint8_t *const ws = static_cast<uint8_t *>(workspace);
+    int32_t *const ids = reinterpret_cast<int32_t *>(ws + L.ids);
+    float *const weights = reinterpret_cast<float *>(ws + L.weights);
+    hipError_t e = route(x, wr, bias, b, m, experts, k, score, norm, scale, type, ids, weights, ws + L.logits, st);
+    if (e == hipSuccess) e = experts_of(x, ids, weights, q1, s1, q2, s2, y, b, m, f, experts, k, type, ws, L, st);
+    return done(e, "twq_moe");
+}
+
+}  // extern "C"

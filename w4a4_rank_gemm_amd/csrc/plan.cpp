@@ -7,6 +7,7 @@
 
 #include "twq_adapters.h"
 #include "twq_kernels.h"
+#include "twq_moe.h"
 
 namespace twq {
 
@@ -151,6 +152,18 @@ DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
     p.t16 = p.t + up((size_t)p.tks * b * r * 4);
     p.part = p.t16 + up((size_t)b * ((r + 31) / 32 * 32) * 4);
     p.total = p.part + (p.ks > 1 ? up((size_t)p.ks * b * m * 4) : 0);
+    return p;
+}
+
+// ---- the layer with 16-bit activations ----
+
+A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
+    A16Plan p{};
+    p.rows = b <= 4 ? 4 : b <= 16 ? 16 : b <= 32 ? 32 : 64;
+    p.fn = n / 16 >= 1024 ? 2 : 1;
+    p.ks = r > 0 ? shrink_slices(b, m, r, (b + tile_rows(b) - 1) / tile_rows(b), 4) : 0;
+    p.t = 0;
+    p.total = r > 0 ? ((size_t)p.ks * b * r * 4 + 255) & ~size_t(255) : 0;
     return p;
 }
 

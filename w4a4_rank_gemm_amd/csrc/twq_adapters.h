@@ -90,6 +90,7 @@ struct ShrinkArgs {
     int64_t b, k;
     int r;
     int bf16;            // type of v and w (rowmax: w is fp16)
+    int w_f16;           // w is fp16 whatever v is ([r][k] only)
     int kmajor;
     const float *sw;     // with rowmax: [k]
     float *rowmax;       // [ks][b]: largest |v sw| of a row over a slice, or NULL (the plain products)

@@ -1,0 +1,163 @@
+// twq_few_device.h -- the product of a few 16-bit rows with packed 4-bit weights of group-wise
+// scales, one wave's share of it (gfx950): the layer with 16-bit activations for few tokens
+// and the experts of the routed layer.
+#pragma once
+
+#include "twq_adapters_device.h"
+
+namespace twq {
+
+// The packed codes as matrix operands of a 16-bit type. Eight codes of one dword become four
+// pairs, in an order that `order` gives eight elements of a row too; the operand's values are
+// the codes times kTimes.
+template <class T>
+struct Codes;
+
+template <>
+struct Codes<F16> {  // pairs (0, 4), (1, 5), (2, 6), (3, 7)
+    static constexpr float kTimes = 1.f;
+    DequantConst c = dequant_const();
+    __device__ __forceinline__ v4i operator()(uint32_t d) const { return dequant8(d, c); }
+    static __device__ __forceinline__ v4i order(v4i x) {
+        return v4i{(int)__builtin_amdgcn_perm((uint32_t)x[2], (uint32_t)x[0], 0x05040100u),
+                   (int)__builtin_amdgcn_perm((uint32_t)x[2], (uint32_t)x[0], 0x07060302u),
+                   (int)__builtin_amdgcn_perm((uint32_t)x[3], (uint32_t)x[1], 0x05040100u),
+                   (int)__builtin_amdgcn_perm((uint32_t)x[3], (uint32_t)x[1], 0x07060302u)};
+    }
+};
+
+// bf16 has no packed arithmetic here: a nibble at the top of a byte is an int8 of 16 times the
+// code, which converts to binary32 exactly and lies in its upper 16 bits.
+template <>
+struct Codes<BF16> {  // pairs (0, 1), (2, 3), ..
+    static constexpr float kTimes = 16.f;
+    __device__ __forceinline__ v4i operator()(uint32_t d) const {
+        const uint32_t even = (d << 4) & 0xF0F0F0F0u, odd = d & 0xF0F0F0F0u;
+        v4i r;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t lo = __builtin_bit_cast(uint32_t, (float)(int8_t)(even >> (8 * t)));
+            const uint32_t hi = __builtin_bit_cast(uint32_t, (float)(int8_t)(odd >> (8 * t)));
+            r[t] = (int)__builtin_amdgcn_perm(hi, lo, 0x07060302u);
+        }
+        return r;
+    }
+    static __device__ __forceinline__ v4i order(v4i x) { return x; }
+};
+
+// LDS written by this wave is read by its other lanes: LDS operations of a wave stay in order,
+// the compiler has to keep them so.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// One wave's share of Y = X W^T for up to XR rows and FN panels of 16 channels: pieces (groups
+// of 128 elements of K) p0 .. p1 - 1, U in flight at a time. For each piece
+//
+//   acc[f][c] += s_W[piece][channel] (codes of the piece, panel f) . (rows 16 c .. 16 c + 15)
+//
+// on 16 x 16 x 32 matrix instructions: the product of one group is exact up to binary32 sums,
+// its scale multiplies the sum. A piece of a panel is 1 KB of contiguous memory, one 16-byte
+// load a lane, and goes to the matrix operands without LDS: lane (channel li, quarter g) holds
+// codes 32 g .. 32 g + 31, eight for each of four instructions. Rows are read along K (16 lanes a
+// row's piece) and turned through the wave's own LDS, so no wave waits for another; a piece's
+// scales too. PARTS = 2: a row's piece is 128 upper and then 128 lower parts of its elements, and
+// both take part in the sum.
+// acc: lane (li, g) holds row 16 c + li, channels 4 g .. 4 g + 3 of panel f.
+template <class T, int FN, int XR, int PARTS, int U>
+struct FewRows {
+    static_assert(XR % 4 == 0 && U <= 4, "rows in fours; a batch's scales are one load");
+    static constexpr int FM = (XR + 15) / 16;
+    static constexpr int XL = XR / 4;                 // row loads of a piece and part
+    static constexpr int SLOT = XR * 16 + 16;         // one (instruction, quarter): 16 bytes a row, padded against bank conflicts
+    static constexpr int PIECE = PARTS * 16 * SLOT;
+    static constexpr int LDS = U * PIECE + FN * 256;  // bytes of a wave
+
+    const uint8_t *w[FN];      // this wave's panels, at piece 0
+    const float *s[FN];        // scales of the panels' first channels, group 0
+    int64_t s_stride;          // floats between groups
+    const uint16_t *x[XL];     // this lane's rows 4 j + lane / 16 at element 8 (lane % 16)
+
+    template <bool STREAM>
+    __device__ __forceinline__ void run(int p0, int p1, uint8_t *lds, v4f (&acc)[FN][FM]) const {
+        const int lane = threadIdx.x % kWave, li = lane & 15, g = lane >> 4;
+        const Codes<T> codes;
+        v4i wn[U][FN], xn[U][PARTS][XL];
+        float sn[FN];
+        auto load = [&](int p) {  // pieces past the last are read again and scaled by zero
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t q = p + u < p1 ? p + u : p1 - 1;
+#pragma unroll
+                for (int f = 0; f < FN; ++f) {
+                    const uint8_t *a = w[f] + q * 1024 + li * 64 + g * 16;
+                    wn[u][f] = STREAM ? __builtin_nontemporal_load(reinterpret_cast<const v4i *>(a)) : load16(a);
+                }
+#pragma unroll
+                for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+                    for (int j = 0; j < XL; ++j) xn[u][h][j] = load16(x[j] + (q * PARTS + h) * 128);
+            }
+            const int64_t q = p + g < p1 ? p + g : p1 - 1;
+#pragma unroll
+            for (int f = 0; f < FN; ++f) sn[f] = s[f][q * s_stride + li];
+        };
+        if (p0 >= p1) return;
+        load(p0);
+        float *const scales = reinterpret_cast<float *>(lds + U * PIECE);
+        const int put = ((lane & 3) * 4 + ((lane >> 2) & 3)) * SLOT + g * 16;  // chunk lane % 16 = 4 quarter + instruction
+        const int get = g * SLOT + (XR < 16 && li >= XR ? XR - 1 : li) * 16;
+        for (int p = p0; p < p1; p += U) {
+            v4i wc[U][FN];
+            wave_fence();
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int f = 0; f < FN; ++f) wc[u][f] = wn[u][f];
+#pragma unroll
+                for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+                    for (int j = 0; j < XL; ++j)
+                        *reinterpret_cast<v4i *>(lds + u * PIECE + h * 16 * SLOT + put + j * 64) = Codes<T>::order(xn[u][h][j]);
+            }
+#pragma unroll
+            for (int f = 0; f < FN; ++f) scales[f * 64 + lane] = p + g < p1 ? sn[f] * (1.f / Codes<T>::kTimes) : 0.f;
+            if (p + U < p1) load(p + U);
+            wave_fence();
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                v4f t[FN][FM];
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    v4i xf[PARTS][FM];
+#pragma unroll
+                    for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+                        for (int c = 0; c < FM; ++c)
+                            xf[h][c] = load16(lds + u * PIECE + (h * 16 + d * 4) * SLOT + get + c * 256);
+#pragma unroll
+                    for (int f = 0; f < FN; ++f) {
+                        const v4i wf = codes((uint32_t)wc[u][f][d]);
+#pragma unroll
+                        for (int c = 0; c < FM; ++c)
+#pragma unroll
+                            for (int h = 0; h < PARTS; ++h)
+                                t[f][c] = T::mfma(wf, xf[h][c], h == 0 && d == 0 ? v4f{0.f, 0.f, 0.f, 0.f} : t[f][c]);
+                    }
+                }
+#pragma unroll
+                for (int f = 0; f < FN; ++f) {
+                    const v4f sc = *reinterpret_cast<const v4f *>(scales + f * 64 + u * 16 + g * 4);
+#pragma unroll
+                    for (int c = 0; c < FM; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[f][c][e] += sc[e] * t[f][c][e];
+                }
+            }
+        }
+        wave_fence();
+    }
+};
+
+}  // namespace twq

@@ -1,0 +1,71 @@
+// twq_moe.h -- launch interface of the layer with 16-bit activations and of the routed layer.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace twq {
+
+// ---- the layer with 16-bit activations ------------------------------------------------------
+
+struct A16Args {
+    const uint16_t *x;    // [b][m]
+    const uint8_t *qw;    // panels
+    const float *sw;      // [m / 128][n]
+    const uint16_t *l2t;  // [n][r] fp16
+    const float *t;       // [ks][b][r] partial sums of X L1
+    int ks;
+    uint16_t *y;          // [b][n]
+    int64_t b, m, n;
+    int r;
+    int bf16;             // type of x and y
+};
+
+struct A16Plan {
+    int rows;      // token rows a CTA
+    int fn;        // panels a CTA
+    int ks;        // K slices of X L1
+    size_t t, total;
+};
+A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r);  // plan.cpp
+hipError_t launch_a16(const A16Args &a, const A16Plan &p, hipStream_t stream);
+
+// ---- the routed layer ------------------------------------------------------------------------
+
+constexpr int64_t kMaxMoeTokens = 256, kMaxExperts = 512, kMaxTopK = 16;
+
+struct RouteArgs {
+    const uint16_t *x;    // [b][m]
+    const uint16_t *wr;   // [experts][m]
+    const float *bias;    // [experts] or NULL
+    int64_t b, m;
+    int experts, k;
+    int bf16;
+    int sigmoid;          // scores: sigmoid (1) or softmax (0) of the logits
+    int norm;             // weights divided by their sum
+    float scale;
+    double *logits;       // [b][experts]
+    int32_t *ids;         // [b][k]
+    float *weights;       // [b][k]
+};
+hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
+
+struct MoeArgs {
+    const uint16_t *x;    // [b][m]
+    const int32_t *ids;   // [b][k], outside [0, experts): none
+    const float *weights; // [b][k]
+    const uint8_t *q1;    // [experts] panels of 2 f channels: f gate, f up
+    const float *s1;      // [m / 128][experts 2 f]
+    const uint8_t *q2;    // [experts] panels of m channels
+    const float *s2;      // [f / 128][experts m]
+    int64_t b, m, f;
+    int experts, k;
+    int bf16;             // type of x and y
+    uint16_t *h;          // [b k][f / 128][2][128] bf16: the experts' inner rows, upper and lower parts
+    float *part;          // [b k][m]: weighted outputs of each token's choices
+    uint16_t *y;          // [b][m]
+};
+hipError_t launch_moe(const MoeArgs &a, hipStream_t stream);
+
+}  // namespace twq
