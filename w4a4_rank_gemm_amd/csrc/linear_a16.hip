@@ -28,7 +28,7 @@ __device__ __forceinline__ void few_lowrank(const A16Args &a, int64_t row0, int6
         for (int c = 0; c < FM; ++c) {
             const int64_t row = row0 + c * 16 + li < last ? row0 + c * 16 + li : last - 1;
             const float *p = a.t + row * a.r + kc;
-            v4f t0 = sum_slices(p, a.b * a.r, a.ks), t1 = sum_slices(p + 4, a.b * a.r, a.ks);
+            v4f t0 = sum_slices(p, a.b * a.r, a.tks), t1 = sum_slices(p + 4, a.b * a.r, a.tks);
             v4i th, tl;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -116,7 +116,358 @@ static hipError_t a16_few(const A16Args &a, const A16Plan &p, hipStream_t stream
     return hipGetLastError();
 }
 
+// ---- many rows ---------------------------------------------------------------------------
+
+// What the tile kernel reads: X in fp16, the scales as ratios, T in two parts.
+//
+// The tile kernel multiplies its sums by mul[G] = unit[G - 1] / unit[G] before group G, so that
+// they are in units of the group's scale when its products (codes times X) are added: one
+// multiplication a sum and group, no second set of sums. unit[G] is s_W[G]; where that is below
+// 2^-90 of the channel's largest (zero among it) the group's codes are masked (its share is
+// below 2^-84 of what any element of X adds through the largest scale) and the unit is the
+// largest. Sums then stay below 7 2^17 2^16 2^90 < 2^126.
+constexpr int kPrepRows = 4, kPrepChannels = 32;
+
+template <class T>
+__device__ __forceinline__ void prepare_row(const A16Args &a, int64_t row) {
+    const int lane = threadIdx.x % kWave;
+    const uint16_t *x = a.x + row * a.m;
+    uint16_t *out = a.x16 + row * a.m;
+    float f = 1.f;
+    if constexpr (T::kBf16) {  // to a largest element in [2^14, 2^15): exact down to 2^-28 of it, off by 2^-39 of it below
+        uint32_t mx = 0;
+        for (int64_t k = lane * 8; k < a.m; k += kWave * 8) {
+            const v4i v = load16(x + k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t lo = (uint32_t)v[e] << 16 & 0x7FFFFFFFu, hi = (uint32_t)v[e] & 0x7FFF0000u;
+                mx = mx > lo ? mx : lo;
+                mx = mx > hi ? mx : hi;
+            }
+        }
+        const int e = scale_exponent(__builtin_bit_cast(float, wave_max_u32(mx)));
+        f = pow2(14 - e);
+        if (lane == 0) a.xe[row] = e - 14;
+    }
+    for (int64_t k = lane * 8; k < a.m; k += kWave * 8) {
+        v4i v = load16(x + k);
+        if constexpr (T::kBf16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = (int)((uint32_t)F16::from_f32(T::to_f32(half_of(v[e], 0)) * f) |
+                             (uint32_t)F16::from_f32(T::to_f32(half_of(v[e], 1)) * f) << 16);
+        }
+        *reinterpret_cast<v4i *>(out + k) = Codes<F16>::order(v);
+    }
+}
+
+__device__ __forceinline__ void prepare_scales(const A16Args &a, int64_t block, float *red) {
+    const int groups = (int)(a.m / 128), gl = threadIdx.x / kPrepChannels;
+    const int64_t c = block * kPrepChannels + threadIdx.x % kPrepChannels, cc = c < a.n ? c : a.n - 1;
+    float top = 0.f;
+    for (int g = gl; g < groups; g += 256 / kPrepChannels) top = __builtin_fmaxf(top, __builtin_fabsf(a.sw[g * a.n + cc]));
+    red[threadIdx.x] = top;
+    __syncthreads();
+    for (int q = 0; q < 256 / kPrepChannels; ++q) top = __builtin_fmaxf(top, red[q * kPrepChannels + threadIdx.x % kPrepChannels]);
+    if (c >= a.n) return;
+    const float least = top * 0x1p-90f;
+    auto on = [&](float s) { return s != 0.f && !(__builtin_fabsf(s) < least); };
+    auto unit = [&](float s) { return on(s) ? s : top == 0.f ? 1.f : top; };
+    for (int g = gl; g < groups; g += 256 / kPrepChannels) {
+        const float s = a.sw[g * a.n + c], before = a.sw[(g > 0 ? g - 1 : 0) * a.n + c];
+        a.mul[g * a.n + c] = unit(before) / unit(s);
+        a.mask[g * a.n + c] = on(s) ? 0xFFFFFFFFu : 0u;
+        for (int q = 0; q < a.ks; ++q)
+            if (g + 1 == (q + 1) * groups / a.ks) a.unit[q * a.n + c] = unit(s);
+    }
+}
+
+// 16 rows, 16 threads a row: T summed over its slices in order, under a power of two a row, in two
+// fp16 parts (22 significant bits).
+__device__ __forceinline__ void prepare_t(const A16Args &a, int64_t block) {
+    const int q = threadIdx.x % 16;
+    const int64_t row = block * 16 + threadIdx.x / 16, rc = row < a.b ? row : a.b - 1;
+    float t[16], mx = 0.f;  // ranks q, q + 16, ..
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+        t[u] = 0.f;
+        if (u * 16 >= a.r) continue;
+        for (int s = 0; s < a.tks; ++s) t[u] += a.t[(s * a.b + rc) * a.r + u * 16 + q];
+        mx = __builtin_fmaxf(mx, __builtin_fabsf(t[u]));
+    }
+    for (int off = 8; off > 0; off >>= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, off, kWave));
+    if (row >= a.b) return;
+    const int e = scale_exponent(mx);
+    if (q == 0) a.te[row] = e - 14;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+        if (u * 16 >= a.r) continue;
+        const int k = u * 16 + q;
+        const float v = t[u] * pow2(14 - e);
+        const uint16_t hi = F16::from_f32(v), lo = F16::from_f32(v - F16::to_f32(hi));
+        uint16_t *p = a.t16 + (row * a.r + k / 8 * 8) * 2 + k % 8;
+        p[0] = hi;
+        p[8] = lo;
+    }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void a16_prepare_kernel(A16Args a, int64_t row_ctas, int64_t scale_ctas) {
+    __shared__ float red[256];
+    int64_t id = blockIdx.x;
+    if (id < row_ctas) {
+        const int64_t row = id * kPrepRows + threadIdx.x / kWave;
+        if (row < a.b) prepare_row<T>(a, row);
+        return;
+    }
+    id -= row_ctas;
+    if (id < scale_ctas)
+        prepare_scales(a, id, red);
+    else
+        prepare_t(a, id - scale_ctas);
+}
+
+// The X operands of two matrix steps (addresses a0, a1) for TB token blocks, 8 KB apart, completed
+// before returning (one statement, so that no other in-flight direct-to-LDS load is waited for).
+template <int TB, int OFF>
+__device__ __forceinline__ void a16_read(uint32_t a0, uint32_t a1, v4i (&r)[2][TB]) {
+    static_assert(TB == 2 || TB == 4, "token blocks");
+    if constexpr (TB == 4)
+        asm volatile(
+            "ds_read_b128 %0, %8 offset:%10\n\t"
+            "ds_read_b128 %1, %8 offset:%11\n\t"
+            "ds_read_b128 %2, %8 offset:%12\n\t"
+            "ds_read_b128 %3, %8 offset:%13\n\t"
+            "ds_read_b128 %4, %9 offset:%10\n\t"
+            "ds_read_b128 %5, %9 offset:%11\n\t"
+            "ds_read_b128 %6, %9 offset:%12\n\t"
+            "ds_read_b128 %7, %9 offset:%13\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[0][2]), "=&v"(r[0][3]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[1][2]),
+              "=&v"(r[1][3])
+            : "v"(a0), "v"(a1), "n"(OFF), "n"(OFF + 8192), "n"(OFF + 16384), "n"(OFF + 24576)
+            : "memory");
+    else
+        asm volatile(
+            "ds_read_b128 %0, %4 offset:%6\n\t"
+            "ds_read_b128 %1, %4 offset:%7\n\t"
+            "ds_read_b128 %2, %5 offset:%6\n\t"
+            "ds_read_b128 %3, %5 offset:%7\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[1][0]), "=&v"(r[1][1])
+            : "v"(a0), "v"(a1), "n"(OFF), "n"(OFF + 8192)
+            : "memory");
+}
+
+// A CTA owns 32 TB tokens x 256 channels over a slice of the groups; its four waves take 64
+// channels each and share the tokens' operands. A group of X (8 TB KB) goes to LDS by direct
+// loads, one group ahead, in 256-byte lines with the 16-byte chunk index XORed by row % 8 and 8
+// ((row / 16) % 2) (one 16-byte read serves lanes 0-7 with 16-23 in a pass). Each wave reads its own
+// codes straight from memory to registers, one group ahead: lane l of a 32-channel block holds
+// channel l % 32, and of each half group the 32 codes of K quarter l / 32. Tokens are the
+// rows of the result and channels its columns, so that a group's scale is one register a lane.
+template <class T, int TB>
+__global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t ntiles, int64_t ttiles) {
+    constexpr int ROWS = 32 * TB, XBYTES = ROWS * 256, XL = 2 * TB;
+    __shared__ __align__(1024) uint8_t ring[2 * XBYTES];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int col = lane % 32, half = lane / 32;
+    // neighbours on an XCD: bands of eight token tiles, channel tile by channel tile
+    const int64_t id = xcd_range(blockIdx.x, ntiles * ttiles), band = id / (8 * ntiles), in = id % (8 * ntiles);
+    const int64_t deep = ttiles - band * 8 < 8 ? ttiles - band * 8 : 8;
+    const int64_t tok0 = (band * 8 + in % deep) * ROWS, n0 = in / deep * kA16N + wave * 64;
+    const int64_t groups = a.m / 128, slice = blockIdx.y, g0 = slice * groups / a.ks, g1 = (slice + 1) * groups / a.ks;
+
+    const int panels = (int)(a.n / 16), panel0 = (int)(n0 / 16) < panels ? (int)(n0 / 16) : panels - 1;
+    uint32_t chan[2], woff[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int p = panel0 + q * 2 + col / 16, pc = p < panels ? p : panels - 1;
+        chan[q] = pc * 16 + col % 16;
+        woff[q] = (uint32_t)((pc - panel0) * groups * 1024) + col % 16 * 64 + half * 16;
+    }
+    const uint8_t *wbase = a.qw + panel0 * groups * 1024;
+    uint32_t xoff[XL];  // block j * 4 + wave of 1 KB: four rows, 16 chunks each
+#pragma unroll
+    for (int j = 0; j < XL; ++j) {
+        const int row = (j * 4 + wave) * 4 + lane / 16, swz = (row & 7) | (row >> 4 & 1) << 3;
+        const int64_t rel = tok0 + row < a.b ? row : a.b - 1 - tok0;
+        xoff[j] = (uint32_t)(rel * a.m * 2 + (lane % 16 ^ swz) * 16);
+    }
+    const uint16_t *xbase = a.x16 + tok0 * a.m;
+    v4i wn[2][2];
+    float mn[2];
+    uint32_t kn[2];
+    auto fetch = [&](int64_t g, int slot) {
+        const __amdgpu_buffer_rsrc_t rx =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(xbase + g * 128), 0, 0x7fffffff, 0x00020000);
+#pragma unroll
+        for (int j = 0; j < XL; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rx, (__attribute__((address_space(3))) void *)(ring + slot * XBYTES + (j * 4 + wave) * 1024), 16, (int)xoff[j], 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            wn[q][0] = load16(wbase + g * 1024 + woff[q]);
+            wn[q][1] = load16(wbase + g * 1024 + 32 + woff[q]);
+            mn[q] = (a.mul + g * a.n)[chan[q]];
+            kn[q] = (a.mask + g * a.n)[chan[q]];
+        }
+    };
+    const DequantConst dq = dequant_const();
+    v16f acc[2][TB];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[q][t][e] = 0.f;
+    // read address of matrix step s of half group st: chunk 8 st + 4 half + s of row `col`; st flips bit 7
+    const int swz = (col & 7) | (col >> 4 & 1) << 3;
+    uint32_t at[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) at[s] = lds_offset(ring) + col * 256 + ((half * 4 + s) ^ swz) * 16;
+
+    fetch(g0, 0);
+    for (int64_t c0 = g0; c0 < g1; c0 += 2) {
+        static_for(std::make_integer_sequence<int, 2>{}, [&](auto u) {
+            constexpr int U = decltype(u)::value, OFF = U * XBYTES;
+            const int64_t g = c0 + U;
+            if (g >= g1) return;
+            wait_vmcnt<0>();  // issued a group ago
+            stage_barrier();  // group g has landed for every wave, and group g - 1 is read
+            v4i w[2][2];
+            float mul[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                mul[q] = mn[q];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[q][h][e] = wn[q][h][e] & (int)kn[q];
+            }
+            if (g + 1 < g1) fetch(g + 1, 1 - U);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int t = 0; t < TB; ++t)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[q][t][e] *= mul[q];
+            static_for(std::make_integer_sequence<int, 4>{}, [&](auto pv) {
+                constexpr int P = decltype(pv)::value;
+                v4i x[2][TB];
+                a16_read<TB, OFF>(at[P % 2 * 2] ^ (P / 2 * 128), at[P % 2 * 2 + 1] ^ (P / 2 * 128), x);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const v8h wf = __builtin_bit_cast(v8h, dequant8((uint32_t)w[q][P / 2][P % 2 * 2 + s], dq));
+#pragma unroll
+                        for (int t = 0; t < TB; ++t) acc[q][t] = mfma_f16_32(__builtin_bit_cast(v8h, x[s][t]), wf, acc[q][t]);
+                    }
+            });
+        });
+    }
+    __syncthreads();
+
+    // true values; then the low-rank term, T L2 2^te; then the stores, turned in this wave's LDS
+    uint16_t *const turn = reinterpret_cast<uint16_t *>(ring) + wave * ROWS * 64;
+    const int64_t last = a.b - 1;
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+        const int64_t tok = tok0 + t * 32 + half * 4;  // + 8 (v / 4) + v % 4
+        float f[16];
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const int64_t i = tok + v / 4 * 8 + v % 4;
+            f[v] = T::kBf16 ? pow2(a.xe[i < last ? i : last]) : 1.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const float u = a.unit[slice * a.n + chan[q]];
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[q][t][v] = acc[q][t][v] * u * f[v];
+        }
+        if (a.r > 0 && slice == 0) {
+            v16f low[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) low[q][v] = 0.f;
+            const int64_t i = tok0 + t * 32 + col;
+            const uint16_t *tp = a.t16 + ((i < last ? i : last) * a.r + half * 8) * 2;
+            for (int k = 0; k < a.r; k += 16) {
+                const v8h hi = __builtin_bit_cast(v8h, load16(tp + k * 2)), lo = __builtin_bit_cast(v8h, load16(tp + k * 2 + 8));
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const v8h l2 = __builtin_bit_cast(v8h, load16(a.l2t + chan[q] * a.r + k + half * 8));
+                    low[q] = mfma_f16_32(lo, l2, low[q]);
+                    low[q] = mfma_f16_32(hi, l2, low[q]);
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int64_t i2 = tok + v / 4 * 8 + v % 4;
+                const float te = pow2(a.te[i2 < last ? i2 : last]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) acc[q][t][v] += low[q][v] * te;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int row = t * 32 + half * 4 + v / 4 * 8 + v % 4;
+                if (a.ks > 1) {
+                    if (tok0 + row < a.b && n0 + q * 32 + col < a.n)
+                        a.part[(slice * a.b + tok0 + row) * a.n + n0 + q * 32 + col] = acc[q][t][v];
+                } else {
+                    turn[row * 64 + q * 32 + col] = T::from_f32(acc[q][t][v]);
+                }
+            }
+    }
+    if (a.ks > 1) return;
+    wave_fence();
+#pragma unroll
+    for (int j = 0; j < ROWS / 8; ++j) {
+        const int row = j * 8 + lane / 8;
+        const int64_t c = n0 + lane % 8 * 8;
+        if (tok0 + row < a.b && c < a.n)
+            *reinterpret_cast<v4i *>(a.y + (tok0 + row) * a.n + c) = load16(turn + row * 64 + lane % 8 * 8);
+    }
+}
+
+// Y = the slices' sums in slice order, rounded once.
+template <class T>
+__global__ __launch_bounds__(256) void a16_join_kernel(const float *part, int ks, int64_t total, uint16_t *y) {
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (at >= total) return;
+    const v4f s = sum_slices(part + at, total, ks);
+    *reinterpret_cast<uint2 *>(y + at) = make_uint2((uint32_t)T::from_f32(s[0]) | (uint32_t)T::from_f32(s[1]) << 16,
+                                                    (uint32_t)T::from_f32(s[2]) | (uint32_t)T::from_f32(s[3]) << 16);
+}
+
+template <class T>
+static hipError_t a16_many(const A16Args &a, const A16Plan &p, hipStream_t stream) {
+    const int64_t row_ctas = (a.b + kPrepRows - 1) / kPrepRows, scale_ctas = (a.n + kPrepChannels - 1) / kPrepChannels;
+    const int64_t t_ctas = a.r > 0 ? (a.b + 15) / 16 : 0;
+    a16_prepare_kernel<T><<<dim3((unsigned)(row_ctas + scale_ctas + t_ctas)), 256, 0, stream>>>(a, row_ctas, scale_ctas);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t ntiles = (a.n + kA16N - 1) / kA16N, ttiles = (a.b + p.rows - 1) / p.rows;
+    const dim3 grid((unsigned)(ntiles * ttiles), (unsigned)p.ks);
+    if (p.rows == 128)
+        a16_tile_kernel<T, 4><<<grid, 256, 0, stream>>>(a, ntiles, ttiles);
+    else
+        a16_tile_kernel<T, 2><<<grid, 256, 0, stream>>>(a, ntiles, ttiles);
+    e = hipGetLastError();
+    if (e != hipSuccess || p.ks == 1) return e;
+    const int64_t total = a.b * a.n;
+    a16_join_kernel<T><<<dim3((unsigned)((total / 4 + 255) / 256)), 256, 0, stream>>>(a.part, p.ks, total, a.y);
+    return hipGetLastError();
+}
+
 hipError_t launch_a16(const A16Args &a, const A16Plan &p, hipStream_t stream) {
+    if (a.b > kFewTokens) return a.bf16 ? a16_many<BF16>(a, p, stream) : a16_many<F16>(a, p, stream);
     if (p.fn == 1) return a.bf16 ? a16_few<BF16, 1>(a, p, stream) : a16_few<F16, 1>(a, p, stream);
     return a.bf16 ? a16_few<BF16, 2>(a, p, stream) : a16_few<F16, 2>(a, p, stream);
 }

@@ -130,7 +130,7 @@ twq_status twq_linear_a16(const void *x, const void *qw, const float *sw, const 
         s.bf16 = type == TWQ_BF16;
         s.w_f16 = 1;
         s.tiles = (b + tile_rows(b) - 1) / tile_rows(b);
-        s.ks = p.ks;
+        s.ks = p.tks;
         s.p = reinterpret_cast<float *>(ws + p.t);
         e = launch_shrink(s, st);
         if (e != hipSuccess) return done(e, "twq_linear_a16");
@@ -141,7 +141,16 @@ twq_status twq_linear_a16(const void *x, const void *qw, const float *sw, const 
     a.sw = sw;
     a.l2t = u16(l2t);
     a.t = reinterpret_cast<const float *>(ws + p.t);
+    a.tks = p.tks;
+    a.x16 = reinterpret_cast<uint16_t *>(ws + p.x16);
+    a.xe = reinterpret_cast<int32_t *>(ws + p.xe);
+    a.mul = reinterpret_cast<float *>(ws + p.mul);
+    a.mask = reinterpret_cast<uint32_t *>(ws + p.mask);
+    a.unit = reinterpret_cast<float *>(ws + p.unit);
+    a.t16 = reinterpret_cast<uint16_t *>(ws + p.t16);
+    a.te = reinterpret_cast<int32_t *>(ws + p.te);
     a.ks = p.ks;
+    a.part = reinterpret_cast<float *>(ws + p.part);
     a.y = static_cast<uint16_t *>(y);
     a.b = b;
     a.m = m;

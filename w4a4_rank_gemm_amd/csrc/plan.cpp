@@ -158,12 +158,33 @@ DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
 // ---- the layer with 16-bit activations ----
 
 A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
+    auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     A16Plan p{};
-    p.rows = b <= 4 ? 4 : b <= 16 ? 16 : b <= 32 ? 32 : 64;
-    p.fn = n / 16 >= 1024 ? 2 : 1;
-    p.ks = r > 0 ? shrink_slices(b, m, r, (b + tile_rows(b) - 1) / tile_rows(b), 4) : 0;
-    p.t = 0;
-    p.total = r > 0 ? ((size_t)p.ks * b * r * 4 + 255) & ~size_t(255) : 0;
+    p.tks = r > 0 ? shrink_slices(b, m, r, (b + tile_rows(b) - 1) / tile_rows(b), 4) : 0;
+    p.ks = 1;
+    p.x16 = up((size_t)p.tks * b * r * 4);
+    p.total = p.x16;
+    if (b <= kFewTokens) {
+        p.rows = b <= 4 ? 4 : b <= 16 ? 16 : b <= 32 ? 32 : 64;
+        p.fn = n / 16 >= 1024 ? 2 : 1;
+        return p;
+    }
+    const int64_t groups = m / 128, ntiles = (n + kA16N - 1) / kA16N;
+    p.rows = 128;
+    if ((b + 127) / 128 * ntiles < 256) p.rows = 64;
+    const int64_t ctas = (b + p.rows - 1) / p.rows * ntiles;
+    int64_t ks = 512 / ctas;
+    if (ks > groups / 4) ks = groups / 4;
+    if (ks > 8) ks = 8;
+    p.ks = ks < 1 ? 1 : (int)ks;
+    p.xe = p.x16 + up((size_t)b * m * 2);
+    p.mul = p.xe + up((size_t)b * 4);
+    p.mask = p.mul + up((size_t)groups * n * 4);
+    p.unit = p.mask + up((size_t)groups * n * 4);
+    p.t16 = p.unit + up((size_t)p.ks * n * 4);
+    p.te = p.t16 + up((size_t)b * r * 4);
+    p.part = p.te + up((size_t)b * 4);
+    p.total = p.part + (p.ks > 1 ? up((size_t)p.ks * b * n * 4) : 0);
     return p;
 }
 

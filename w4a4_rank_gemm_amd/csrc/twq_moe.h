@@ -9,24 +9,41 @@ namespace twq {
 
 // ---- the layer with 16-bit activations ------------------------------------------------------
 
+// Up to kFewTokens rows the product is bound by the weights' read (a few-row kernel); above by the
+// matrix cores (a tile kernel, which wants X in fp16 in the order of the expanded codes, and
+// the scales as ratios of neighbouring groups).
+constexpr int64_t kFewTokens = 64;
+constexpr int kA16N = 256;  // channels of a tile CTA: 64 a wave
+
 struct A16Args {
     const uint16_t *x;    // [b][m]
     const uint8_t *qw;    // panels
     const float *sw;      // [m / 128][n]
     const uint16_t *l2t;  // [n][r] fp16
-    const float *t;       // [ks][b][r] partial sums of X L1
-    int ks;
+    const float *t;       // [tks][b][r] partial sums of X L1
+    int tks;
     uint16_t *y;          // [b][n]
     int64_t b, m, n;
     int r;
     int bf16;             // type of x and y
+    // tile kernel
+    uint16_t *x16;        // [b][m] fp16: X 2^-xe, eight elements in the order 0 4 1 5 2 6 3 7
+    int32_t *xe;          // [b] (bf16)
+    float *mul;           // [m / 128][n]: unit of the group before over this group's
+    uint32_t *mask;       // [m / 128][n]: all ones, or 0 for a group without weight
+    float *unit;          // [ks][n]: unit of a slice's last group
+    uint16_t *t16;        // [b][r / 8][2][8]: X L1 2^-te in two fp16 parts
+    int32_t *te;          // [b]
+    int ks;               // slices of K
+    float *part;          // [ks][b][n] when ks > 1
 };
 
 struct A16Plan {
     int rows;      // token rows a CTA
-    int fn;        // panels a CTA
-    int ks;        // K slices of X L1
-    size_t t, total;
+    int fn;        // few rows: panels a CTA
+    int tks;       // K slices of X L1
+    int ks;        // tile kernel: K slices
+    size_t t, x16, xe, mul, mask, unit, t16, te, part, total;
 };
 A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r);  // plan.cpp
 hipError_t launch_a16(const A16Args &a, const A16Plan &p, hipStream_t stream);
