@@ -10,16 +10,71 @@
 
 namespace twq {
 
+// T = X L1 for few rows: a CTA owns 16 rows x 16 ranks over a slice of K, which its 16 waves
+// split; each wave's loads are all in flight before the first is used, and the waves' sums are
+// added in wave order. A fp16 L1 meets bf16 rows as two exact bf16 parts.
 constexpr int kFewWaves = 8;
+constexpr int kTWaves = 16, kTSteps = 4;
+
+template <class T>
+__global__ __launch_bounds__(kTWaves *kWave) void a16_t_kernel(A16Args a) {
+    __shared__ v4f red[kTWaves][kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, li = lane & 15, g = lane >> 4;
+    const int64_t rank0 = (int64_t)blockIdx.x * 16, row = (int64_t)blockIdx.y * 16 + li, slice = blockIdx.z;
+    const int steps = (int)(a.m / 32), parts = a.tks * kTWaves, part = (int)slice * kTWaves + wave;
+    const int s0 = (int)((int64_t)part * steps / parts), s1 = (int)((int64_t)(part + 1) * steps / parts);
+    const uint16_t *w = a.l1t + (rank0 + li) * a.m + g * 8, *x = a.x + (row < a.b ? row : a.b - 1) * a.m + g * 8;
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    for (int s = s0; s < s1; s += kTSteps) {
+        v4i wv[kTSteps], xv[kTSteps];
+#pragma unroll
+        for (int u = 0; u < kTSteps; ++u) {
+            const int q = s + u < s1 ? s + u : s1 - 1;
+            wv[u] = load16(w + q * 32);
+            xv[u] = load16(x + q * 32);
+        }
+#pragma unroll
+        for (int u = 0; u < kTSteps; ++u) {
+            if (s + u >= s1) break;
+            if constexpr (T::kBf16) {
+                v4i hi, lo;
+                split_f16(wv[u], hi, lo);
+                acc = T::mfma(lo, xv[u], acc);
+                acc = T::mfma(hi, xv[u], acc);
+            } else {
+                acc = T::mfma(wv[u], xv[u], acc);
+            }
+        }
+    }
+    red[wave][lane] = acc;
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int q = 1; q < kTWaves; ++q) {
+        const v4f o = red[q][lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += o[e];
+    }
+    if (row < a.b) *reinterpret_cast<v4f *>(a.t + (slice * a.b + row) * a.r + rank0 + g * 4) = acc;
+}
+
+hipError_t launch_a16_t(const A16Args &a, hipStream_t stream) {
+    const dim3 grid((unsigned)(a.r / 16), (unsigned)((a.b + 15) / 16), (unsigned)a.tks);
+    if (a.bf16)
+        a16_t_kernel<BF16><<<grid, kTWaves * kWave, 0, stream>>>(a);
+    else
+        a16_t_kernel<F16><<<grid, kTWaves * kWave, 0, stream>>>(a);
+    return hipGetLastError();
+}
 
 // acc += T L2 for 16 FM rows and FN panels, this wave's share of the ranks (blocks of 32). T is
 // summed over its slices in order and taken as two bf16 parts (16 significant bits), L2 as its
 // two exact ones: the four products are T L2 up to 2^-17 of T.
 template <int FN, int FM>
-__device__ __forceinline__ void few_lowrank(const A16Args &a, int64_t row0, int64_t last, const int64_t (&chan)[FN], int wave,
-                                            v4f (&acc)[FN][FM]) {
+__device__ __forceinline__ void few_lowrank(const A16Args &a, int64_t row0, int64_t last, const int64_t (&chan)[FN], int share,
+                                            int shares, v4f (&acc)[FN][FM]) {
     const int lane = threadIdx.x % kWave, li = lane & 15, g = lane >> 4;
-    for (int rb = wave; rb * 32 < a.r; rb += kFewWaves) {
+    for (int rb = share; rb * 32 < a.r; rb += shares) {
         const int k = rb * 32 + g * 8, kc = k < a.r ? k : a.r - 8;
         v4i wh[FN], wl[FN];
 #pragma unroll
@@ -50,16 +105,16 @@ __device__ __forceinline__ void few_lowrank(const A16Args &a, int64_t row0, int6
     }
 }
 
-// Few rows: a CTA owns FN panels of 16 channels and up to XR rows; its eight waves split K and
-// their sums are added in wave order.
+// Few rows: groups of KW waves (kw, a power of two) own FN panels of 16 channels and up to XR rows
+// each over a slice of K, which their waves split; the waves' sums are added in wave order.
 template <class T, int FN, int XR, int U>
-__global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a) {
+__global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a, int kw) {
     typedef FewRows<T, FN, XR, 1, U> Rows;
     constexpr int FM = Rows::FM, RED = kFewWaves * FN * FM * 1024;
     __shared__ __align__(16) uint8_t smem[kFewWaves * Rows::LDS > RED ? kFewWaves * Rows::LDS : RED];
-    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int64_t panels = a.n / 16, pieces = a.m / 128, panel0 = (int64_t)blockIdx.x * FN, row0 = (int64_t)blockIdx.y * XR;
-    const int64_t last = row0 + XR < a.b ? row0 + XR : a.b;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), share = wave & (kw - 1);
+    const int64_t panels = a.n / 16, pieces = a.m / 128, row0 = (int64_t)blockIdx.y * XR, slice = blockIdx.z;
+    const int64_t panel0 = ((int64_t)blockIdx.x * kFewWaves + wave) / kw * FN, last = row0 + XR < a.b ? row0 + XR : a.b;
     Rows rows;
     int64_t chan[FN];
 #pragma unroll
@@ -76,44 +131,63 @@ __global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a) {
         rows.x[j] = a.x + (row < last ? row : last - 1) * a.m + lane % 16 * 8;
     }
     v4f acc[FN][FM] = {};
-    rows.template run<true>((int)(wave * pieces / kFewWaves), (int)((wave + 1) * pieces / kFewWaves), smem + wave * Rows::LDS, acc);
-    if (a.r > 0) few_lowrank<FN, FM>(a, row0, last, chan, wave, acc);
-    __syncthreads();
-    v4f *const red = reinterpret_cast<v4f *>(smem);
+    const int64_t part = slice * kw + share, parts = (int64_t)a.ks * kw;
+    if (panel0 < panels) {
+        rows.template run<true>((int)(part * pieces / parts), (int)((part + 1) * pieces / parts), smem + wave * Rows::LDS, acc, [&] {
+            if (a.r > 0 && slice == 0) few_lowrank<FN, FM>(a, row0, last, chan, share, kw, acc);
+        });
+    }
+    join_waves(smem, kw, wave, acc);
+    const int li = lane & 15, g = lane >> 4;
 #pragma unroll
-    for (int f = 0; f < FN; ++f)
+    for (int c = 0; c < FM; ++c) {
+        const int64_t row = row0 + c * 16 + li;
+        if (c % kw != share || row >= last) continue;
 #pragma unroll
-        for (int c = 0; c < FM; ++c) red[((wave * FN + f) * FM + c) * kWave + lane] = acc[f][c];
-    __syncthreads();
-    for (int t = tid; t < FN * FM * kWave; t += kFewWaves * kWave) {
-        v4f s = red[t];
-#pragma unroll
-        for (int w = 1; w < kFewWaves; ++w) {
-            const v4f o = red[w * FN * FM * kWave + t];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] += o[e];
+        for (int f = 0; f < FN; ++f) {
+            if (panel0 + f >= panels) continue;
+            const int64_t at = row * a.n + (panel0 + f) * 16 + g * 4;
+            const v4f s = acc[f][c];
+            if (a.ks > 1)
+                *reinterpret_cast<v4f *>(a.part + slice * a.b * a.n + at) = s;
+            else
+                *reinterpret_cast<uint2 *>(a.y + at) = make_uint2((uint32_t)T::from_f32(s[0]) | (uint32_t)T::from_f32(s[1]) << 16,
+                                                                  (uint32_t)T::from_f32(s[2]) | (uint32_t)T::from_f32(s[3]) << 16);
         }
-        const int64_t panel = panel0 + t / kWave / FM, row = row0 + t / kWave % FM * 16 + t % 16;
-        if (panel < panels && row < last)
-            *reinterpret_cast<uint2 *>(a.y + row * a.n + panel * 16 + t % kWave / 16 * 4) =
-                make_uint2((uint32_t)T::from_f32(s[0]) | (uint32_t)T::from_f32(s[1]) << 16,
-                           (uint32_t)T::from_f32(s[2]) | (uint32_t)T::from_f32(s[3]) << 16);
     }
 }
 
-template <class T, int FN>
-static hipError_t a16_few(const A16Args &a, const A16Plan &p, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.n / 16 + FN - 1) / FN), (unsigned)((a.b + p.rows - 1) / p.rows));
-    constexpr int NT = kFewWaves * kWave;
-    if (p.rows == 4)
-        a16_few_kernel<T, FN, 4, 4><<<grid, NT, 0, stream>>>(a);
-    else if (p.rows == 16)
-        a16_few_kernel<T, FN, 16, 2><<<grid, NT, 0, stream>>>(a);
-    else if (p.rows == 32)
-        a16_few_kernel<T, FN, 32, 1><<<grid, NT, 0, stream>>>(a);
-    else
-        a16_few_kernel<T, FN, 64, 1><<<grid, NT, 0, stream>>>(a);
+// Y = the slices' sums in slice order, rounded once.
+template <class T>
+__global__ __launch_bounds__(256) void a16_join_kernel(const float *part, int ks, int64_t total, uint16_t *y) {
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (at >= total) return;
+    const v4f s = sum_slices(part + at, total, ks);
+    *reinterpret_cast<uint2 *>(y + at) = make_uint2((uint32_t)T::from_f32(s[0]) | (uint32_t)T::from_f32(s[1]) << 16,
+                                                    (uint32_t)T::from_f32(s[2]) | (uint32_t)T::from_f32(s[3]) << 16);
+}
+
+template <class T>
+static hipError_t a16_join(const A16Args &a, hipStream_t stream) {
+    const int64_t total = a.b * a.n;
+    a16_join_kernel<T><<<dim3((unsigned)((total / 4 + 255) / 256)), 256, 0, stream>>>(a.part, a.ks, total, a.y);
     return hipGetLastError();
+}
+
+template <class T, int FN, int XR, int U>
+static hipError_t a16_few(const A16Args &a, const A16Plan &p, hipStream_t stream) {
+    const int64_t groups = (a.n / 16 + FN - 1) / FN, per = kFewWaves / p.kw;
+    const dim3 grid((unsigned)((groups + per - 1) / per), (unsigned)((a.b + XR - 1) / XR), (unsigned)a.ks);
+    a16_few_kernel<T, FN, XR, U><<<grid, kFewWaves * kWave, 0, stream>>>(a, p.kw);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || a.ks == 1 ? e : a16_join<T>(a, stream);
+}
+
+template <class T>
+static hipError_t a16_rows(const A16Args &a, const A16Plan &p, hipStream_t stream) {
+    if (p.rows == 4) return a16_few<T, 1, 4, 2>(a, p, stream);
+    if (p.rows == 16) return p.fn == 1 ? a16_few<T, 1, 16, 1>(a, p, stream) : a16_few<T, 2, 16, 1>(a, p, stream);
+    return p.rows == 32 ? a16_few<T, 2, 32, 1>(a, p, stream) : a16_few<T, 2, 64, 1>(a, p, stream);
 }
 
 // ---- many rows ---------------------------------------------------------------------------
@@ -436,16 +510,6 @@ __global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t nti
     }
 }
 
-// Y = the slices' sums in slice order, rounded once.
-template <class T>
-__global__ __launch_bounds__(256) void a16_join_kernel(const float *part, int ks, int64_t total, uint16_t *y) {
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (at >= total) return;
-    const v4f s = sum_slices(part + at, total, ks);
-    *reinterpret_cast<uint2 *>(y + at) = make_uint2((uint32_t)T::from_f32(s[0]) | (uint32_t)T::from_f32(s[1]) << 16,
-                                                    (uint32_t)T::from_f32(s[2]) | (uint32_t)T::from_f32(s[3]) << 16);
-}
-
 template <class T>
 static hipError_t a16_many(const A16Args &a, const A16Plan &p, hipStream_t stream) {
     const int64_t row_ctas = (a.b + kPrepRows - 1) / kPrepRows, scale_ctas = (a.n + kPrepChannels - 1) / kPrepChannels;
@@ -460,16 +524,12 @@ static hipError_t a16_many(const A16Args &a, const A16Plan &p, hipStream_t strea
     else
         a16_tile_kernel<T, 2><<<grid, 256, 0, stream>>>(a, ntiles, ttiles);
     e = hipGetLastError();
-    if (e != hipSuccess || p.ks == 1) return e;
-    const int64_t total = a.b * a.n;
-    a16_join_kernel<T><<<dim3((unsigned)((total / 4 + 255) / 256)), 256, 0, stream>>>(a.part, p.ks, total, a.y);
-    return hipGetLastError();
+    return e != hipSuccess || p.ks == 1 ? e : a16_join<T>(a, stream);
 }
 
 hipError_t launch_a16(const A16Args &a, const A16Plan &p, hipStream_t stream) {
-    if (a.b > kFewTokens) return a.bf16 ? a16_many<BF16>(a, p, stream) : a16_many<F16>(a, p, stream);
-    if (p.fn == 1) return a.bf16 ? a16_few<BF16, 1>(a, p, stream) : a16_few<F16, 1>(a, p, stream);
-    return a.bf16 ? a16_few<BF16, 2>(a, p, stream) : a16_few<F16, 2>(a, p, stream);
+    if (p.many) return a.bf16 ? a16_many<BF16>(a, p, stream) : a16_many<F16>(a, p, stream);
+    return a.bf16 ? a16_rows<BF16>(a, p, stream) : a16_rows<F16>(a, p, stream);
 }
 
 }  // namespace twq

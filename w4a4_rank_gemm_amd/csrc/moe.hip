@@ -15,113 +15,229 @@ namespace twq {
 
 // Logits in binary64: the products of two 16-bit values are exact in it and their sums all but
 // exact, so that the choice of experts is that of the formula (binary32 sums would swap experts
-// whose logits differ by less than their rounding). A wave owns one expert and kRouteTokens
-// tokens, its lanes split K.
+// whose logits differ by less than their rounding).
+//
+// Few products: a CTA owns one expert and kRouteTokens tokens, its waves and lanes split K, four
+// loads in flight.
 constexpr int kRouteTokens = 4, kRouteWaves = 4;
 
 template <class T>
 __global__ __launch_bounds__(kRouteWaves *kWave) void route_logits_kernel(RouteArgs a) {
-    const int lane = threadIdx.x % kWave, e = blockIdx.x * kRouteWaves + threadIdx.x / kWave;
-    if (e >= a.experts) return;
+    __shared__ double red[kRouteWaves][kRouteTokens];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, e = blockIdx.x;
     const int64_t t0 = (int64_t)blockIdx.y * kRouteTokens;
     const uint16_t *w = a.wr + (int64_t)e * a.m, *x[kRouteTokens];
 #pragma unroll
     for (int t = 0; t < kRouteTokens; ++t) x[t] = a.x + (t0 + t < a.b ? t0 + t : a.b - 1) * a.m;
     double acc[kRouteTokens] = {};
-    for (int64_t k = lane * 8; k < a.m; k += kWave * 8) {
-        const v4i wv = load16(w + k);
-        v4i xv[kRouteTokens];
+    for (int64_t k0 = threadIdx.x * 8; k0 < a.m; k0 += kRouteWaves * kWave * 8 * 4) {
+        v4i wv[4], xv[4][kRouteTokens];
 #pragma unroll
-        for (int t = 0; t < kRouteTokens; ++t) xv[t] = load16(x[t] + k);
+        for (int u = 0; u < 4; ++u) {
+            const int64_t k = k0 + u * kRouteWaves * kWave * 8, kc = k < a.m ? k : 0;
+            wv[u] = load16(w + kc);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const double wd = T::to_f32(half_of(wv[q / 2], q % 2));
+            for (int t = 0; t < kRouteTokens; ++t) xv[u][t] = load16(x[t] + kc);
+        }
 #pragma unroll
-            for (int t = 0; t < kRouteTokens; ++t) acc[t] = __builtin_fma((double)T::to_f32(half_of(xv[t][q / 2], q % 2)), wd, acc[t]);
+        for (int u = 0; u < 4; ++u) {
+            if (k0 + u * kRouteWaves * kWave * 8 >= a.m) break;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const double wd = T::to_f32(half_of(wv[u][q / 2], q % 2));
+#pragma unroll
+                for (int t = 0; t < kRouteTokens; ++t)
+                    acc[t] = __builtin_fma((double)T::to_f32(half_of(xv[u][t][q / 2], q % 2)), wd, acc[t]);
+            }
         }
     }
 #pragma unroll
     for (int t = 0; t < kRouteTokens; ++t) {
         for (int off = 32; off > 0; off >>= 1) acc[t] += __shfl_xor(acc[t], off, kWave);
-        if (lane == 0 && t0 + t < a.b) a.logits[(t0 + t) * a.experts + e] = acc[t];
+        if (lane == 0) red[wave][t] = acc[t];
+    }
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t < kRouteTokens && t0 + t < a.b) {
+        double s = red[0][t];
+        for (int q = 1; q < kRouteWaves; ++q) s += red[q][t];
+        a.logits[(t0 + t) * a.experts + e] = s;
     }
 }
 
-// The k best experts of a token, one wave a token: lane l holds experts l, l + 64, .. Each round
-// takes the largest of what is left, the lowest index among equals. A NaN counts as lowest.
-constexpr int kHeld = kMaxExperts / kWave;
+// Many products: tiles of 16 experts x 16 tokens on binary64 matrix instructions, K split over the
+// CTA's 16 waves, whose sums are added in wave order. Element e of a lane's eight goes to
+// instruction e, for both operands. Result: lane (li, g) holds token li, experts 4 v + g.
+typedef double v4d __attribute__((ext_vector_type(4)));
+constexpr int kTileWaves = 16, kTileSteps = 4;
 
-__global__ __launch_bounds__(kRouteWaves *kWave) void route_choose_kernel(RouteArgs a) {
+template <class T>
+__global__ __launch_bounds__(kTileWaves *kWave) void route_logits_tile_kernel(RouteArgs a) {
+    __shared__ double red[kTileWaves][4][kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, li = lane & 15, g = lane >> 4;
+    const int64_t e0 = (int64_t)blockIdx.x * 16, tok = (int64_t)blockIdx.y * 16 + li, e = e0 + li;
+    const int steps = (int)(a.m / 32), s0 = wave * steps / kTileWaves, s1 = (wave + 1) * steps / kTileWaves;
+    const uint16_t *w = a.wr + (e < a.experts ? e : a.experts - 1) * a.m + g * 8, *x = a.x + (tok < a.b ? tok : a.b - 1) * a.m + g * 8;
+    v4d acc = {0, 0, 0, 0};
+    for (int s = s0; s < s1; s += kTileSteps) {
+        v4i wv[kTileSteps], xv[kTileSteps];
+#pragma unroll
+        for (int u = 0; u < kTileSteps; ++u) {
+            const int q = s + u < s1 ? s + u : s1 - 1;
+            wv[u] = load16(w + q * 32);
+            xv[u] = load16(x + q * 32);
+        }
+#pragma unroll
+        for (int u = 0; u < kTileSteps; ++u) {
+            if (s + u >= s1) break;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)T::to_f32(half_of(wv[u][q / 2], q % 2)),
+                                                           (double)T::to_f32(half_of(xv[u][q / 2], q % 2)), acc, 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) red[wave][v][lane] = acc[v];
+    __syncthreads();
+    if (wave >= 4) return;
+    double s = red[0][wave][lane];
+    for (int q = 1; q < kTileWaves; ++q) s += red[q][wave][lane];
+    if (tok < a.b && e0 + 4 * wave + g < a.experts) a.logits[tok * a.experts + e0 + 4 * wave + g] = s;
+}
+
+// Maximum over the 64 lanes, uniform: within rows of 16 lanes by DPP moves, then over the four rows.
+__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
+    auto step = [&](auto ctrl) {
+        constexpr int C = decltype(ctrl)::value;
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, C, 0xF, 0xF, false);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), C, 0xF, 0xF, false);
+        const uint64_t o = (uint64_t)hi << 32 | lo;
+        v = v > o ? v : o;
+    };
+    step(std::integral_constant<int, 0xB1>{});   // quad_perm [1, 0, 3, 2]
+    step(std::integral_constant<int, 0x4E>{});   // quad_perm [2, 3, 0, 1]
+    step(std::integral_constant<int, 0x141>{});  // row_half_mirror
+    step(std::integral_constant<int, 0x140>{});  // row_mirror
+    uint64_t best = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), r * 16) << 32 |
+                           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, r * 16);
+        best = best > o ? best : o;
+    }
+    return best;
+}
+
+__device__ __forceinline__ double wave_sum_f64(double v) {
+    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+    return v;
+}
+
+// The k best experts of a token by one wave; lane l holds experts l, l + 64, .. as keys whose
+// unsigned order is the order of the values (0: none or taken, 1: NaN). Each round takes the largest
+// key, the lowest index among equals. Probabilities of all experts are formed only where they
+// are asked for: with a bias, or softmax weights that are not divided by their sum.
+__device__ __forceinline__ uint64_t order_key(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 to 0
+    return v == v ? u ^ ((u >> 63) ? ~uint64_t(0) : uint64_t(1) << 63) : 1;
+}
+__device__ __forceinline__ double key_value(uint64_t k) {
+    return __builtin_bit_cast(double, k >> 63 ? k ^ uint64_t(1) << 63 : ~k);
+}
+
+template <int H>
+__device__ __forceinline__ void choose_experts(const RouteArgs &a, int64_t tok) {
     const int lane = threadIdx.x % kWave;
-    const int64_t tok = (int64_t)blockIdx.x * kRouteWaves + threadIdx.x / kWave;
-    if (tok >= a.b) return;
-    const double none = -__builtin_inf();
-    double l[kHeld], p[kHeld], mx = none;
+    double l[H], p[H];
+    uint64_t key[H], best = 0;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < H; ++i) {
         const int e = i * kWave + lane;
-        const double v = e < a.experts ? a.logits[tok * a.experts + e] : none;
-        l[i] = v == v ? v : none;
-        mx = l[i] > mx ? l[i] : mx;
+        l[i] = a.logits[tok * a.experts + (e < a.experts ? e : 0)];
+        key[i] = e < a.experts ? order_key(l[i]) : 0;
+        p[i] = 0;
+        best = best > key[i] ? best : key[i];
     }
-    for (int off = 32; off > 0; off >>= 1) {
-        const double o = __shfl_xor(mx, off, kWave);
-        mx = o > mx ? o : mx;
-    }
-    double sum = 0;
+    const bool every = a.bias || (!a.sigmoid && !a.norm);
+    double top = 0, sum = 1;
+    if (every && !a.sigmoid) {
+        top = key_value(wave_max_u64(best));
+        sum = 0;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        p[i] = i * kWave + lane >= a.experts ? 0.0 : a.sigmoid ? 1.0 / (1.0 + exp(-l[i])) : exp(l[i] - mx);
-        sum += p[i];
-    }
-    if (!a.sigmoid) {
-        for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) p[i] /= sum;
+        for (int i = 0; i < H; ++i) {
+            p[i] = key[i] ? exp(l[i] - top) : 0.0;
+            sum += p[i];
+        }
+        sum = wave_sum_f64(sum);
     }
     if (a.bias) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
+        for (int i = 0; i < H; ++i) {
             const int e = i * kWave + lane;
-            const double v = e < a.experts ? p[i] + (double)a.bias[e] : none;
-            l[i] = v == v ? v : none;
+            p[i] = a.sigmoid ? 1.0 / (1.0 + exp(-l[i])) : p[i] / sum;
+            key[i] = e < a.experts ? order_key(p[i] + (double)a.bias[e]) : 0;
         }
     }
-    uint32_t taken = 0;
     int mine = 0;
-    double weight = 0, total = 0;  // lane j: choice j
+    double value = 0, first = 0;  // of lane j's choice j: its logit, or with a bias its probability
     for (int j = 0; j < a.k; ++j) {
-        double best = none, prob = 0;
-        int at = INT32_MAX;
+        uint64_t k = 0;
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int e = i * kWave + lane;
-            if (e < a.experts && !(taken >> i & 1) && (l[i] > best || at == INT32_MAX)) best = l[i], at = e, prob = p[i];
+        for (int i = 0; i < H; ++i) k = k > key[i] ? k : key[i];
+        k = wave_max_u64(k);
+        int at = -1;
+        double v = key_value(k);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const uint64_t hit = __ballot(key[i] == k);
+            if (at >= 0 || hit == 0) continue;
+            const int o = __builtin_ctzll(hit);
+            at = i * kWave + o;
+            if (lane == o) key[i] = 0;
+            if (a.bias) v = __shfl(p[i], o, kWave);
         }
-        for (int off = 32; off > 0; off >>= 1) {
-            const double o = __shfl_xor(best, off, kWave), q = __shfl_xor(prob, off, kWave);
-            const int w = __shfl_xor(at, off, kWave);
-            if (w != INT32_MAX && (at == INT32_MAX || o > best || (o == best && w < at))) best = o, at = w, prob = q;
-        }
-        if (at % kWave == lane) taken |= 1u << at / kWave;
-        total += prob;
-        if (lane == j) mine = at, weight = prob;
+        if (j == 0) first = v;
+        if (lane == j) mine = at, value = v;
     }
+    double w = 0;
+    if (lane < a.k) w = a.bias ? value : a.sigmoid ? 1.0 / (1.0 + exp(-value)) : exp(value - (every ? top : first)) / sum;
+    const double total = wave_sum_f64(w);
     if (lane < a.k) {
         a.ids[tok * a.k + lane] = mine;
-        a.weights[tok * a.k + lane] = (float)((a.norm ? (total > 0 ? weight / total : 0.0) : weight) * a.scale);
+        a.weights[tok * a.k + lane] = (float)((a.norm ? (total > 0 ? w / total : 0.0) : w) * a.scale);
     }
 }
 
+template <int H>
+__global__ __launch_bounds__(kWave) void route_choose_kernel(RouteArgs a) {
+    choose_experts<H>(a, blockIdx.x);
+}
+
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.experts + kRouteWaves - 1) / kRouteWaves), (unsigned)((a.b + kRouteTokens - 1) / kRouteTokens));
-    if (a.bf16)
-        route_logits_kernel<BF16><<<grid, kRouteWaves * kWave, 0, stream>>>(a);
-    else
-        route_logits_kernel<F16><<<grid, kRouteWaves * kWave, 0, stream>>>(a);
+    const unsigned b = (unsigned)a.b;
+    if (a.b * a.experts >= 16384) {
+        const dim3 grid((unsigned)((a.experts + 15) / 16), (b + 15) / 16);
+        if (a.bf16)
+            route_logits_tile_kernel<BF16><<<grid, kTileWaves * kWave, 0, stream>>>(a);
+        else
+            route_logits_tile_kernel<F16><<<grid, kTileWaves * kWave, 0, stream>>>(a);
+    } else {
+        const dim3 grid((unsigned)a.experts, (b + kRouteTokens - 1) / kRouteTokens);
+        if (a.bf16)
+            route_logits_kernel<BF16><<<grid, kRouteWaves * kWave, 0, stream>>>(a);
+        else
+            route_logits_kernel<F16><<<grid, kRouteWaves * kWave, 0, stream>>>(a);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    route_choose_kernel<<<dim3((unsigned)((a.b + kRouteWaves - 1) / kRouteWaves)), kRouteWaves * kWave, 0, stream>>>(a);
+    if (a.experts <= 64)
+        route_choose_kernel<1><<<b, kWave, 0, stream>>>(a);
+    else if (a.experts <= 128)
+        route_choose_kernel<2><<<b, kWave, 0, stream>>>(a);
+    else if (a.experts <= 256)
+        route_choose_kernel<4><<<b, kWave, 0, stream>>>(a);
+    else
+        route_choose_kernel<8><<<b, kWave, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -131,13 +247,25 @@ constexpr int kMoeWaves = 8, kMoeThreads = kMoeWaves * kWave, kMaxPairs = kMaxMo
 
 // The pairs (token, choice) of this CTA's expert, in order, in `list`; returns their number. With at
 // most as many pairs as experts a slot is a pair, and the first pair of an expert takes all of its
-// pairs; otherwise a slot is an expert. All threads call it.
+// pairs; otherwise a slot is an expert. All threads call it. Up to 64 pairs every wave writes the
+// whole list for itself.
 __device__ __forceinline__ int expert_pairs(const MoeArgs &a, int slot, int &expert, uint16_t *list, int *count) {
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, n = (int)a.b * a.k;
+    const uint64_t below = (uint64_t(1) << lane) - 1;
+    int have = 0;
+    if (n <= kWave) {
+        const int id = lane < n ? a.ids[lane] : -1;
+        expert = n <= a.experts ? __shfl(id, slot, kWave) : slot;
+        if ((unsigned)expert >= (unsigned)a.experts) return 0;
+        const uint64_t hit = __ballot(lane < n && id == expert);
+        if (hit >> lane & 1) list[__popcll(hit & below)] = (uint16_t)lane;
+        wave_fence();
+        have = __popcll(hit);
+        return n <= a.experts && __builtin_ctzll(hit) != slot ? 0 : have;
+    }
     int id = tid < n ? a.ids[tid] : -1;
     expert = n <= a.experts ? a.ids[slot] : slot;
     if ((unsigned)expert >= (unsigned)a.experts) return 0;
-    int have = 0;
     for (int i0 = 0; i0 < n; i0 += kMoeThreads) {
         const int i = i0 + tid;
         if (i0 > 0) id = i < n ? a.ids[i] : -1;
@@ -150,39 +278,22 @@ __device__ __forceinline__ int expert_pairs(const MoeArgs &a, int slot, int &exp
             before += w < wave ? count[w] : 0;
             have += count[w];
         }
-        if (hit >> lane & 1) list[before + __popcll(hit & ((uint64_t(1) << lane) - 1))] = (uint16_t)i;
+        if (hit >> lane & 1) list[before + __popcll(hit & below)] = (uint16_t)i;
         __syncthreads();
     }
     return n <= a.experts && list[0] != slot ? 0 : have;
 }
 
-// The waves' sums, in wave order: element t of FN x 64 lanes for thread t.
-template <int FN>
-__device__ __forceinline__ v4f join_waves(v4f *red, const v4f (&acc)[FN][1], int t) {
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    __syncthreads();
-#pragma unroll
-    for (int f = 0; f < FN; ++f) red[(wave * FN + f) * kWave + lane] = acc[f][0];
-    __syncthreads();
-    v4f s = red[t];
-#pragma unroll
-    for (int w = 1; w < kMoeWaves; ++w) {
-        const v4f o = red[w * FN * kWave + t];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] += o[e];
-    }
-    return s;
-}
-
+// Gate and up rows of one panel of 16 inner channels, kw waves to a panel.
 template <class T, int XR, int U>
-__device__ __forceinline__ void up_tile(const MoeArgs &a, int expert, const uint16_t *list, int rows, uint8_t *smem) {
+__device__ __forceinline__ void up_tile(const MoeArgs &a, int expert, const uint16_t *list, int rows, uint8_t *smem, int wave_lds, int kw) {
     typedef FewRows<T, 2, XR, 1, U> Rows;
-    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int64_t pieces = a.m / 128, half = a.f / 16, panel = blockIdx.x;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), share = wave & (kw - 1);
+    const int64_t pieces = a.m / 128, half = a.f / 16, unit = ((int64_t)blockIdx.x * kMoeWaves + wave) / kw;
     Rows r;
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
-        const int64_t p = expert * 2 * half + f * half + panel;  // gate, up
+        const int64_t p = expert * 2 * half + f * half + (unit < half ? unit : half - 1);  // gate, up
         r.w[f] = a.q1 + p * pieces * 1024;
         r.s[f] = a.s1 + p * 16;
     }
@@ -193,35 +304,32 @@ __device__ __forceinline__ void up_tile(const MoeArgs &a, int expert, const uint
         r.x[j] = a.x + (int64_t)(list[i < rows ? i : rows - 1] / a.k) * a.m + lane % 16 * 8;
     }
     v4f acc[2][1] = {};
-    r.template run<false>((int)(wave * pieces / kMoeWaves), (int)((wave + 1) * pieces / kMoeWaves), smem + wave * Rows::LDS, acc);
-    v4f *const red = reinterpret_cast<v4f *>(smem);
-    const v4f s = join_waves<2>(red, acc, tid % (2 * kWave));
-    __syncthreads();
-    if (tid < 2 * kWave) red[tid] = s;
-    __syncthreads();
+    if (unit < half)
+        r.template run<true>((int)(share * pieces / kw), (int)((share + 1) * pieces / kw), smem + wave * wave_lds, acc, [] {});
+    join_waves(smem, kw, wave, acc);
     // h = silu(gate) up, as two bf16 parts (16 significant bits: one would round as coarsely as a
     // bf16 output, and the type of an fp16 layer could overflow)
-    if (tid < kWave && tid % 16 < rows) {
-        const v4f gate = red[tid], up = red[kWave + tid];
+    if (share == 0 && unit < half && lane % 16 < rows) {
         uint16_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float h = gate[e] / (1.f + __expf(-gate[e])) * up[e];
+            const float gate = acc[0][0][e], h = gate / (1.f + __expf(-gate)) * acc[1][0][e];
             hi[e] = BF16::from_f32(h);
             lo[e] = BF16::from_f32(h - BF16::to_f32(hi[e]));
         }
-        const int64_t c = panel * 16 + tid / 16 * 4;
-        uint16_t *p = a.h + ((int64_t)list[tid % 16] * (a.f / 128) + c / 128) * 256 + c % 128;
+        const int64_t c = unit * 16 + lane / 16 * 4;
+        uint16_t *p = a.h + ((int64_t)list[lane % 16] * (a.f / 128) + c / 128) * 256 + c % 128;
         *reinterpret_cast<uint2 *>(p) = make_uint2((uint32_t)hi[0] | (uint32_t)hi[1] << 16, (uint32_t)hi[2] | (uint32_t)hi[3] << 16);
         *reinterpret_cast<uint2 *>(p + 128) = make_uint2((uint32_t)lo[0] | (uint32_t)lo[1] << 16, (uint32_t)lo[2] | (uint32_t)lo[3] << 16);
     }
 }
 
 template <class T>
-__global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(MoeArgs a) {
-    constexpr int LDS = kMoeWaves * FewRows<T, 2, 16, 1, 2>::LDS;
-    static_assert(LDS >= kMoeWaves * FewRows<T, 2, 4, 1, 4>::LDS && LDS >= kMoeWaves * 2 * 1024, "shared buffer");
-    __shared__ __align__(16) uint8_t smem[LDS];
+__global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a, int kw) {
+    // one place a wave, whatever the rows of a tile: waves may be at different tiles
+    constexpr int LDS = FewRows<T, 2, 16, 1, 1>::LDS;
+    static_assert(LDS >= FewRows<T, 2, 4, 1, 2>::LDS && LDS >= 2 * 1024, "shared buffer");
+    __shared__ __align__(16) uint8_t smem[kMoeWaves * LDS];
     __shared__ uint16_t list[kMaxPairs];
     __shared__ int count[kMoeWaves];
     int expert;
@@ -229,22 +337,24 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(MoeArgs a) {
     for (int i = 0; i < n; i += 16) {
         const int rows = n - i < 16 ? n - i : 16;
         if (rows <= 4)
-            up_tile<T, 4, 4>(a, expert, list + i, rows, smem);
+            up_tile<T, 4, 2>(a, expert, list + i, rows, smem, LDS, kw);
         else
-            up_tile<T, 16, 2>(a, expert, list + i, rows, smem);
-        __syncthreads();
+            up_tile<T, 16, 1>(a, expert, list + i, rows, smem, LDS, kw);
+        if (kw > 1) __syncthreads();
     }
 }
 
+// Two panels of 16 output channels, kw waves to them.
 template <int XR, int U>
-__device__ __forceinline__ void down_tile(const MoeArgs &a, int expert, const uint16_t *list, int rows, uint8_t *smem) {
+__device__ __forceinline__ void down_tile(const MoeArgs &a, int expert, const uint16_t *list, int rows, uint8_t *smem, int wave_lds, int kw) {
     typedef FewRows<BF16, 2, XR, 2, U> Rows;
-    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int64_t pieces = a.f / 128, panels = a.m / 16, panel0 = (int64_t)blockIdx.x * 2;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), share = wave & (kw - 1);
+    const int64_t pieces = a.f / 128, panels = a.m / 16, unit = ((int64_t)blockIdx.x * kMoeWaves + wave) / kw;
+    const bool mine = unit * 2 < panels;  // m is a multiple of 128
     Rows r;
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
-        const int64_t p = expert * panels + panel0 + f;  // m is a multiple of 128
+        const int64_t p = expert * panels + (mine ? unit * 2 + f : 0);
         r.w[f] = a.q2 + p * pieces * 1024;
         r.s[f] = a.s2 + p * 16;
     }
@@ -255,21 +365,26 @@ __device__ __forceinline__ void down_tile(const MoeArgs &a, int expert, const ui
         r.x[j] = a.h + (int64_t)list[i < rows ? i : rows - 1] * a.f * 2 + lane % 16 * 8;
     }
     v4f acc[2][1] = {};
-    r.template run<false>((int)(wave * pieces / kMoeWaves), (int)((wave + 1) * pieces / kMoeWaves), smem + wave * Rows::LDS, acc);
-    v4f s = join_waves<2>(reinterpret_cast<v4f *>(smem), acc, tid % (2 * kWave));
-    if (tid < 2 * kWave && tid % 16 < rows) {
-        const int pair = list[tid % 16];
+    if (mine)
+        r.template run<true>((int)(share * pieces / kw), (int)((share + 1) * pieces / kw), smem + wave * wave_lds, acc, [] {});
+    join_waves(smem, kw, wave, acc);
+    if (share == 0 && mine && lane % 16 < rows) {
+        const int pair = list[lane % 16];
         const float w = a.weights[pair];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] *= w;
-        *reinterpret_cast<v4f *>(a.part + (int64_t)pair * a.m + (panel0 + tid / kWave) * 16 + tid % kWave / 16 * 4) = s;
+        for (int f = 0; f < 2; ++f) {
+            v4f s = acc[f][0];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] *= w;
+            *reinterpret_cast<v4f *>(a.part + (int64_t)pair * a.m + unit * 32 + f * 16 + lane / 16 * 4) = s;
+        }
     }
 }
 
-__global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a) {
-    constexpr int LDS = kMoeWaves * FewRows<BF16, 2, 16, 2, 1>::LDS;
-    static_assert(LDS >= kMoeWaves * FewRows<BF16, 2, 4, 2, 2>::LDS && LDS >= kMoeWaves * 2 * 1024, "shared buffer");
-    __shared__ __align__(16) uint8_t smem[LDS];
+__global__ __launch_bounds__(kMoeThreads, 4) void moe_down_kernel(MoeArgs a, int kw) {
+    constexpr int LDS = FewRows<BF16, 2, 16, 2, 1>::LDS;
+    static_assert(LDS >= FewRows<BF16, 2, 4, 2, 2>::LDS && LDS >= 2 * 1024, "shared buffer");
+    __shared__ __align__(16) uint8_t smem[kMoeWaves * LDS];
     __shared__ uint16_t list[kMaxPairs];
     __shared__ int count[kMoeWaves];
     int expert;
@@ -277,10 +392,10 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a) {
     for (int i = 0; i < n; i += 16) {
         const int rows = n - i < 16 ? n - i : 16;
         if (rows <= 4)
-            down_tile<4, 2>(a, expert, list + i, rows, smem);
+            down_tile<4, 2>(a, expert, list + i, rows, smem, LDS, kw);
         else
-            down_tile<16, 1>(a, expert, list + i, rows, smem);
-        __syncthreads();
+            down_tile<16, 1>(a, expert, list + i, rows, smem, LDS, kw);
+        if (kw > 1) __syncthreads();
     }
 }
 
@@ -300,17 +415,26 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
                                                                  (uint32_t)T::from_f32(s[2]) | (uint32_t)T::from_f32(s[3]) << 16);
 }
 
+// Waves that share a panel's K: until the chip's 1024 SIMDs have two each, while each keeps two pieces.
+static int share_waves(int64_t units, int64_t pieces) {
+    int kw = 1;
+    while (kw < kMoeWaves && units * kw < 2048 && pieces >= kw * 4) kw *= 2;
+    return kw;
+}
+
 hipError_t launch_moe(const MoeArgs &a, hipStream_t stream) {
     const int64_t pairs = a.b * a.k;
     const unsigned slots = (unsigned)(pairs < a.experts ? pairs : a.experts);
-    const dim3 up((unsigned)(a.f / 16), slots), down((unsigned)(a.m / 32), slots);
+    int ku = share_waves(a.f / 16 * slots, a.m / 128), kd = share_waves(a.m / 32 * slots, a.f / 128);
+    const dim3 up((unsigned)((a.f / 16 * ku + kMoeWaves - 1) / kMoeWaves), slots);
+    const dim3 down((unsigned)((a.m / 32 * kd + kMoeWaves - 1) / kMoeWaves), slots);
     if (a.bf16)
-        moe_up_kernel<BF16><<<up, kMoeThreads, 0, stream>>>(a);
+        moe_up_kernel<BF16><<<up, kMoeThreads, 0, stream>>>(a, ku);
     else
-        moe_up_kernel<F16><<<up, kMoeThreads, 0, stream>>>(a);
+        moe_up_kernel<F16><<<up, kMoeThreads, 0, stream>>>(a, ku);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    moe_down_kernel<<<down, kMoeThreads, 0, stream>>>(a);
+    moe_down_kernel<<<down, kMoeThreads, 0, stream>>>(a, kd);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const dim3 join((unsigned)((a.m + 1023) / 1024), (unsigned)a.b);

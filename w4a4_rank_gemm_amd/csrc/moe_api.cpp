@@ -120,27 +120,13 @@ twq_status twq_linear_a16(const void *x, const void *qw, const float *sw, const 
     const hipStream_t st = static_cast<hipStream_t>(stream);
     uint8_t *const ws = static_cast<uint8_t *>(workspace);
     hipError_t e = hipSuccess;
-    if (r > 0) {
-        ShrinkArgs s{};
-        s.v = u16(x);
-        s.w = u16(l1t);
-        s.b = b;
-        s.k = m;
-        s.r = (int)r;
-        s.bf16 = type == TWQ_BF16;
-        s.w_f16 = 1;
-        s.tiles = (b + tile_rows(b) - 1) / tile_rows(b);
-        s.ks = p.tks;
-        s.p = reinterpret_cast<float *>(ws + p.t);
-        e = launch_shrink(s, st);
-        if (e != hipSuccess) return done(e, "twq_linear_a16");
-    }
     A16Args a{};
     a.x = u16(x);
     a.qw = static_cast<const uint8_t *>(qw);
     a.sw = sw;
+    a.l1t = u16(l1t);
     a.l2t = u16(l2t);
-    a.t = reinterpret_cast<const float *>(ws + p.t);
+    a.t = reinterpret_cast<float *>(ws + p.t);
     a.tks = p.tks;
     a.x16 = reinterpret_cast<uint16_t *>(ws + p.x16);
     a.xe = reinterpret_cast<int32_t *>(ws + p.xe);
@@ -157,6 +143,22 @@ twq_status twq_linear_a16(const void *x, const void *qw, const float *sw, const 
     a.n = n;
     a.r = (int)r;
     a.bf16 = type == TWQ_BF16;
+    if (r > 0 && !p.many) e = launch_a16_t(a, st);
+    if (r > 0 && p.many) {
+        ShrinkArgs s{};
+        s.v = u16(x);
+        s.w = u16(l1t);
+        s.b = b;
+        s.k = m;
+        s.r = (int)r;
+        s.bf16 = type == TWQ_BF16;
+        s.w_f16 = 1;
+        s.tiles = (b + tile_rows(b) - 1) / tile_rows(b);
+        s.ks = p.tks;
+        s.p = a.t;
+        e = launch_shrink(s, st);
+    }
+    if (e != hipSuccess) return done(e, "twq_linear_a16");
     return done(launch_a16(a, p, st), "twq_linear_a16");
 }
 

@@ -160,13 +160,23 @@ DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
 A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     A16Plan p{};
-    p.tks = r > 0 ? shrink_slices(b, m, r, (b + tile_rows(b) - 1) / tile_rows(b), 4) : 0;
+    p.many = b > kFewTokens;
+    if (r > 0 && p.many) p.tks = shrink_slices(b, m, r, (b + tile_rows(b) - 1) / tile_rows(b), 4);
+    if (r > 0 && !p.many) p.tks = m >= 16384 ? 16 : (int)((m + 1023) / 1024);
     p.ks = 1;
     p.x16 = up((size_t)p.tks * b * r * 4);
     p.total = p.x16;
-    if (b <= kFewTokens) {
+    if (!p.many) {
+        const int64_t panels = n / 16, pieces = m / 128;
         p.rows = b <= 4 ? 4 : b <= 16 ? 16 : b <= 32 ? 32 : 64;
-        p.fn = n / 16 >= 1024 ? 2 : 1;
+        p.fn = p.rows == 4 || (p.rows == 16 && panels < 512) ? 1 : 2;
+        const int64_t units = (panels + p.fn - 1) / p.fn;
+        p.kw = 1;
+        while (p.kw < 8 && units * p.kw < (p.rows == 4 ? 3072 : 1536) && pieces >= p.kw * 2) p.kw *= 2;
+        if (p.rows >= 32)
+            while (p.ks < 8 && units * p.kw * p.ks < 2048 && pieces >= p.kw * p.ks * 4) p.ks *= 2;
+        p.part = p.x16;
+        p.total = p.part + (p.ks > 1 ? up((size_t)p.ks * b * n * 4) : 0);
         return p;
     }
     const int64_t groups = m / 128, ntiles = (n + kA16N - 1) / kA16N;

@@ -79,8 +79,9 @@ struct FewRows {
     int64_t s_stride;          // floats between groups
     const uint16_t *x[XL];     // this lane's rows 4 j + lane / 16 at element 8 (lane % 16)
 
-    template <bool STREAM>
-    __device__ __forceinline__ void run(int p0, int p1, uint8_t *lds, v4f (&acc)[FN][FM]) const {
+    // `between` runs after the first loads are issued.
+    template <bool STREAM, class F>
+    __device__ __forceinline__ void run(int p0, int p1, uint8_t *lds, v4f (&acc)[FN][FM], F &&between) const {
         const int lane = threadIdx.x % kWave, li = lane & 15, g = lane >> 4;
         const Codes<T> codes;
         v4i wn[U][FN], xn[U][PARTS][XL];
@@ -103,8 +104,9 @@ struct FewRows {
 #pragma unroll
             for (int f = 0; f < FN; ++f) sn[f] = s[f][q * s_stride + li];
         };
-        if (p0 >= p1) return;
+        if (p0 >= p1) return between();
         load(p0);
+        between();
         float *const scales = reinterpret_cast<float *>(lds + U * PIECE);
         const int put = ((lane & 3) * 4 + ((lane >> 2) & 3)) * SLOT + g * 16;  // chunk lane % 16 = 4 quarter + instruction
         const int get = g * SLOT + (XR < 16 && li >= XR ? XR - 1 : li) * 16;
@@ -159,5 +161,36 @@ struct FewRows {
         wave_fence();
     }
 };
+
+// The sums of the KW waves (a power of two) that share a panel group's K, neighbours `wave / KW`
+// in a CTA: wave kw of them gets the sums of row blocks c = kw, kw + KW, .. in acc, added in wave
+// order. All threads of the CTA call it; `red` holds FN FM KB a wave.
+template <int FN, int FM>
+__device__ __forceinline__ void join_waves(uint8_t *smem, int kw_count, int wave, v4f (&acc)[FN][FM]) {
+    if (kw_count == 1) return;
+    const int lane = threadIdx.x % kWave;
+    v4f *const red = reinterpret_cast<v4f *>(smem) + lane;
+    __syncthreads();
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+#pragma unroll
+        for (int c = 0; c < FM; ++c) red[((wave * FN + f) * FM + c) * kWave] = acc[f][c];
+    __syncthreads();
+    const int first = wave & -kw_count;
+#pragma unroll
+    for (int c = 0; c < FM; ++c) {
+        if (c % kw_count != wave - first) continue;
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+            v4f s = red[((first * FN + f) * FM + c) * kWave];
+            for (int w = 1; w < kw_count; ++w) {
+                const v4f o = red[(((first + w) * FN + f) * FM + c) * kWave];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] += o[e];
+            }
+            acc[f][c] = s;
+        }
+    }
+}
 
 }  // namespace twq

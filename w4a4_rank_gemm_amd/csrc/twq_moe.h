@@ -19,8 +19,9 @@ struct A16Args {
     const uint16_t *x;    // [b][m]
     const uint8_t *qw;    // panels
     const float *sw;      // [m / 128][n]
+    const uint16_t *l1t;  // [r][m] fp16
     const uint16_t *l2t;  // [n][r] fp16
-    const float *t;       // [tks][b][r] partial sums of X L1
+    float *t;             // [tks][b][r] partial sums of X L1
     int tks;
     uint16_t *y;          // [b][n]
     int64_t b, m, n;
@@ -39,13 +40,15 @@ struct A16Args {
 };
 
 struct A16Plan {
+    int many;      // the tile kernel
     int rows;      // token rows a CTA
-    int fn;        // few rows: panels a CTA
+    int fn, kw;    // few rows: panels of a wave, waves that share their K
     int tks;       // K slices of X L1
-    int ks;        // tile kernel: K slices
+    int ks;        // K slices of the product
     size_t t, x16, xe, mul, mask, unit, t16, te, part, total;
 };
 A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r);  // plan.cpp
+hipError_t launch_a16_t(const A16Args &a, hipStream_t stream);  // few rows: t
 hipError_t launch_a16(const A16Args &a, const A16Plan &p, hipStream_t stream);
 
 // ---- the routed layer ------------------------------------------------------------------------
