@@ -102,7 +102,9 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t) {
     return hipSuccess;
 }
 
-hipError_t launch_moe(const MoeArgs &a, hipStream_t) {
+hipError_t launch_moe(const MoeArgs &a, const MoePlan &p, hipStream_t) {
+    if (p.slots < 1 || p.slots > a.b * a.k || p.slots > a.experts || a.ks < 1 || p.few != (a.b <= kFewMoe) || (p.few && p.up_shared))
+        return hipErrorInvalidValue;
     rd(a.x, a.b * a.m * 2);
     rd(a.ids, a.b * a.k * 4);
     rd(a.weights, a.b * a.k * 4);
@@ -111,7 +113,12 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t) {
     rd(a.q2, a.experts * a.m * a.f / 2);
     rd(a.s2, a.f / 128 * a.experts * a.m * 4);
     wr(a.h, a.b * a.k * a.f * 4);
-    wr(a.part, a.b * a.k * a.m * 4);
+    if (p.few) {
+        wr(a.entries, a.b * a.k * sizeof(MoeEntry));
+        wr(a.entry_count, 4);
+    } else {
+        wr(a.part, a.ks * a.b * a.k * a.m * 4);
+    }
     wr(a.y, a.b * a.m * 2);
     return hipSuccess;
 }
@@ -169,7 +176,7 @@ int main() {
     for (const auto &c : layers)
         for (int type : {TWQ_F16, TWQ_BF16}) layer(c[0], c[1], c[2], c[3], type);
     const int64_t moes[][5] = {{0, 256, 128, 4, 2}, {1, 128, 128, 1, 1}, {1, 512, 384, 64, 8}, {3, 256, 256, 5, 5}, {17, 384, 128, 60, 4},
-                               {256, 128, 128, 16, 16}, {100, 256, 128, 512, 3}};
+                               {256, 128, 128, 16, 16}, {100, 256, 128, 512, 3}, {16, 128, 256, 20, 16}, {20, 128, 8192, 2, 2}};
     for (const auto &c : moes)
         for (int type : {TWQ_F16, TWQ_BF16}) routed(c[0], c[1], c[2], c[3], c[4], type);
     if (g_fail) {

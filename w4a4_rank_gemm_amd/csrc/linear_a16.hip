@@ -105,6 +105,30 @@ __device__ __forceinline__ void few_lowrank(const A16Args &a, int64_t row0, int6
     }
 }
 
+// Stores the row blocks c = share, share + shares, .. of FN panels: Y, or this slice's sums.
+template <class T, int FN, int FM>
+__device__ __forceinline__ void a16_store(const A16Args &a, const v4f (&acc)[FN][FM], int64_t row0, int64_t last, int64_t panel0,
+                                          int64_t slice, int shares, int share) {
+    const int64_t panels = a.n / 16;
+    const int lane = threadIdx.x % kWave, li = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int c = 0; c < FM; ++c) {
+        const int64_t row = row0 + c * 16 + li;
+        if (c % shares != share || row >= last) continue;
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+            if (panel0 + f >= panels) continue;
+            const int64_t at = row * a.n + (panel0 + f) * 16 + g * 4;
+            const v4f s = acc[f][c];
+            if (a.ks > 1)
+                *reinterpret_cast<v4f *>(a.part + slice * a.b * a.n + at) = s;
+            else
+                *reinterpret_cast<uint2 *>(a.y + at) = make_uint2((uint32_t)T::from_f32(s[0]) | (uint32_t)T::from_f32(s[1]) << 16,
+                                                                  (uint32_t)T::from_f32(s[2]) | (uint32_t)T::from_f32(s[3]) << 16);
+        }
+    }
+}
+
 // Few rows: groups of KW waves (kw, a power of two) own FN panels of 16 channels and up to XR rows
 // each over a slice of K, which their waves split; the waves' sums are added in wave order.
 template <class T, int FN, int XR, int U>
@@ -138,23 +162,38 @@ __global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a, in
         });
     }
     join_waves(smem, kw, wave, acc);
-    const int li = lane & 15, g = lane >> 4;
+    a16_store<T, FN, FM>(a, acc, row0, last, panel0, slice, kw, share);
+}
+
+// The same with rows and K shared by the CTA's eight waves, FN panels each (SharedRows).
+template <class T, int FN, int XR, int U>
+__global__ __launch_bounds__(kSharedWaves *kWave) void a16_shared_kernel(A16Args a) {
+    typedef SharedRows<T, FN, XR, 1, U> Rows;
+    constexpr int FM = Rows::FM;
+    __shared__ __align__(16) uint8_t smem[Rows::LDS];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t panels = a.n / 16, pieces = a.m / 128, row0 = (int64_t)blockIdx.y * XR, slice = blockIdx.z;
+    const int64_t panel0 = ((int64_t)blockIdx.x * kSharedWaves + wave) * FN, last = row0 + XR < a.b ? row0 + XR : a.b;
+    Rows rows;
+    int64_t chan[FN];
 #pragma unroll
-    for (int c = 0; c < FM; ++c) {
-        const int64_t row = row0 + c * 16 + li;
-        if (c % kw != share || row >= last) continue;
-#pragma unroll
-        for (int f = 0; f < FN; ++f) {
-            if (panel0 + f >= panels) continue;
-            const int64_t at = row * a.n + (panel0 + f) * 16 + g * 4;
-            const v4f s = acc[f][c];
-            if (a.ks > 1)
-                *reinterpret_cast<v4f *>(a.part + slice * a.b * a.n + at) = s;
-            else
-                *reinterpret_cast<uint2 *>(a.y + at) = make_uint2((uint32_t)T::from_f32(s[0]) | (uint32_t)T::from_f32(s[1]) << 16,
-                                                                  (uint32_t)T::from_f32(s[2]) | (uint32_t)T::from_f32(s[3]) << 16);
-        }
+    for (int f = 0; f < FN; ++f) {
+        const int64_t p = panel0 + f < panels ? panel0 + f : panels - 1;
+        chan[f] = p * 16;
+        rows.w[f] = a.qw + p * pieces * 1024;
+        rows.s[f] = a.sw + p * 16;
     }
+    rows.s_stride = a.n;
+#pragma unroll
+    for (int j = 0; j < Rows::PER; ++j) {
+        const int64_t row = row0 + Rows::row_of(j);
+        rows.x[j] = a.x + (row < last ? row : last - 1) * a.m + Rows::offset_of(j);
+    }
+    v4f acc[FN][FM] = {};
+    rows.run((int)(slice * pieces / a.ks), (int)((slice + 1) * pieces / a.ks), smem, acc, [&] {
+        if (a.r > 0 && slice == 0) few_lowrank<FN, FM>(a, row0, last, chan, 0, 1, acc);
+    });
+    a16_store<T, FN, FM>(a, acc, row0, last, panel0, slice, 1, 0);
 }
 
 // Y = the slices' sums in slice order, rounded once.
@@ -183,11 +222,21 @@ static hipError_t a16_few(const A16Args &a, const A16Plan &p, hipStream_t stream
     return e != hipSuccess || a.ks == 1 ? e : a16_join<T>(a, stream);
 }
 
+template <class T, int FN, int XR, int U>
+static hipError_t a16_shared(const A16Args &a, hipStream_t stream) {
+    const int64_t groups = (a.n / 16 + FN - 1) / FN;
+    const dim3 grid((unsigned)((groups + kSharedWaves - 1) / kSharedWaves), (unsigned)((a.b + XR - 1) / XR), (unsigned)a.ks);
+    a16_shared_kernel<T, FN, XR, U><<<grid, kSharedWaves * kWave, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || a.ks == 1 ? e : a16_join<T>(a, stream);
+}
+
 template <class T>
 static hipError_t a16_rows(const A16Args &a, const A16Plan &p, hipStream_t stream) {
     if (p.rows == 4) return a16_few<T, 1, 4, 2>(a, p, stream);
     if (p.rows == 16) return p.fn == 1 ? a16_few<T, 1, 16, 1>(a, p, stream) : a16_few<T, 2, 16, 1>(a, p, stream);
-    return p.rows == 32 ? a16_few<T, 2, 32, 1>(a, p, stream) : a16_few<T, 2, 64, 1>(a, p, stream);
+    if (p.rows == 32) return a16_shared<T, 1, 32, 2>(a, stream);
+    return p.fn == 1 ? a16_shared<T, 1, 64, 2>(a, stream) : a16_shared<T, 2, 64, 2>(a, stream);
 }
 
 // ---- many rows ---------------------------------------------------------------------------

@@ -105,27 +105,13 @@ __global__ __launch_bounds__(kTileWaves *kWave) void route_logits_tile_kernel(Ro
     if (tok < a.b && e0 + 4 * wave + g < a.experts) a.logits[tok * a.experts + e0 + 4 * wave + g] = s;
 }
 
-// Maximum over the 64 lanes, uniform: within rows of 16 lanes by DPP moves, then over the four rows.
+// Maximum over the 64 lanes, uniform: the upper halves first, the lower ones among those that tie.
 __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
-    auto step = [&](auto ctrl) {
-        constexpr int C = decltype(ctrl)::value;
-        const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, C, 0xF, 0xF, false);
-        const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), C, 0xF, 0xF, false);
-        const uint64_t o = (uint64_t)hi << 32 | lo;
-        v = v > o ? v : o;
-    };
-    step(std::integral_constant<int, 0xB1>{});   // quad_perm [1, 0, 3, 2]
-    step(std::integral_constant<int, 0x4E>{});   // quad_perm [2, 3, 0, 1]
-    step(std::integral_constant<int, 0x141>{});  // row_half_mirror
-    step(std::integral_constant<int, 0x140>{});  // row_mirror
-    uint64_t best = 0;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), r * 16) << 32 |
-                           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, r * 16);
-        best = best > o ? best : o;
-    }
-    return best;
+    const uint32_t hi = (uint32_t)(v >> 32), top = wave_max_u32(hi);
+    const uint64_t tied = __ballot(hi == top);
+    const uint32_t low = tied & (tied - 1) ? wave_max_u32(hi == top ? (uint32_t)v : 0)
+                                           : (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, __builtin_ctzll(tied));
+    return (uint64_t)top << 32 | low;
 }
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
@@ -208,9 +194,15 @@ __device__ __forceinline__ void choose_experts(const RouteArgs &a, int64_t tok) 
     }
 }
 
-template <int H>
 __global__ __launch_bounds__(kWave) void route_choose_kernel(RouteArgs a) {
-    choose_experts<H>(a, blockIdx.x);
+    if (a.experts <= kWave)
+        choose_experts<1>(a, blockIdx.x);
+    else if (a.experts <= 2 * kWave)
+        choose_experts<2>(a, blockIdx.x);
+    else if (a.experts <= 4 * kWave)
+        choose_experts<4>(a, blockIdx.x);
+    else
+        choose_experts<8>(a, blockIdx.x);
 }
 
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
@@ -230,14 +222,7 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (a.experts <= 64)
-        route_choose_kernel<1><<<b, kWave, 0, stream>>>(a);
-    else if (a.experts <= 128)
-        route_choose_kernel<2><<<b, kWave, 0, stream>>>(a);
-    else if (a.experts <= 256)
-        route_choose_kernel<4><<<b, kWave, 0, stream>>>(a);
-    else
-        route_choose_kernel<8><<<b, kWave, 0, stream>>>(a);
+    route_choose_kernel<<<(unsigned)a.b, kWave, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -284,6 +269,22 @@ __device__ __forceinline__ int expert_pairs(const MoeArgs &a, int slot, int &exp
     return n <= a.experts && list[0] != slot ? 0 : have;
 }
 
+// h = silu(gate) up of four channels of a panel and one pair, as two bf16 parts (16 significant bits:
+// one would round as coarsely as a bf16 output, and the type of an fp16 layer could overflow).
+__device__ __forceinline__ void store_inner(const MoeArgs &a, const v4f &gate, const v4f &up, int pair, int64_t panel) {
+    uint16_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float h = gate[e] / (1.f + __expf(-gate[e])) * up[e];
+        hi[e] = BF16::from_f32(h);
+        lo[e] = BF16::from_f32(h - BF16::to_f32(hi[e]));
+    }
+    const int64_t c = panel * 16 + threadIdx.x % kWave / 16 * 4;
+    uint16_t *p = a.h + ((int64_t)pair * (a.f / 128) + c / 128) * 256 + c % 128;
+    *reinterpret_cast<uint2 *>(p) = make_uint2((uint32_t)hi[0] | (uint32_t)hi[1] << 16, (uint32_t)hi[2] | (uint32_t)hi[3] << 16);
+    *reinterpret_cast<uint2 *>(p + 128) = make_uint2((uint32_t)lo[0] | (uint32_t)lo[1] << 16, (uint32_t)lo[2] | (uint32_t)lo[3] << 16);
+}
+
 // Gate and up rows of one panel of 16 inner channels, kw waves to a panel.
 template <class T, int XR, int U>
 __device__ __forceinline__ void up_tile(const MoeArgs &a, int expert, const uint16_t *list, int rows, uint8_t *smem, int wave_lds, int kw) {
@@ -307,31 +308,68 @@ __device__ __forceinline__ void up_tile(const MoeArgs &a, int expert, const uint
     if (unit < half)
         r.template run<true>((int)(share * pieces / kw), (int)((share + 1) * pieces / kw), smem + wave * wave_lds, acc, [] {});
     join_waves(smem, kw, wave, acc);
-    // h = silu(gate) up, as two bf16 parts (16 significant bits: one would round as coarsely as a
-    // bf16 output, and the type of an fp16 layer could overflow)
-    if (share == 0 && unit < half && lane % 16 < rows) {
-        uint16_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float gate = acc[0][0][e], h = gate / (1.f + __expf(-gate)) * acc[1][0][e];
-            hi[e] = BF16::from_f32(h);
-            lo[e] = BF16::from_f32(h - BF16::to_f32(hi[e]));
-        }
-        const int64_t c = unit * 16 + lane / 16 * 4;
-        uint16_t *p = a.h + ((int64_t)list[lane % 16] * (a.f / 128) + c / 128) * 256 + c % 128;
-        *reinterpret_cast<uint2 *>(p) = make_uint2((uint32_t)hi[0] | (uint32_t)hi[1] << 16, (uint32_t)hi[2] | (uint32_t)hi[3] << 16);
-        *reinterpret_cast<uint2 *>(p + 128) = make_uint2((uint32_t)lo[0] | (uint32_t)lo[1] << 16, (uint32_t)lo[2] | (uint32_t)lo[3] << 16);
-    }
+    if (share == 0 && unit < half && lane % 16 < rows) store_inner(a, acc[0][0], acc[1][0], list[lane % 16], unit);
 }
 
+// The work list of the down kernel for few tokens: the experts asked for, each with its pairs, at most
+// one a token (an expert that a token names again is another entry). One CTA, in its LDS.
+struct EntryScratch {
+    int32_t id[kFewPairs], again[kFewPairs], number[kFewPairs];
+    MoeEntry entries[kFewPairs];
+};
+__device__ __forceinline__ void expert_entries(const MoeArgs &a, EntryScratch &s) {
+    const int i = threadIdx.x, n = (int)a.b * a.k;  // at most kFewPairs, fewer than threads
+    const int id = i < n ? a.ids[i] : -1;
+    const bool on = (unsigned)id < (unsigned)a.experts;
+    if (i < n) s.id[i] = id;
+    __syncthreads();
+    int turn = 0, first = i, at = 0;  // how often its token named the expert before; the entry's first pair; place in the entry
+    if (on)
+        for (int j = i / a.k * a.k; j < i; ++j) turn += s.id[j] == id;
+    if (i < n) s.again[i] = turn;
+    __syncthreads();
+    if (on)
+        for (int j = i - 1; j >= 0; --j)
+            if (s.id[j] == id && s.again[j] == turn) first = j, ++at;
+    if (i < n) s.number[i] = on && first == i;
+    __syncthreads();
+    int entry = 0, rows = 0, all = 0;
+    for (int j = 0; on && j < n; ++j) {
+        entry += j < first ? s.number[j] : 0;
+        rows += s.id[j] == id && s.again[j] == turn;
+    }
+    MoeEntry &e = s.entries[entry];
+    if (on && first == i) {
+        e.expert = id;
+        e.rows = rows;
+        for (int t = 0; t < kFewMoe; ++t) e.place[t] = -1;
+    }
+    for (int j = 0; i == 0 && j < n; ++j) all += s.number[j];
+    __syncthreads();
+    if (on) {
+        e.pair[at] = (int16_t)i;
+        e.place[i / a.k] = (int8_t)at;
+    }
+    if (i == 0) *a.entry_count = all;
+    __syncthreads();
+    for (int j = i; j < n * (int)(sizeof(MoeEntry) / 16); j += kMoeThreads)
+        reinterpret_cast<v4i *>(a.entries)[j] = reinterpret_cast<const v4i *>(s.entries)[j];
+}
+
+// kw waves to a panel of gate and up rows. One more row of CTAs than there are slots (few tokens)
+// makes the down kernel's work list.
 template <class T>
-__global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a, int kw) {
+__global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a, int slots, int kw) {
     // one place a wave, whatever the rows of a tile: waves may be at different tiles
     constexpr int LDS = FewRows<T, 2, 16, 1, 1>::LDS;
-    static_assert(LDS >= FewRows<T, 2, 4, 1, 2>::LDS && LDS >= 2 * 1024, "shared buffer");
+    static_assert(LDS >= FewRows<T, 2, 4, 1, 2>::LDS && LDS >= 2 * 1024 && kMoeWaves * LDS >= (int)sizeof(EntryScratch), "shared buffer");
     __shared__ __align__(16) uint8_t smem[kMoeWaves * LDS];
     __shared__ uint16_t list[kMaxPairs];
     __shared__ int count[kMoeWaves];
+    if ((int)blockIdx.y == slots) {
+        if (blockIdx.x == 0) expert_entries(a, *reinterpret_cast<EntryScratch *>(smem));
+        return;
+    }
     int expert;
     const int n = expert_pairs(a, blockIdx.y, expert, list, count);
     for (int i = 0; i < n; i += 16) {
@@ -344,62 +382,130 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a, int k
     }
 }
 
-// Two panels of 16 output channels, kw waves to them.
-template <int XR, int U>
-__device__ __forceinline__ void down_tile(const MoeArgs &a, int expert, const uint16_t *list, int rows, uint8_t *smem, int wave_lds, int kw) {
-    typedef FewRows<BF16, 2, XR, 2, U> Rows;
-    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), share = wave & (kw - 1);
-    const int64_t pieces = a.f / 128, panels = a.m / 16, unit = ((int64_t)blockIdx.x * kMoeWaves + wave) / kw;
-    const bool mine = unit * 2 < panels;  // m is a multiple of 128
-    Rows r;
+// Few tokens: a CTA owns a panel of 16 output channels and all of the work list, whose pieces its 16
+// waves split evenly; a wave adds its products to its tokens' sums with their weights, the waves'
+// sums are added in wave order and rounded once. No partial output reaches memory.
+constexpr int kDownWaves = 16, kDownThreads = kDownWaves * kWave;
+
+template <class T>
+__global__ __launch_bounds__(kDownThreads) void moe_down_few_kernel(MoeArgs a) {
+    typedef FewRows<BF16, 1, kFewMoe, 2, 2> Rows;
+    __shared__ __align__(16) uint8_t smem[kDownWaves * Rows::LDS];
+    __shared__ MoeEntry entries[kFewPairs];
+    __shared__ float weights[kFewPairs];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave), n = (int)a.b * a.k;
+    const int li = lane & 15, g = lane >> 4;
+    if (tid < n) weights[tid] = a.weights[tid];
+    if (tid < n * (int)(sizeof(MoeEntry) / 16))  // entries past the last are not used
+        reinterpret_cast<v4i *>(entries)[tid] = load16(reinterpret_cast<const uint8_t *>(a.entries) + tid * 16);
+    const int pieces = (int)(a.f / 128), all = *a.entry_count * pieces, u1 = (int)((int64_t)(wave + 1) * all / kDownWaves);
+    const int64_t panel = xcd_range(blockIdx.x, gridDim.x);  // neighbours share lines of scales
+    __syncthreads();
+    v4f sum[1][1] = {};
+    for (int u = (int)((int64_t)wave * all / kDownWaves); u < u1;) {
+        const MoeEntry &e = entries[u / pieces];
+        const int p0 = u % pieces, p1 = pieces - p0 < u1 - u ? pieces : p0 + u1 - u;
+        const int64_t p = e.expert * (a.m / 16) + panel;
+        Rows r;
+        r.w[0] = a.q2 + p * pieces * 1024;
+        r.s[0] = a.s2 + p * 16;
+        r.s_stride = a.experts * a.m;
+        r.x[0] = a.h + (int64_t)e.pair[g < e.rows ? g : e.rows - 1] * a.f * 2 + li * 8;
+        v4f acc[1][1] = {};
+        r.template run<true>(p0, p1, smem + wave * Rows::LDS, acc, [] {});
+        const int place = li < kFewMoe ? e.place[li] : -1;  // column of this lane's token
+        const float w = place < 0 ? 0.f : weights[e.pair[place]];
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-        const int64_t p = expert * panels + (mine ? unit * 2 + f : 0);
-        r.w[f] = a.q2 + p * pieces * 1024;
-        r.s[f] = a.s2 + p * 16;
-    }
-    r.s_stride = a.experts * a.m;
-#pragma unroll
-    for (int j = 0; j < Rows::XL; ++j) {
-        const int i = 4 * j + lane / 16;
-        r.x[j] = a.h + (int64_t)list[i < rows ? i : rows - 1] * a.f * 2 + lane % 16 * 8;
-    }
-    v4f acc[2][1] = {};
-    if (mine)
-        r.template run<true>((int)(share * pieces / kw), (int)((share + 1) * pieces / kw), smem + wave * wave_lds, acc, [] {});
-    join_waves(smem, kw, wave, acc);
-    if (share == 0 && mine && lane % 16 < rows) {
-        const int pair = list[lane % 16];
-        const float w = a.weights[pair];
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-            v4f s = acc[f][0];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] *= w;
-            *reinterpret_cast<v4f *>(a.part + (int64_t)pair * a.m + unit * 32 + f * 16 + lane / 16 * 4) = s;
+        for (int q = 0; q < 4; ++q) {
+            const float v = __shfl(acc[0][0][q], (lane & 48) + (place < 0 ? 0 : place), kWave);
+            if (place >= 0) sum[0][0][q] += w * v;
         }
+        u += p1 - p0;
+    }
+    join_waves(smem, kDownWaves, wave, sum);
+    if (wave == 0 && li < a.b) {
+        const v4f s = sum[0][0];
+        *reinterpret_cast<uint2 *>(a.y + li * a.m + panel * 16 + g * 4) =
+            make_uint2((uint32_t)T::from_f32(s[0]) | (uint32_t)T::from_f32(s[1]) << 16,
+                       (uint32_t)T::from_f32(s[2]) | (uint32_t)T::from_f32(s[3]) << 16);
     }
 }
 
-__global__ __launch_bounds__(kMoeThreads, 4) void moe_down_kernel(MoeArgs a, int kw) {
-    constexpr int LDS = FewRows<BF16, 2, 16, 2, 1>::LDS;
-    static_assert(LDS >= FewRows<BF16, 2, 4, 2, 2>::LDS && LDS >= 2 * 1024, "shared buffer");
-    __shared__ __align__(16) uint8_t smem[kMoeWaves * LDS];
+// Many rows an expert, or many experts: the CTA's eight waves share an expert's rows and K, and own
+// eight panels of inner (output) channels each.
+template <class T, int XR, int U>
+__global__ __launch_bounds__(kMoeThreads) void moe_up_shared_kernel(MoeArgs a) {
+    typedef SharedRows<T, 2, XR, 1, U> Rows;
+    __shared__ __align__(16) uint8_t smem[Rows::LDS];
     __shared__ uint16_t list[kMaxPairs];
     __shared__ int count[kMoeWaves];
     int expert;
     const int n = expert_pairs(a, blockIdx.y, expert, list, count);
-    for (int i = 0; i < n; i += 16) {
-        const int rows = n - i < 16 ? n - i : 16;
-        if (rows <= 4)
-            down_tile<4, 2>(a, expert, list + i, rows, smem, LDS, kw);
-        else
-            down_tile<16, 1>(a, expert, list + i, rows, smem, LDS, kw);
-        if (kw > 1) __syncthreads();
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t pieces = a.m / 128, half = a.f / 16, panel = (int64_t)blockIdx.x * kMoeWaves + wave;  // f is a multiple of 128
+    Rows r;
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+        const int64_t p = expert * 2 * half + f * half + panel;
+        r.w[f] = a.q1 + p * pieces * 1024;
+        r.s[f] = a.s1 + p * 16;
+    }
+    r.s_stride = a.experts * 2 * a.f;
+    for (int i = 0; i < n; i += XR) {
+        const int rows = n - i < XR ? n - i : XR;
+#pragma unroll
+        for (int j = 0; j < Rows::PER; ++j) {
+            const int row = Rows::row_of(j);
+            r.x[j] = a.x + (int64_t)(list[i + (row < rows ? row : rows - 1)] / a.k) * a.m + Rows::offset_of(j);
+        }
+        v4f acc[2][Rows::FM] = {};
+        r.run(0, (int)pieces, smem, acc, [] {});
+#pragma unroll
+        for (int c = 0; c < Rows::FM; ++c)
+            if (c * 16 + lane % 16 < rows) store_inner(a, acc[0][c], acc[1][c], list[i + c * 16 + lane % 16], panel);
+        __syncthreads();
     }
 }
 
-// y = the sum of a token's weighted parts, in the order of its choices, rounded once.
+template <int XR>
+__global__ __launch_bounds__(kMoeThreads) void moe_down_shared_kernel(MoeArgs a) {
+    typedef SharedRows<BF16, 1, XR, 2, 1> Rows;
+    __shared__ __align__(16) uint8_t smem[Rows::LDS];
+    __shared__ uint16_t list[kMaxPairs];
+    __shared__ int count[kMoeWaves];
+    int expert;
+    const int n = expert_pairs(a, blockIdx.y, expert, list, count);
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t pieces = a.f / 128, panel = (int64_t)blockIdx.x * kMoeWaves + wave, p = expert * (a.m / 16) + panel;  // m is a multiple of 128
+    const int64_t slice = blockIdx.z;
+    Rows r;
+    r.w[0] = a.q2 + p * pieces * 1024;
+    r.s[0] = a.s2 + p * 16;
+    r.s_stride = a.experts * a.m;
+    for (int i = 0; i < n; i += XR) {
+        const int rows = n - i < XR ? n - i : XR;
+#pragma unroll
+        for (int j = 0; j < Rows::PER; ++j) {
+            const int row = Rows::row_of(j);
+            r.x[j] = a.h + (int64_t)list[i + (row < rows ? row : rows - 1)] * a.f * 2 + Rows::offset_of(j);
+        }
+        v4f acc[1][Rows::FM] = {};
+        r.run((int)(slice * pieces / a.ks), (int)((slice + 1) * pieces / a.ks), smem, acc, [] {});
+#pragma unroll
+        for (int c = 0; c < Rows::FM; ++c)
+            if (c * 16 + lane % 16 < rows) {
+                const int pair = list[i + c * 16 + lane % 16];
+                const float w = a.weights[pair];
+                v4f s = acc[0][c];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] *= w;
+                *reinterpret_cast<v4f *>(a.part + ((slice * a.b * a.k + pair) * a.m + panel * 16 + lane / 16 * 4)) = s;
+            }
+        __syncthreads();
+    }
+}
+
+// y = the sum of a token's weighted parts, in the order of its choices and of K's slices, rounded once.
 template <class T>
 __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
     const int64_t tok = blockIdx.y, c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
@@ -407,42 +513,42 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
     v4f s = {0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < a.k; ++j) {
         if ((unsigned)a.ids[tok * a.k + j] >= (unsigned)a.experts) continue;
-        const v4f o = *reinterpret_cast<const v4f *>(a.part + (tok * a.k + j) * a.m + c);
+        for (int q = 0; q < a.ks; ++q) {
+            const v4f o = *reinterpret_cast<const v4f *>(a.part + ((q * a.b + tok) * a.k + j) * a.m + c);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] += o[e];
+            for (int e = 0; e < 4; ++e) s[e] += o[e];
+        }
     }
     *reinterpret_cast<uint2 *>(a.y + tok * a.m + c) = make_uint2((uint32_t)T::from_f32(s[0]) | (uint32_t)T::from_f32(s[1]) << 16,
                                                                  (uint32_t)T::from_f32(s[2]) | (uint32_t)T::from_f32(s[3]) << 16);
 }
 
-// Waves that share a panel's K: until the chip's 1024 SIMDs have two each, while each keeps two pieces.
-static int share_waves(int64_t units, int64_t pieces) {
-    int kw = 1;
-    while (kw < kMoeWaves && units * kw < 2048 && pieces >= kw * 4) kw *= 2;
-    return kw;
-}
-
-hipError_t launch_moe(const MoeArgs &a, hipStream_t stream) {
-    const int64_t pairs = a.b * a.k;
-    const unsigned slots = (unsigned)(pairs < a.experts ? pairs : a.experts);
-    int ku = share_waves(a.f / 16 * slots, a.m / 128), kd = share_waves(a.m / 32 * slots, a.f / 128);
-    const dim3 up((unsigned)((a.f / 16 * ku + kMoeWaves - 1) / kMoeWaves), slots);
-    const dim3 down((unsigned)((a.m / 32 * kd + kMoeWaves - 1) / kMoeWaves), slots);
-    if (a.bf16)
-        moe_up_kernel<BF16><<<up, kMoeThreads, 0, stream>>>(a, ku);
+template <class T>
+static hipError_t moe_typed(const MoeArgs &a, const MoePlan &p, hipStream_t stream) {
+    if (p.up_shared)
+        moe_up_shared_kernel<T, 32, 1><<<dim3((unsigned)(a.f / 128), (unsigned)p.slots), kMoeThreads, 0, stream>>>(a);
     else
-        moe_up_kernel<F16><<<up, kMoeThreads, 0, stream>>>(a, ku);
+        moe_up_kernel<T><<<dim3((unsigned)((a.f / 16 * p.up_waves + kMoeWaves - 1) / kMoeWaves), (unsigned)(p.slots + p.few)), kMoeThreads, 0,
+                           stream>>>(a, p.slots, p.up_waves);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    moe_down_kernel<<<down, kMoeThreads, 0, stream>>>(a, kd);
+    if (p.few) {
+        moe_down_few_kernel<T><<<(unsigned)(a.m / 16), kDownThreads, 0, stream>>>(a);
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)(a.m / 128), (unsigned)p.slots, (unsigned)p.ks);
+    if (p.down_rows == 16)
+        moe_down_shared_kernel<16><<<grid, kMoeThreads, 0, stream>>>(a);
+    else
+        moe_down_shared_kernel<32><<<grid, kMoeThreads, 0, stream>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const dim3 join((unsigned)((a.m + 1023) / 1024), (unsigned)a.b);
-    if (a.bf16)
-        moe_join_kernel<BF16><<<join, 256, 0, stream>>>(a);
-    else
-        moe_join_kernel<F16><<<join, 256, 0, stream>>>(a);
+    moe_join_kernel<T><<<dim3((unsigned)((a.m + 1023) / 1024), (unsigned)a.b), 256, 0, stream>>>(a);
     return hipGetLastError();
+}
+
+hipError_t launch_moe(const MoeArgs &a, const MoePlan &p, hipStream_t stream) {
+    return a.bf16 ? moe_typed<BF16>(a, p, stream) : moe_typed<F16>(a, p, stream);
 }
 
 }  // namespace twq

@@ -34,27 +34,10 @@ twq_status done(hipError_t e, const char *name) { return e == hipSuccess ? TWQ_O
 
 const uint16_t *u16(const void *p) { return static_cast<const uint16_t *>(p); }
 
-struct MoeLayout {
-    size_t h, part, experts;             // of twq_moe_experts
-    size_t logits, ids, weights, total;  // of twq_moe, behind it
-};
-
 size_t route_bytes(int64_t b, int64_t experts) { return align256((size_t)(b * experts) * 8); }
 
-MoeLayout moe_layout(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k) {
-    MoeLayout L{};
-    L.h = 0;
-    L.part = align256((size_t)(b * k * f) * 4);
-    L.experts = L.part + align256((size_t)(b * k * m) * 4);
-    L.logits = L.experts;
-    L.ids = L.logits + route_bytes(b, experts);
-    L.weights = L.ids + align256((size_t)(b * k) * 4);
-    L.total = L.weights + align256((size_t)(b * k) * 4);
-    return L;
-}
-
-hipError_t route(const void *x, const void *wr, const float *bias, int64_t b, int64_t m, int64_t experts, int64_t k, int score,
-                 int norm, float scale, int type, int32_t *ids, float *weights, void *logits, hipStream_t stream) {
+RouteArgs route_args(const void *x, const void *wr, const float *bias, int64_t b, int64_t m, int64_t experts, int64_t k, int score,
+                     int norm, float scale, int type, int32_t *ids, float *weights, void *logits) {
     RouteArgs a{};
     a.x = u16(x);
     a.wr = u16(wr);
@@ -70,12 +53,13 @@ hipError_t route(const void *x, const void *wr, const float *bias, int64_t b, in
     a.logits = static_cast<double *>(logits);
     a.ids = ids;
     a.weights = weights;
-    return launch_route(a, stream);
+    return a;
 }
 
-hipError_t experts_of(const void *x, const int32_t *ids, const float *weights, const void *q1, const float *s1, const void *q2,
-                      const float *s2, void *y, int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k, int type,
-                      uint8_t *ws, const MoeLayout &L, hipStream_t stream) {
+MoeArgs moe_args(const void *x, const int32_t *ids, const float *weights, const void *q1, const float *s1, const void *q2,
+                 const float *s2, void *y, int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k, int type, void *workspace,
+                 const MoePlan &p) {
+    uint8_t *const ws = static_cast<uint8_t *>(workspace);
     MoeArgs a{};
     a.x = u16(x);
     a.ids = ids;
@@ -90,10 +74,16 @@ hipError_t experts_of(const void *x, const int32_t *ids, const float *weights, c
     a.experts = (int)experts;
     a.k = (int)k;
     a.bf16 = type == TWQ_BF16;
-    a.h = reinterpret_cast<uint16_t *>(ws + L.h);
-    a.part = reinterpret_cast<float *>(ws + L.part);
+    a.h = reinterpret_cast<uint16_t *>(ws + p.h);
+    a.ks = p.ks;
+    if (!p.few) {
+        a.part = reinterpret_cast<float *>(ws + p.part);
+    } else {
+        a.entries = reinterpret_cast<MoeEntry *>(ws + p.entries);
+        a.entry_count = reinterpret_cast<int32_t *>(a.entries + b * k);
+    }
     a.y = static_cast<uint16_t *>(y);
-    return launch_moe(a, stream);
+    return a;
 }
 
 }  // namespace
@@ -177,13 +167,14 @@ twq_status twq_moe_route(const void *x, const void *wr, const float *bias, int64
     if (!aligned16(x) || !aligned16(wr) || !aligned16(bias) || !aligned16(ids) || !aligned16(weights)) return TWQ_ERR_ALIGN;
     if (!workspace || workspace_bytes < route_bytes(b, experts)) return TWQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return TWQ_ERR_ALIGN;
-    return done(route(x, wr, bias, b, m, experts, k, score, norm, scale, type, ids, weights, workspace,
-                      static_cast<hipStream_t>(stream)), "twq_moe_route");
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const RouteArgs a = route_args(x, wr, bias, b, m, experts, k, score, norm, scale, type, ids, weights, workspace);
+    return done(launch_route(a, st), "twq_moe_route");
 }
 
 size_t twq_moe_experts_workspace_bytes(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k) {
     if (!valid_experts(b, m, f, experts, k)) return 0;
-    return moe_layout(b, m, f, experts, k).experts;
+    return plan_moe(b, m, f, experts, k).experts;
 }
 
 twq_status twq_moe_experts(const void *x, const int32_t *ids, const float *weights, const void *q1, const float *s1,
@@ -196,16 +187,16 @@ twq_status twq_moe_experts(const void *x, const int32_t *ids, const float *weigh
     if (!aligned16(x) || !aligned16(ids) || !aligned16(weights) || !aligned16(q1) || !aligned16(s1) || !aligned16(q2) ||
         !aligned16(s2) || !aligned16(y))
         return TWQ_ERR_ALIGN;
-    const MoeLayout L = moe_layout(b, m, f, experts, k);
-    if (!workspace || workspace_bytes < L.experts) return TWQ_ERR_WORKSPACE;
+    const MoePlan p = plan_moe(b, m, f, experts, k);
+    if (!workspace || workspace_bytes < p.experts) return TWQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return TWQ_ERR_ALIGN;
-    return done(experts_of(x, ids, weights, q1, s1, q2, s2, y, b, m, f, experts, k, type, static_cast<uint8_t *>(workspace), L,
-                           static_cast<hipStream_t>(stream)), "twq_moe_experts");
+    const MoeArgs a = moe_args(x, ids, weights, q1, s1, q2, s2, y, b, m, f, experts, k, type, workspace, p);
+    return done(launch_moe(a, p, static_cast<hipStream_t>(stream)), "twq_moe_experts");
 }
 
 size_t twq_moe_workspace_bytes(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k) {
     if (!valid_experts(b, m, f, experts, k) || !valid_route(b, m, experts, k)) return 0;
-    return moe_layout(b, m, f, experts, k).total;
+    return plan_moe(b, m, f, experts, k).total;
 }
 
 twq_status twq_moe(const void *x, const void *wr, const float *bias, const void *q1, const float *s1, const void *q2,
@@ -218,15 +209,16 @@ twq_status twq_moe(const void *x, const void *wr, const float *bias, const void 
     if (!aligned16(x) || !aligned16(wr) || !aligned16(bias) || !aligned16(q1) || !aligned16(s1) || !aligned16(q2) ||
         !aligned16(s2) || !aligned16(y))
         return TWQ_ERR_ALIGN;
-    const MoeLayout L = moe_layout(b, m, f, experts, k);
-    if (!workspace || workspace_bytes < L.total) return TWQ_ERR_WORKSPACE;
+    const MoePlan p = plan_moe(b, m, f, experts, k);
+    if (!workspace || workspace_bytes < p.total) return TWQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return TWQ_ERR_ALIGN;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     uint8_t *const ws = static_cast<uint8_t *>(workspace);
-    int32_t *const ids = reinterpret_cast<int32_t *>(ws + L.ids);
-    float *const weights = reinterpret_cast<float *>(ws + L.weights);
-    hipError_t e = route(x, wr, bias, b, m, experts, k, score, norm, scale, type, ids, weights, ws + L.logits, st);
-    if (e == hipSuccess) e = experts_of(x, ids, weights, q1, s1, q2, s2, y, b, m, f, experts, k, type, ws, L, st);
+    const RouteArgs r = route_args(x, wr, bias, b, m, experts, k, score, norm, scale, type, reinterpret_cast<int32_t *>(ws + p.ids),
+                                   reinterpret_cast<float *>(ws + p.weights), ws + p.logits);
+    const MoeArgs a = moe_args(x, r.ids, r.weights, q1, s1, q2, s2, y, b, m, f, experts, k, type, workspace, p);
+    hipError_t e = launch_route(r, st);
+    if (e == hipSuccess) e = launch_moe(a, p, st);
     return done(e, "twq_moe");
 }
 

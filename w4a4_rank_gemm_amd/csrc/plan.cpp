@@ -169,12 +169,18 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
     if (!p.many) {
         const int64_t panels = n / 16, pieces = m / 128;
         p.rows = b <= 4 ? 4 : b <= 16 ? 16 : b <= 32 ? 32 : 64;
-        p.fn = p.rows == 4 || (p.rows == 16 && panels < 512) ? 1 : 2;
-        const int64_t units = (panels + p.fn - 1) / p.fn;
-        p.kw = 1;
-        while (p.kw < 8 && units * p.kw < (p.rows == 4 ? 3072 : 1536) && pieces >= p.kw * 2) p.kw *= 2;
-        if (p.rows >= 32)
-            while (p.ks < 8 && units * p.kw * p.ks < 2048 && pieces >= p.kw * p.ks * 4) p.ks *= 2;
+        if (p.rows <= 16) {
+            p.fn = p.rows == 4 || panels < 512 ? 1 : 2;
+            const int64_t units = (panels + p.fn - 1) / p.fn;
+            p.kw = 1;
+            while (p.kw < 8 && units * p.kw < (p.rows == 4 ? 3072 : 1536) && pieces >= p.kw * 2) p.kw *= 2;
+        } else {
+            p.fn = p.rows == 64 && panels >= 1536 ? 2 : 1;
+            const int64_t ctas = (panels + 8 * p.fn - 1) / (8 * p.fn);
+            int64_t ks = 256 / ctas;
+            if (ks > pieces / 4) ks = pieces / 4;
+            p.ks = ks < 1 ? 1 : ks > 16 ? 16 : (int)ks;
+        }
         p.part = p.x16;
         p.total = p.part + (p.ks > 1 ? up((size_t)p.ks * b * n * 4) : 0);
         return p;
@@ -195,6 +201,30 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
     p.te = p.t16 + up((size_t)b * r * 4);
     p.part = p.te + up((size_t)b * 4);
     p.total = p.part + (p.ks > 1 ? up((size_t)p.ks * b * n * 4) : 0);
+    return p;
+}
+
+MoePlan plan_moe(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k) {
+    auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+    MoePlan p{};
+    const int64_t pairs = b * k, slots = pairs < experts ? pairs : experts;
+    p.few = b <= kFewMoe;
+    p.slots = (int)slots;
+    p.up_shared = !p.few && pairs >= experts * 4 && f / 128 * slots >= 256;
+    p.up_waves = 1;
+    while (p.up_waves < 8 && f / 16 * slots * p.up_waves < 5000 && m / 128 >= p.up_waves * 8) p.up_waves *= 2;
+    p.down_rows = pairs >= experts * 12 ? 32 : 16;
+    p.ks = 1;
+    if (!p.few)
+        while (p.ks < 8 && m / 128 * slots * p.ks < 256 && f / 128 >= p.ks * 8) p.ks *= 2;
+    p.h = 0;
+    p.part = up((size_t)(pairs * f) * 4);
+    p.entries = p.part;
+    p.experts = !p.few ? p.part + up((size_t)(p.ks * pairs * m) * 4) : p.entries + up((size_t)pairs * sizeof(MoeEntry) + 16);
+    p.logits = p.experts;
+    p.ids = p.logits + up((size_t)(b * experts) * 8);
+    p.weights = p.ids + up((size_t)pairs * 4);
+    p.total = p.weights + up((size_t)pairs * 4);
     return p;
 }
 

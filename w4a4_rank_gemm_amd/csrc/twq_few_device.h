@@ -162,6 +162,115 @@ struct FewRows {
     }
 };
 
+// The same product for the eight waves of a CTA that own neighbouring panel groups and share rows
+// and K: the rows' pieces p0 .. p1 - 1 go through LDS once for all of them, U at a time into one of
+// two buffers, with one barrier a step. All waves call it with the same pieces.
+constexpr int kSharedWaves = 8;
+
+template <class T, int FN, int XR, int PARTS, int U>
+struct SharedRows {
+    static_assert(XR % 16 == 0 && U <= 4, "a batch's scales are one load");
+    static constexpr int NT = kSharedWaves * kWave, FM = XR / 16;
+    static constexpr int CHUNKS = U * PARTS * XR * 16, PER = CHUNKS / NT;  // 16-byte chunks of a step, and a thread's
+    static_assert(CHUNKS % NT == 0, "every thread loads the same number of chunks");
+    static constexpr int SLOT = XR * 16 + 16, PIECE = PARTS * 16 * SLOT;
+    static constexpr int LDS = 2 * U * PIECE + kSharedWaves * FN * 256;
+
+    const uint8_t *w[FN];    // this wave's panels, at piece 0
+    const float *s[FN];      // scales of the panels' first channels, group 0
+    int64_t s_stride;        // floats between groups
+    const uint16_t *x[PER];  // chunk j of this thread, at piece 0 (see at)
+
+    // Row, and offset in it at piece 0, of this thread's chunk j.
+    static __device__ __forceinline__ int row_of(int j) { return (j * NT + (int)threadIdx.x) / 16 % XR; }
+    static __device__ __forceinline__ int offset_of(int j) { return (j * NT + (int)threadIdx.x) / (16 * XR) % PARTS * 128 + (int)threadIdx.x % 16 * 8; }
+
+    template <class F>
+    __device__ __forceinline__ void run(int p0, int p1, uint8_t *lds, v4f (&acc)[FN][FM], F &&between) const {
+        const int tid = threadIdx.x, lane = tid % kWave, li = lane & 15, g = lane >> 4;
+        const Codes<T> codes;
+        v4i wn[U][FN], xn[PER];
+        float sn[FN];
+        auto load = [&](int p) {  // pieces past the last are read again and scaled by zero
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const int u = (j * NT + tid) / (16 * XR * PARTS);
+                const int64_t q = p + u < p1 ? p + u : p1 - 1;
+                xn[j] = load16(x[j] + q * (128 * PARTS));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t q = p + u < p1 ? p + u : p1 - 1;
+#pragma unroll
+                for (int f = 0; f < FN; ++f)
+                    wn[u][f] = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w[f] + q * 1024 + li * 64 + g * 16));
+            }
+            const int64_t q = p + g < p1 ? p + g : p1 - 1;
+#pragma unroll
+            for (int f = 0; f < FN; ++f) sn[f] = s[f][q * s_stride + li];
+        };
+        if (p0 >= p1) return between();
+        load(p0);
+        between();
+        float *const scales = reinterpret_cast<float *>(lds + 2 * U * PIECE) + tid / kWave * FN * 64;
+        int put[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int c = tid % 16, q = (j * NT + tid) / 16;  // chunk 4 quarter + instruction of row q % XR
+            put[j] = (q / XR) * (16 * SLOT) + ((c & 3) * 4 + (c >> 2)) * SLOT + q % XR * 16;
+        }
+        const int get = g * SLOT + li * 16;
+        uint8_t *buf = lds;
+        for (int p = p0; p < p1; p += U) {
+            v4i wc[U][FN];
+            wave_fence();
+#pragma unroll
+            for (int j = 0; j < PER; ++j) *reinterpret_cast<v4i *>(buf + put[j]) = Codes<T>::order(xn[j]);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int f = 0; f < FN; ++f) wc[u][f] = wn[u][f];
+#pragma unroll
+            for (int f = 0; f < FN; ++f) scales[f * 64 + lane] = p + g < p1 ? sn[f] * (1.f / Codes<T>::kTimes) : 0.f;
+            if (p + U < p1) load(p + U);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            stage_barrier();  // this step's rows are written, and the other buffer is read
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                v4f t[FN][FM];
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    v4i xf[PARTS][FM];
+#pragma unroll
+                    for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+                        for (int c = 0; c < FM; ++c)
+                            xf[h][c] = load16(buf + u * PIECE + (h * 16 + d * 4) * SLOT + get + c * 256);
+#pragma unroll
+                    for (int f = 0; f < FN; ++f) {
+                        const v4i wf = codes((uint32_t)wc[u][f][d]);
+#pragma unroll
+                        for (int c = 0; c < FM; ++c)
+#pragma unroll
+                            for (int h = 0; h < PARTS; ++h)
+                                t[f][c] = T::mfma(wf, xf[h][c], h == 0 && d == 0 ? v4f{0.f, 0.f, 0.f, 0.f} : t[f][c]);
+                    }
+                }
+#pragma unroll
+                for (int f = 0; f < FN; ++f) {
+                    const v4f sc = *reinterpret_cast<const v4f *>(scales + f * 64 + u * 16 + g * 4);
+#pragma unroll
+                    for (int c = 0; c < FM; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[f][c][e] += sc[e] * t[f][c][e];
+                }
+            }
+            buf = buf == lds ? lds + U * PIECE : lds;
+        }
+        wave_fence();
+    }
+};
+
 // The sums of the KW waves (a power of two) that share a panel group's K, neighbours `wave / KW`
 // in a CTA: wave kw of them gets the sums of row blocks c = kw, kw + KW, .. in acc, added in wave
 // order. All threads of the CTA call it; `red` holds FN FM KB a wave.

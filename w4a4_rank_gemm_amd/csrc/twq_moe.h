@@ -42,7 +42,7 @@ struct A16Args {
 struct A16Plan {
     int many;      // the tile kernel
     int rows;      // token rows a CTA
-    int fn, kw;    // few rows: panels of a wave, waves that share their K
+    int fn, kw;    // few rows: panels of a wave; up to 16 rows: waves that share their K
     int tks;       // K slices of X L1
     int ks;        // K slices of the product
     size_t t, x16, xe, mul, mask, unit, t16, te, part, total;
@@ -71,6 +71,15 @@ struct RouteArgs {
 };
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
 
+// Tokens whose outputs the down kernel sums by itself, from a work list of at most kFewPairs entries.
+constexpr int kFewMoe = 4, kFewPairs = kFewMoe * (int)kMaxTopK;
+struct alignas(16) MoeEntry {
+    int32_t expert, rows;     // rows: its pairs (token, choice), in order
+    int16_t pair[kFewMoe];
+    int8_t place[kFewMoe];    // of each token: which of the pairs is its own, or -1
+};
+static_assert(sizeof(MoeEntry) == 32, "read in 16-byte pieces");
+
 struct MoeArgs {
     const uint16_t *x;    // [b][m]
     const int32_t *ids;   // [b][k], outside [0, experts): none
@@ -83,9 +92,24 @@ struct MoeArgs {
     int experts, k;
     int bf16;             // type of x and y
     uint16_t *h;          // [b k][f / 128][2][128] bf16: the experts' inner rows, upper and lower parts
-    float *part;          // [b k][m]: weighted outputs of each token's choices
+    int ks;               // K slices of the down product above kFewMoe tokens
+    float *part;          // [ks][b k][m]: weighted outputs of each token's choices, above kFewMoe tokens
+    MoeEntry *entries;    // [b k], up to kFewMoe tokens
+    int32_t *entry_count;
     uint16_t *y;          // [b][m]
 };
-hipError_t launch_moe(const MoeArgs &a, hipStream_t stream);
+
+struct MoePlan {
+    int few;         // the down kernel sums a token's outputs by itself
+    int slots;       // rows of CTAs: pairs (token, choice) or experts
+    int up_shared;   // gate and up: a CTA's waves share rows and K
+    int up_waves;    // or: waves that share a panel's K
+    int down_rows;   // above kFewMoe tokens: rows of a tile
+    int ks;
+    size_t h, part, entries, experts;    // workspace of the experts' products, its size
+    size_t logits, ids, weights, total;  // of the whole layer, behind it
+};
+MoePlan plan_moe(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k);  // plan.cpp
+hipError_t launch_moe(const MoeArgs &a, const MoePlan &p, hipStream_t stream);
 
 }  // namespace twq
