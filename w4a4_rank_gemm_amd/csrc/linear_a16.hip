@@ -149,15 +149,16 @@ __global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a, in
         rows.s[f] = a.sw + p * 16;
     }
     rows.s_stride = a.n;
+    rows.x = a.x + row0 * a.m;
 #pragma unroll
     for (int j = 0; j < Rows::XL; ++j) {
-        const int64_t row = row0 + 4 * j + lane / 16;
-        rows.x[j] = a.x + (row < last ? row : last - 1) * a.m + lane % 16 * 8;
+        const int row = 4 * j + lane / 16, most = (int)(last - row0) - 1;
+        rows.row[j] = (uint32_t)((row < most ? row : most) * a.m * 2);
     }
     v4f acc[FN][FM] = {};
     const int64_t part = slice * kw + share, parts = (int64_t)a.ks * kw;
     if (panel0 < panels) {
-        rows.template run<true>((int)(part * pieces / parts), (int)((part + 1) * pieces / parts), smem + wave * Rows::LDS, acc, [&] {
+        rows.run((int)(part * pieces / parts), (int)((part + 1) * pieces / parts), smem + wave * Rows::LDS, acc, [&] {
             if (a.r > 0 && slice == 0) few_lowrank<FN, FM>(a, row0, last, chan, share, kw, acc);
         });
     }
@@ -184,10 +185,11 @@ __global__ __launch_bounds__(kSharedWaves *kWave) void a16_shared_kernel(A16Args
         rows.s[f] = a.sw + p * 16;
     }
     rows.s_stride = a.n;
+    rows.x = a.x + row0 * a.m;
 #pragma unroll
     for (int j = 0; j < Rows::PER; ++j) {
-        const int64_t row = row0 + Rows::row_of(j);
-        rows.x[j] = a.x + (row < last ? row : last - 1) * a.m + Rows::offset_of(j);
+        const int row = Rows::row_of(j), most = (int)(last - row0) - 1;
+        rows.row[j] = (uint32_t)((row < most ? row : most) * a.m * 2);
     }
     v4f acc[FN][FM] = {};
     rows.run((int)(slice * pieces / a.ks), (int)((slice + 1) * pieces / a.ks), smem, acc, [&] {

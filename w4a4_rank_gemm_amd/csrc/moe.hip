@@ -240,7 +240,7 @@ __device__ __forceinline__ int expert_pairs(const MoeArgs &a, int slot, int &exp
     int have = 0;
     if (n <= kWave) {
         const int id = lane < n ? a.ids[lane] : -1;
-        expert = n <= a.experts ? __shfl(id, slot, kWave) : slot;
+        expert = n <= a.experts ? __builtin_amdgcn_readlane(id, slot) : slot;
         if ((unsigned)expert >= (unsigned)a.experts) return 0;
         const uint64_t hit = __ballot(lane < n && id == expert);
         if (hit >> lane & 1) list[__popcll(hit & below)] = (uint16_t)lane;
@@ -249,7 +249,7 @@ __device__ __forceinline__ int expert_pairs(const MoeArgs &a, int slot, int &exp
         return n <= a.experts && __builtin_ctzll(hit) != slot ? 0 : have;
     }
     int id = tid < n ? a.ids[tid] : -1;
-    expert = n <= a.experts ? a.ids[slot] : slot;
+    expert = n <= a.experts ? __builtin_amdgcn_readfirstlane(a.ids[slot]) : slot;
     if ((unsigned)expert >= (unsigned)a.experts) return 0;
     for (int i0 = 0; i0 < n; i0 += kMoeThreads) {
         const int i = i0 + tid;
@@ -299,14 +299,15 @@ __device__ __forceinline__ void up_tile(const MoeArgs &a, int expert, const uint
         r.s[f] = a.s1 + p * 16;
     }
     r.s_stride = a.experts * 2 * a.f;
+    r.x = a.x;
 #pragma unroll
     for (int j = 0; j < Rows::XL; ++j) {
         const int i = 4 * j + lane / 16;
-        r.x[j] = a.x + (int64_t)(list[i < rows ? i : rows - 1] / a.k) * a.m + lane % 16 * 8;
+        r.row[j] = (uint32_t)((list[i < rows ? i : rows - 1] / a.k) * a.m * 2);
     }
     v4f acc[2][1] = {};
     if (unit < half)
-        r.template run<true>((int)(share * pieces / kw), (int)((share + 1) * pieces / kw), smem + wave * wave_lds, acc, [] {});
+        r.run((int)(share * pieces / kw), (int)((share + 1) * pieces / kw), smem + wave * wave_lds, acc, [] {});
     join_waves(smem, kw, wave, acc);
     if (share == 0 && unit < half && lane % 16 < rows) store_inner(a, acc[0][0], acc[1][0], list[lane % 16], unit);
 }
@@ -405,14 +406,15 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_few_kernel(MoeArgs a) {
     for (int u = (int)((int64_t)wave * all / kDownWaves); u < u1;) {
         const MoeEntry &e = entries[u / pieces];
         const int p0 = u % pieces, p1 = pieces - p0 < u1 - u ? pieces : p0 + u1 - u;
-        const int64_t p = e.expert * (a.m / 16) + panel;
+        const int64_t p = __builtin_amdgcn_readfirstlane(e.expert) * (a.m / 16) + panel;
         Rows r;
         r.w[0] = a.q2 + p * pieces * 1024;
         r.s[0] = a.s2 + p * 16;
         r.s_stride = a.experts * a.m;
-        r.x[0] = a.h + (int64_t)e.pair[g < e.rows ? g : e.rows - 1] * a.f * 2 + li * 8;
+        r.x = a.h;
+        r.row[0] = (uint32_t)(e.pair[g < e.rows ? g : e.rows - 1] * a.f * 4);
         v4f acc[1][1] = {};
-        r.template run<true>(p0, p1, smem + wave * Rows::LDS, acc, [] {});
+        r.run(p0, p1, smem + wave * Rows::LDS, acc, [] {});
         const int place = li < kFewMoe ? e.place[li] : -1;  // column of this lane's token
         const float w = place < 0 ? 0.f : weights[e.pair[place]];
 #pragma unroll
@@ -451,12 +453,13 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_shared_kernel(MoeArgs a) {
         r.s[f] = a.s1 + p * 16;
     }
     r.s_stride = a.experts * 2 * a.f;
+    r.x = a.x;
     for (int i = 0; i < n; i += XR) {
         const int rows = n - i < XR ? n - i : XR;
 #pragma unroll
         for (int j = 0; j < Rows::PER; ++j) {
             const int row = Rows::row_of(j);
-            r.x[j] = a.x + (int64_t)(list[i + (row < rows ? row : rows - 1)] / a.k) * a.m + Rows::offset_of(j);
+            r.row[j] = (uint32_t)((list[i + (row < rows ? row : rows - 1)] / a.k) * a.m * 2);
         }
         v4f acc[2][Rows::FM] = {};
         r.run(0, (int)pieces, smem, acc, [] {});
@@ -482,12 +485,13 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_shared_kernel(MoeArgs a)
     r.w[0] = a.q2 + p * pieces * 1024;
     r.s[0] = a.s2 + p * 16;
     r.s_stride = a.experts * a.m;
+    r.x = a.h;
     for (int i = 0; i < n; i += XR) {
         const int rows = n - i < XR ? n - i : XR;
 #pragma unroll
         for (int j = 0; j < Rows::PER; ++j) {
             const int row = Rows::row_of(j);
-            r.x[j] = a.h + (int64_t)list[i + (row < rows ? row : rows - 1)] * a.f * 2 + Rows::offset_of(j);
+            r.row[j] = (uint32_t)(list[i + (row < rows ? row : rows - 1)] * a.f * 4);  // at most 4095 x 2^19
         }
         v4f acc[1][Rows::FM] = {};
         r.run((int)(slice * pieces / a.ks), (int)((slice + 1) * pieces / a.ks), smem, acc, [] {});

@@ -52,6 +52,14 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
+// Zeros that stay in registers, as the first addend of a chain of matrix instructions: a constant
+// would be moved into each chain's result first.
+__device__ __forceinline__ v4f held_zero() {
+    v4f z = {0.f, 0.f, 0.f, 0.f};
+    asm("" : "+v"(z));
+    return z;
+}
+
 // One wave's share of Y = X W^T for up to XR rows and FN panels of 16 channels: pieces (groups
 // of 128 elements of K) p0 .. p1 - 1, U in flight at a time. For each piece
 //
@@ -74,35 +82,45 @@ struct FewRows {
     static constexpr int PIECE = PARTS * 16 * SLOT;
     static constexpr int LDS = U * PIECE + FN * 256;  // bytes of a wave
 
+    // Pointers are the same in all lanes, and lanes add 32-bit offsets, so that a piece's addresses
+    // cost no vector instructions.
     const uint8_t *w[FN];      // this wave's panels, at piece 0
     const float *s[FN];        // scales of the panels' first channels, group 0
     int64_t s_stride;          // floats between groups
-    const uint16_t *x[XL];     // this lane's rows 4 j + lane / 16 at element 8 (lane % 16)
+    const uint16_t *x;         // rows
+    uint32_t row[XL];          // bytes to this lane's rows 4 j + lane / 16 (rows lie within 4 GB)
 
     // `between` runs after the first loads are issued.
-    template <bool STREAM, class F>
+    template <class F>
     __device__ __forceinline__ void run(int p0, int p1, uint8_t *lds, v4f (&acc)[FN][FM], F &&between) const {
         const int lane = threadIdx.x % kWave, li = lane & 15, g = lane >> 4;
         const Codes<T> codes;
+        const v4f zero = held_zero();
         v4i wn[U][FN], xn[U][PARTS][XL];
         float sn[FN];
+        const uint32_t woff = li * 64 + g * 16, soff = li * 4;
+        uint32_t xoff[XL];
+#pragma unroll
+        for (int j = 0; j < XL; ++j) xoff[j] = row[j] + li * 16;
+        const int64_t s_step = s_stride * 4;
         auto load = [&](int p) {  // pieces past the last are read again and scaled by zero
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t q = p + u < p1 ? p + u : p1 - 1;
 #pragma unroll
                 for (int f = 0; f < FN; ++f) {
-                    const uint8_t *a = w[f] + q * 1024 + li * 64 + g * 16;
-                    wn[u][f] = STREAM ? __builtin_nontemporal_load(reinterpret_cast<const v4i *>(a)) : load16(a);
+                    const uint8_t *const a = w[f] + q * 1024;
+                    wn[u][f] = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(a + woff));
                 }
 #pragma unroll
                 for (int h = 0; h < PARTS; ++h)
 #pragma unroll
-                    for (int j = 0; j < XL; ++j) xn[u][h][j] = load16(x[j] + (q * PARTS + h) * 128);
+                    for (int j = 0; j < XL; ++j) xn[u][h][j] = load16(reinterpret_cast<const uint8_t *>(x) + (q * PARTS + h) * 256 + xoff[j]);
             }
-            const int64_t q = p + g < p1 ? p + g : p1 - 1;
+            const uint32_t q = (U == 1 ? 0 : p + g < p1 ? g : p1 - 1 - p) * (uint32_t)s_step;  // U neighbouring groups
 #pragma unroll
-            for (int f = 0; f < FN; ++f) sn[f] = s[f][q * s_stride + li];
+            for (int f = 0; f < FN; ++f)
+                sn[f] = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(s[f]) + p * s_step + (q + soff));
         };
         if (p0 >= p1) return between();
         load(p0);
@@ -145,7 +163,7 @@ struct FewRows {
                         for (int c = 0; c < FM; ++c)
 #pragma unroll
                             for (int h = 0; h < PARTS; ++h)
-                                t[f][c] = T::mfma(wf, xf[h][c], h == 0 && d == 0 ? v4f{0.f, 0.f, 0.f, 0.f} : t[f][c]);
+                                t[f][c] = T::mfma(wf, xf[h][c], h == 0 && d == 0 ? zero : t[f][c]);
                     }
                 }
 #pragma unroll
@@ -179,35 +197,44 @@ struct SharedRows {
     const uint8_t *w[FN];    // this wave's panels, at piece 0
     const float *s[FN];      // scales of the panels' first channels, group 0
     int64_t s_stride;        // floats between groups
-    const uint16_t *x[PER];  // chunk j of this thread, at piece 0 (see at)
+    const uint16_t *x;       // rows
+    uint32_t row[PER];       // bytes to row row_of(j) (rows lie within 4 GB)
 
-    // Row, and offset in it at piece 0, of this thread's chunk j.
+    // Row of this thread's chunk j.
     static __device__ __forceinline__ int row_of(int j) { return (j * NT + (int)threadIdx.x) / 16 % XR; }
-    static __device__ __forceinline__ int offset_of(int j) { return (j * NT + (int)threadIdx.x) / (16 * XR) % PARTS * 128 + (int)threadIdx.x % 16 * 8; }
 
     template <class F>
     __device__ __forceinline__ void run(int p0, int p1, uint8_t *lds, v4f (&acc)[FN][FM], F &&between) const {
         const int tid = threadIdx.x, lane = tid % kWave, li = lane & 15, g = lane >> 4;
         const Codes<T> codes;
+        const v4f zero = held_zero();
         v4i wn[U][FN], xn[PER];
         float sn[FN];
+        const uint32_t woff = li * 64 + g * 16, soff = li * 4;
+        uint32_t xoff[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) xoff[j] = row[j] + (j * NT + tid) / (16 * XR) % PARTS * 256 + tid % 16 * 16;
+        const int64_t s_step = s_stride * 4;
         auto load = [&](int p) {  // pieces past the last are read again and scaled by zero
+            const uint8_t *const xp = reinterpret_cast<const uint8_t *>(x) + (int64_t)p * (256 * PARTS);
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 const int u = (j * NT + tid) / (16 * XR * PARTS);
-                const int64_t q = p + u < p1 ? p + u : p1 - 1;
-                xn[j] = load16(x[j] + q * (128 * PARTS));
+                xn[j] = load16(xp + (xoff[j] + (U == 1 ? 0 : p + u < p1 ? u : p1 - 1 - p) * (256 * PARTS)));
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t q = p + u < p1 ? p + u : p1 - 1;
 #pragma unroll
-                for (int f = 0; f < FN; ++f)
-                    wn[u][f] = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w[f] + q * 1024 + li * 64 + g * 16));
+                for (int f = 0; f < FN; ++f) {
+                    const uint8_t *const a = w[f] + q * 1024;
+                    wn[u][f] = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(a + woff));
+                }
             }
-            const int64_t q = p + g < p1 ? p + g : p1 - 1;
+            const uint32_t q = (U == 1 ? 0 : p + g < p1 ? g : p1 - 1 - p) * (uint32_t)s_step;
 #pragma unroll
-            for (int f = 0; f < FN; ++f) sn[f] = s[f][q * s_stride + li];
+            for (int f = 0; f < FN; ++f)
+                sn[f] = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(s[f]) + p * s_step + (q + soff));
         };
         if (p0 >= p1) return between();
         load(p0);
@@ -253,7 +280,7 @@ struct SharedRows {
                         for (int c = 0; c < FM; ++c)
 #pragma unroll
                             for (int h = 0; h < PARTS; ++h)
-                                t[f][c] = T::mfma(wf, xf[h][c], h == 0 && d == 0 ? v4f{0.f, 0.f, 0.f, 0.f} : t[f][c]);
+                                t[f][c] = T::mfma(wf, xf[h][c], h == 0 && d == 0 ? zero : t[f][c]);
                     }
                 }
 #pragma unroll
