@@ -96,7 +96,8 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t) {
     rd(a.x, a.b * a.m * 2);
     rd(a.wr, a.experts * a.m * 2);
     rd(a.bias, a.bias ? a.experts * 4 : 0);
-    wr(a.logits, a.b * a.experts * 8);
+    if (a.slices < 1) return hipErrorInvalidValue;
+    wr(a.logits, a.slices * a.b * a.experts * 8);
     wr(a.ids, a.b * a.k * 4);
     wr(a.weights, a.b * a.k * 4);
     return hipSuccess;
@@ -176,7 +177,7 @@ int main() {
     for (const auto &c : layers)
         for (int type : {TWQ_F16, TWQ_BF16}) layer(c[0], c[1], c[2], c[3], type);
     const int64_t moes[][5] = {{0, 256, 128, 4, 2}, {1, 128, 128, 1, 1}, {1, 512, 384, 64, 8}, {3, 256, 256, 5, 5}, {17, 384, 128, 60, 4},
-                               {256, 128, 128, 16, 16}, {100, 256, 128, 512, 3}, {16, 128, 256, 20, 16}, {20, 128, 8192, 2, 2}};
+                               {256, 128, 128, 16, 16}, {100, 256, 128, 512, 3}, {16, 128, 256, 20, 16}, {20, 128, 8192, 2, 2}, {256, 1024, 128, 300, 4}, {2, 4096, 128, 40, 4}};
     for (const auto &c : moes)
         for (int type : {TWQ_F16, TWQ_BF16}) routed(c[0], c[1], c[2], c[3], c[4], type);
     if (g_fail) {

@@ -465,10 +465,16 @@ __global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t nti
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 mul[q] = mn[q];
+                w[q][0] = wn[q][0];
+                w[q][1] = wn[q][1];
+            }
+            if (__builtin_expect(__ballot((kn[0] & kn[1]) == 0) != 0, 0)) {  // rarely a group without weight
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[q][h][e] = wn[q][h][e] & (int)kn[q];
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[q][h][e] &= (int)kn[q];
             }
             if (g + 1 < g1) fetch(g + 1, 1 - U);
 #pragma unroll

@@ -65,44 +65,66 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_logits_kernel(RouteA
     }
 }
 
-// Many products: tiles of 16 experts x 16 tokens on binary64 matrix instructions, K split over the
-// CTA's 16 waves, whose sums are added in wave order. Element e of a lane's eight goes to
-// instruction e, for both operands. Result: lane (li, g) holds token li, experts 4 v + g.
+// Many products: tiles of 32 experts x 32 tokens on binary64 matrix instructions (16 x 16 x 4, four a
+// wave, so that an element is converted for two of them), K split over slices and the CTA's 16
+// waves, whose sums are added in wave order. Element e of a lane's eight goes to instruction e, for both
+// operands. Result: lane (li, g) holds token li, experts 4 v + g of a 16 x 16 block.
 typedef double v4d __attribute__((ext_vector_type(4)));
-constexpr int kTileWaves = 16, kTileSteps = 4;
+constexpr int kTileWaves = 16;
 
 template <class T>
 __global__ __launch_bounds__(kTileWaves *kWave) void route_logits_tile_kernel(RouteArgs a) {
-    __shared__ double red[kTileWaves][4][kWave];
+    __shared__ double red[kTileWaves][4][4][kWave];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, li = lane & 15, g = lane >> 4;
-    const int64_t e0 = (int64_t)blockIdx.x * 16, tok = (int64_t)blockIdx.y * 16 + li, e = e0 + li;
-    const int steps = (int)(a.m / 32), s0 = wave * steps / kTileWaves, s1 = (wave + 1) * steps / kTileWaves;
-    const uint16_t *w = a.wr + (e < a.experts ? e : a.experts - 1) * a.m + g * 8, *x = a.x + (tok < a.b ? tok : a.b - 1) * a.m + g * 8;
-    v4d acc = {0, 0, 0, 0};
-    for (int s = s0; s < s1; s += kTileSteps) {
-        v4i wv[kTileSteps], xv[kTileSteps];
+    const int64_t e0 = (int64_t)blockIdx.x * 32, t0 = (int64_t)blockIdx.y * 32, slice = blockIdx.z;
+    const int steps = (int)(a.m / 32), parts = a.slices * kTileWaves, part = (int)slice * kTileWaves + wave;
+    const int s0 = (int)((int64_t)part * steps / parts), s1 = (int)((int64_t)(part + 1) * steps / parts);
+    const uint16_t *w[2], *x[2];
 #pragma unroll
-        for (int u = 0; u < kTileSteps; ++u) {
-            const int q = s + u < s1 ? s + u : s1 - 1;
-            wv[u] = load16(w + q * 32);
-            xv[u] = load16(x + q * 32);
+    for (int q = 0; q < 2; ++q) {
+        const int64_t e = e0 + q * 16 + li, t = t0 + q * 16 + li;
+        w[q] = a.wr + (e < a.experts ? e : a.experts - 1) * a.m + g * 8;
+        x[q] = a.x + (t < a.b ? t : a.b - 1) * a.m + g * 8;
+    }
+    v4d acc[2][2] = {};
+    v4i wn[2], xn[2];
+    auto load = [&](int s) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            wn[q] = load16(w[q] + s * 32);
+            xn[q] = load16(x[q] + s * 32);
         }
+    };
+    if (s0 < s1) load(s0);
+    for (int s = s0; s < s1; ++s) {
+        const v4i wc[2] = {wn[0], wn[1]}, xc[2] = {xn[0], xn[1]};
+        if (s + 1 < s1) load(s + 1);
 #pragma unroll
-        for (int u = 0; u < kTileSteps; ++u) {
-            if (s + u >= s1) break;
+        for (int e = 0; e < 8; ++e) {
+            double wd[2], xd[2];
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)T::to_f32(half_of(wv[u][q / 2], q % 2)),
-                                                           (double)T::to_f32(half_of(xv[u][q / 2], q % 2)), acc, 0, 0, 0);
+            for (int q = 0; q < 2; ++q) {
+                wd[q] = T::to_f32(half_of(wc[q][e / 2], e % 2));
+                xd[q] = T::to_f32(half_of(xc[q][e / 2], e % 2));
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) acc[q][t] = __builtin_amdgcn_mfma_f64_16x16x4f64(wd[q], xd[t], acc[q][t], 0, 0, 0);
         }
     }
 #pragma unroll
-    for (int v = 0; v < 4; ++v) red[wave][v][lane] = acc[v];
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) red[wave][q * 2 + t][v][lane] = acc[q][t][v];
     __syncthreads();
-    if (wave >= 4) return;
-    double s = red[0][wave][lane];
-    for (int q = 1; q < kTileWaves; ++q) s += red[q][wave][lane];
-    if (tok < a.b && e0 + 4 * wave + g < a.experts) a.logits[tok * a.experts + e0 + 4 * wave + g] = s;
+    const int blk = wave / 4, v = wave % 4;
+    double sum = red[0][blk][v][lane];
+    for (int q = 1; q < kTileWaves; ++q) sum += red[q][blk][v][lane];
+    const int64_t t = t0 + blk % 2 * 16 + li, e = e0 + blk / 2 * 16 + 4 * v + g;
+    if (t < a.b && e < a.experts) a.logits[(slice * a.b + t) * a.experts + e] = sum;
 }
 
 // Maximum over the 64 lanes, uniform: the upper halves first, the lower ones among those that tie.
@@ -139,7 +161,9 @@ __device__ __forceinline__ void choose_experts(const RouteArgs &a, int64_t tok) 
 #pragma unroll
     for (int i = 0; i < H; ++i) {
         const int e = i * kWave + lane;
-        l[i] = a.logits[tok * a.experts + (e < a.experts ? e : 0)];
+        const double *const from = a.logits + tok * a.experts + (e < a.experts ? e : 0);
+        l[i] = from[0];
+        for (int q = 1; q < a.slices; ++q) l[i] += from[q * a.b * a.experts];
         key[i] = e < a.experts ? order_key(l[i]) : 0;
         p[i] = 0;
         best = best > key[i] ? best : key[i];
@@ -207,8 +231,8 @@ __global__ __launch_bounds__(kWave) void route_choose_kernel(RouteArgs a) {
 
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
     const unsigned b = (unsigned)a.b;
-    if (a.b * a.experts >= 16384) {
-        const dim3 grid((unsigned)((a.experts + 15) / 16), (b + 15) / 16);
+    if (a.tiled) {
+        const dim3 grid((unsigned)((a.experts + 31) / 32), (b + 31) / 32, (unsigned)a.slices);
         if (a.bf16)
             route_logits_tile_kernel<BF16><<<grid, kTileWaves * kWave, 0, stream>>>(a);
         else
@@ -222,7 +246,7 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    route_choose_kernel<<<(unsigned)a.b, kWave, 0, stream>>>(a);
+    route_choose_kernel<<<b, kWave, 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -34,11 +34,12 @@ twq_status done(hipError_t e, const char *name) { return e == hipSuccess ? TWQ_O
 
 const uint16_t *u16(const void *p) { return static_cast<const uint16_t *>(p); }
 
-size_t route_bytes(int64_t b, int64_t experts) { return align256((size_t)(b * experts) * 8); }
-
 RouteArgs route_args(const void *x, const void *wr, const float *bias, int64_t b, int64_t m, int64_t experts, int64_t k, int score,
                      int norm, float scale, int type, int32_t *ids, float *weights, void *logits) {
+    const RoutePlan p = plan_route(b, m, experts);
     RouteArgs a{};
+    a.tiled = p.tiled;
+    a.slices = p.slices;
     a.x = u16(x);
     a.wr = u16(wr);
     a.bias = bias;
@@ -154,7 +155,7 @@ twq_status twq_linear_a16(const void *x, const void *qw, const float *sw, const 
 
 size_t twq_moe_route_workspace_bytes(int64_t b, int64_t m, int64_t experts, int64_t k) {
     if (!valid_route(b, m, experts, k)) return 0;
-    return route_bytes(b, experts);
+    return b > 0 ? plan_route(b, m, experts).total : 0;
 }
 
 twq_status twq_moe_route(const void *x, const void *wr, const float *bias, int64_t b, int64_t m, int64_t experts, int64_t k,
@@ -165,7 +166,8 @@ twq_status twq_moe_route(const void *x, const void *wr, const float *bias, int64
     if (b == 0) return TWQ_OK;
     if (!x || !wr || !ids || !weights) return TWQ_ERR_NULL;
     if (!aligned16(x) || !aligned16(wr) || !aligned16(bias) || !aligned16(ids) || !aligned16(weights)) return TWQ_ERR_ALIGN;
-    if (!workspace || workspace_bytes < route_bytes(b, experts)) return TWQ_ERR_WORKSPACE;
+    const size_t need = plan_route(b, m, experts).total;
+    if (!workspace || workspace_bytes < need) return TWQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return TWQ_ERR_ALIGN;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const RouteArgs a = route_args(x, wr, bias, b, m, experts, k, score, norm, scale, type, ids, weights, workspace);

@@ -204,6 +204,18 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
     return p;
 }
 
+RoutePlan plan_route(int64_t b, int64_t m, int64_t experts) {
+    RoutePlan p{};
+    p.slices = 1;
+    p.tiled = b * experts >= 16384;
+    if (p.tiled) {
+        const int64_t tiles = (experts + 31) / 32 * ((b + 31) / 32);
+        while (p.slices < 8 && tiles * p.slices < 256 && m / 512 >= p.slices * 2) p.slices *= 2;
+    }
+    p.total = ((size_t)(p.slices * b * experts) * 8 + 255) & ~size_t(255);
+    return p;
+}
+
 MoePlan plan_moe(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k) {
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     MoePlan p{};
@@ -222,7 +234,7 @@ MoePlan plan_moe(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k) {
     p.entries = p.part;
     p.experts = !p.few ? p.part + up((size_t)(p.ks * pairs * m) * 4) : p.entries + up((size_t)pairs * sizeof(MoeEntry) + 16);
     p.logits = p.experts;
-    p.ids = p.logits + up((size_t)(b * experts) * 8);
+    p.ids = p.logits + plan_route(b, m, experts).total;
     p.weights = p.ids + up((size_t)pairs * 4);
     p.total = p.weights + up((size_t)pairs * 4);
     return p;

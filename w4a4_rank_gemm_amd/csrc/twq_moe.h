@@ -65,10 +65,17 @@ struct RouteArgs {
     int sigmoid;          // scores: sigmoid (1) or softmax (0) of the logits
     int norm;             // weights divided by their sum
     float scale;
-    double *logits;       // [b][experts]
+    int tiled;            // logits on matrix instructions
+    int slices;           // K slices of the logits
+    double *logits;       // [slices][b][experts]
     int32_t *ids;         // [b][k]
     float *weights;       // [b][k]
 };
+struct RoutePlan {
+    int tiled, slices;
+    size_t total;  // logits
+};
+RoutePlan plan_route(int64_t b, int64_t m, int64_t experts);  // plan.cpp
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
 
 // Tokens whose outputs the down kernel sums by itself, from a work list of at most kFewPairs entries.
