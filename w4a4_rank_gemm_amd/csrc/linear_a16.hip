@@ -67,12 +67,27 @@ hipError_t launch_a16_t(const A16Args &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// acc += T L2 for 16 FM rows and FN panels, this wave's share of the ranks (blocks of 32). T is
-// summed over its slices in order and taken as two bf16 parts (16 significant bits), L2 as its
-// two exact ones: the four products are T L2 up to 2^-17 of T.
+// Eight ranks k .. k + 7 of row `row` of T, summed over its slices in order, as two bf16 parts
+// (16 significant bits); zeros past the last rank.
+__device__ __forceinline__ void few_t(const A16Args &a, int64_t row, int k, v4i &hi, v4i &lo) {
+    const float *p = a.t + row * a.r + (k < a.r ? k : 0);
+    const v4f t[2] = {sum_slices(p, a.b * a.r, a.tks), sum_slices(p + 4, a.b * a.r, a.tks)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float v0 = k < a.r ? t[e / 2][e % 2 * 2] : 0.f, v1 = k < a.r ? t[e / 2][e % 2 * 2 + 1] : 0.f;
+        const uint16_t h0 = BF16::from_f32(v0), h1 = BF16::from_f32(v1);
+        const uint16_t l0 = BF16::from_f32(v0 - BF16::to_f32(h0)), l1 = BF16::from_f32(v1 - BF16::to_f32(h1));
+        hi[e] = (int)((uint32_t)h0 | (uint32_t)h1 << 16);
+        lo[e] = (int)((uint32_t)l0 | (uint32_t)l1 << 16);
+    }
+}
+
+// acc += T L2 for 16 FM rows and FN panels, a wave's blocks of 32 ranks share, share + shares, .. L2
+// is taken as its two exact bf16 parts: the four products are T L2 up to 2^-18 of T. Up to four rows
+// a wave sums the slices of T for itself (staged is NULL); more rows share what stage_t left.
 template <int FN, int FM>
-__device__ __forceinline__ void few_lowrank(const A16Args &a, int64_t row0, int64_t last, const int64_t (&chan)[FN], int share,
-                                            int shares, v4f (&acc)[FN][FM]) {
+__device__ __forceinline__ void few_lowrank(const A16Args &a, const uint8_t *staged, const int64_t (&chan)[FN], int share, int shares,
+                                            v4f (&acc)[FN][FM]) {
     const int lane = threadIdx.x % kWave, li = lane & 15, g = lane >> 4;
     for (int rb = share; rb * 32 < a.r; rb += shares) {
         const int k = rb * 32 + g * 8, kc = k < a.r ? k : a.r - 8;
@@ -81,18 +96,14 @@ __device__ __forceinline__ void few_lowrank(const A16Args &a, int64_t row0, int6
         for (int f = 0; f < FN; ++f) split_f16(load16(a.l2t + (chan[f] + li) * a.r + kc), wh[f], wl[f]);
 #pragma unroll
         for (int c = 0; c < FM; ++c) {
-            const int64_t row = row0 + c * 16 + li < last ? row0 + c * 16 + li : last - 1;
-            const float *p = a.t + row * a.r + kc;
-            v4f t0 = sum_slices(p, a.b * a.r, a.tks), t1 = sum_slices(p + 4, a.b * a.r, a.tks);
             v4i th, tl;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float v0 = k < a.r ? (e < 2 ? t0[2 * e] : t1[2 * e - 4]) : 0.f;
-                const float v1 = k < a.r ? (e < 2 ? t0[2 * e + 1] : t1[2 * e - 3]) : 0.f;
-                const uint16_t h0 = BF16::from_f32(v0), h1 = BF16::from_f32(v1);
-                th[e] = (int)((uint32_t)h0 | (uint32_t)h1 << 16);
-                const uint16_t l0 = BF16::from_f32(v0 - BF16::to_f32(h0)), l1 = BF16::from_f32(v1 - BF16::to_f32(h1));
-                tl[e] = (int)((uint32_t)l0 | (uint32_t)l1 << 16);
+            if (staged) {
+                const uint8_t *p = staged + (kc / 8 * (16 * FM) + c * 16 + li) * 32;
+                const v4i zero = {0, 0, 0, 0};
+                th = k < a.r ? load16(p) : zero;
+                tl = k < a.r ? load16(p + 16) : zero;
+            } else {
+                few_t(a, li < a.b ? li : a.b - 1, k, th, tl);
             }
 #pragma unroll
             for (int f = 0; f < FN; ++f) {
@@ -105,16 +116,32 @@ __device__ __forceinline__ void few_lowrank(const A16Args &a, int64_t row0, int6
     }
 }
 
+// T's parts of all rows to LDS, [r / 8][R rows][hi, lo], by the whole CTA: each of its waves would
+// otherwise read T's slices again (64 tokens, 4096 -> 14336, 64 ranks: 44 us, this way 31).
+template <int R>
+__device__ __forceinline__ void stage_t(const A16Args &a, uint8_t *lds) {
+    __syncthreads();
+    const int eights = a.r / 8;
+    for (int i = threadIdx.x; i < (int)a.b * eights; i += kFewWaves * kWave) {
+        const int row = i / eights, k8 = i % eights;
+        v4i hi, lo;
+        few_t(a, row, k8 * 8, hi, lo);
+        *reinterpret_cast<v4i *>(lds + (k8 * R + row) * 32) = hi;
+        *reinterpret_cast<v4i *>(lds + (k8 * R + row) * 32 + 16) = lo;
+    }
+    __syncthreads();
+}
+
 // Stores the row blocks c = share, share + shares, .. of FN panels: Y, or this slice's sums.
 template <class T, int FN, int FM>
-__device__ __forceinline__ void a16_store(const A16Args &a, const v4f (&acc)[FN][FM], int64_t row0, int64_t last, int64_t panel0,
-                                          int64_t slice, int shares, int share) {
+__device__ __forceinline__ void a16_store(const A16Args &a, const v4f (&acc)[FN][FM], int64_t panel0, int64_t slice, int shares,
+                                          int share) {
     const int64_t panels = a.n / 16;
     const int lane = threadIdx.x % kWave, li = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int c = 0; c < FM; ++c) {
-        const int64_t row = row0 + c * 16 + li;
-        if (c % shares != share || row >= last) continue;
+        const int64_t row = c * 16 + li;
+        if (c % shares != share || row >= a.b) continue;
 #pragma unroll
         for (int f = 0; f < FN; ++f) {
             if (panel0 + f >= panels) continue;
@@ -129,16 +156,15 @@ __device__ __forceinline__ void a16_store(const A16Args &a, const v4f (&acc)[FN]
     }
 }
 
-// Few rows: groups of KW waves (kw, a power of two) own FN panels of 16 channels and up to XR rows
-// each over a slice of K, which their waves split; the waves' sums are added in wave order.
+// Up to 16 rows: groups of kw waves (a power of two) own FN panels of 16 channels each and split their
+// K; the waves' sums are added in wave order.
 template <class T, int FN, int XR, int U>
 __global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a, int kw) {
     typedef FewRows<T, FN, XR, 1, U> Rows;
-    constexpr int FM = Rows::FM, RED = kFewWaves * FN * FM * 1024;
-    __shared__ __align__(16) uint8_t smem[kFewWaves * Rows::LDS > RED ? kFewWaves * Rows::LDS : RED];
+    static_assert(Rows::FM == 1 && kFewWaves * Rows::LDS >= XR * 4 * 256, "T's parts of 256 ranks");
+    __shared__ __align__(16) uint8_t smem[kFewWaves * Rows::LDS];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), share = wave & (kw - 1);
-    const int64_t panels = a.n / 16, pieces = a.m / 128, row0 = (int64_t)blockIdx.y * XR, slice = blockIdx.z;
-    const int64_t panel0 = ((int64_t)blockIdx.x * kFewWaves + wave) / kw * FN, last = row0 + XR < a.b ? row0 + XR : a.b;
+    const int64_t panels = a.n / 16, pieces = a.m / 128, panel0 = ((int64_t)blockIdx.x * kFewWaves + wave) / kw * FN;
     Rows rows;
     int64_t chan[FN];
 #pragma unroll
@@ -149,32 +175,35 @@ __global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a, in
         rows.s[f] = a.sw + p * 16;
     }
     rows.s_stride = a.n;
-    rows.x = a.x + row0 * a.m;
+    rows.x = a.x;
 #pragma unroll
     for (int j = 0; j < Rows::XL; ++j) {
-        const int row = 4 * j + lane / 16, most = (int)(last - row0) - 1;
-        rows.row[j] = (uint32_t)((row < most ? row : most) * a.m * 2);
+        const int row = 4 * j + lane / 16;
+        rows.row[j] = (uint32_t)((row < a.b ? row : a.b - 1) * a.m * 2);
     }
-    v4f acc[FN][FM] = {};
-    const int64_t part = slice * kw + share, parts = (int64_t)a.ks * kw;
-    if (panel0 < panels) {
-        rows.run((int)(part * pieces / parts), (int)((part + 1) * pieces / parts), smem + wave * Rows::LDS, acc, [&] {
-            if (a.r > 0 && slice == 0) few_lowrank<FN, FM>(a, row0, last, chan, share, kw, acc);
+    v4f acc[FN][1] = {};
+    if (panel0 < panels)
+        rows.run((int)(share * pieces / kw), (int)((share + 1) * pieces / kw), smem + wave * Rows::LDS, acc, [&] {
+            if (XR == 4 && a.r > 0) few_lowrank<FN, 1>(a, nullptr, chan, share, kw, acc);
         });
+    if (XR > 4 && a.r > 0) {
+        stage_t<16>(a, smem);
+        if (panel0 < panels) few_lowrank<FN, 1>(a, smem, chan, share, kw, acc);
     }
     join_waves(smem, kw, wave, acc);
-    a16_store<T, FN, FM>(a, acc, row0, last, panel0, slice, kw, share);
+    a16_store<T, FN, 1>(a, acc, panel0, 0, kw, share);
 }
 
-// The same with rows and K shared by the CTA's eight waves, FN panels each (SharedRows).
+// Up to 64 rows: the CTA's eight waves own FN panels each and share the rows and a slice of K.
 template <class T, int FN, int XR, int U>
 __global__ __launch_bounds__(kSharedWaves *kWave) void a16_shared_kernel(A16Args a) {
     typedef SharedRows<T, FN, XR, 1, U> Rows;
     constexpr int FM = Rows::FM;
+    static_assert(Rows::LDS >= XR * 4 * 256 && kSharedWaves == kFewWaves, "T's parts of 256 ranks");
     __shared__ __align__(16) uint8_t smem[Rows::LDS];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int64_t panels = a.n / 16, pieces = a.m / 128, row0 = (int64_t)blockIdx.y * XR, slice = blockIdx.z;
-    const int64_t panel0 = ((int64_t)blockIdx.x * kSharedWaves + wave) * FN, last = row0 + XR < a.b ? row0 + XR : a.b;
+    const int64_t panels = a.n / 16, pieces = a.m / 128, slice = blockIdx.y;
+    const int64_t panel0 = ((int64_t)blockIdx.x * kSharedWaves + wave) * FN;
     Rows rows;
     int64_t chan[FN];
 #pragma unroll
@@ -185,17 +214,19 @@ __global__ __launch_bounds__(kSharedWaves *kWave) void a16_shared_kernel(A16Args
         rows.s[f] = a.sw + p * 16;
     }
     rows.s_stride = a.n;
-    rows.x = a.x + row0 * a.m;
+    rows.x = a.x;
 #pragma unroll
     for (int j = 0; j < Rows::PER; ++j) {
-        const int row = Rows::row_of(j), most = (int)(last - row0) - 1;
-        rows.row[j] = (uint32_t)((row < most ? row : most) * a.m * 2);
+        const int row = Rows::row_of(j);
+        rows.row[j] = (uint32_t)((row < a.b ? row : a.b - 1) * a.m * 2);
     }
     v4f acc[FN][FM] = {};
-    rows.run((int)(slice * pieces / a.ks), (int)((slice + 1) * pieces / a.ks), smem, acc, [&] {
-        if (a.r > 0 && slice == 0) few_lowrank<FN, FM>(a, row0, last, chan, 0, 1, acc);
-    });
-    a16_store<T, FN, FM>(a, acc, row0, last, panel0, slice, 1, 0);
+    rows.run((int)(slice * pieces / a.ks), (int)((slice + 1) * pieces / a.ks), smem, acc);
+    if (a.r > 0 && slice == 0) {
+        stage_t<XR>(a, smem);
+        few_lowrank<FN, FM>(a, smem, chan, 0, 1, acc);
+    }
+    a16_store<T, FN, FM>(a, acc, panel0, slice, 1, 0);
 }
 
 // Y = the slices' sums in slice order, rounded once.
@@ -218,16 +249,14 @@ static hipError_t a16_join(const A16Args &a, hipStream_t stream) {
 template <class T, int FN, int XR, int U>
 static hipError_t a16_few(const A16Args &a, const A16Plan &p, hipStream_t stream) {
     const int64_t groups = (a.n / 16 + FN - 1) / FN, per = kFewWaves / p.kw;
-    const dim3 grid((unsigned)((groups + per - 1) / per), (unsigned)((a.b + XR - 1) / XR), (unsigned)a.ks);
-    a16_few_kernel<T, FN, XR, U><<<grid, kFewWaves * kWave, 0, stream>>>(a, p.kw);
-    const hipError_t e = hipGetLastError();
-    return e != hipSuccess || a.ks == 1 ? e : a16_join<T>(a, stream);
+    a16_few_kernel<T, FN, XR, U><<<dim3((unsigned)((groups + per - 1) / per)), kFewWaves * kWave, 0, stream>>>(a, p.kw);
+    return hipGetLastError();
 }
 
 template <class T, int FN, int XR, int U>
 static hipError_t a16_shared(const A16Args &a, hipStream_t stream) {
     const int64_t groups = (a.n / 16 + FN - 1) / FN;
-    const dim3 grid((unsigned)((groups + kSharedWaves - 1) / kSharedWaves), (unsigned)((a.b + XR - 1) / XR), (unsigned)a.ks);
+    const dim3 grid((unsigned)((groups + kSharedWaves - 1) / kSharedWaves), (unsigned)a.ks);
     a16_shared_kernel<T, FN, XR, U><<<grid, kSharedWaves * kWave, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || a.ks == 1 ? e : a16_join<T>(a, stream);

@@ -459,9 +459,10 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_few_kernel(MoeArgs a) {
 
 // Many rows an expert, or many experts: the CTA's eight waves share an expert's rows and K, and own
 // eight panels of inner (output) channels each.
-template <class T, int XR, int U>
+template <class T>
 __global__ __launch_bounds__(kMoeThreads) void moe_up_shared_kernel(MoeArgs a) {
-    typedef SharedRows<T, 2, XR, 1, U> Rows;
+    constexpr int XR = 32;
+    typedef SharedRows<T, 2, XR, 1, 1> Rows;
     __shared__ __align__(16) uint8_t smem[Rows::LDS];
     __shared__ uint16_t list[kMaxPairs];
     __shared__ int count[kMoeWaves];
@@ -486,7 +487,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_shared_kernel(MoeArgs a) {
             r.row[j] = (uint32_t)((list[i + (row < rows ? row : rows - 1)] / a.k) * a.m * 2);
         }
         v4f acc[2][Rows::FM] = {};
-        r.run(0, (int)pieces, smem, acc, [] {});
+        r.run(0, (int)pieces, smem, acc);
 #pragma unroll
         for (int c = 0; c < Rows::FM; ++c)
             if (c * 16 + lane % 16 < rows) store_inner(a, acc[0][c], acc[1][c], list[i + c * 16 + lane % 16], panel);
@@ -518,7 +519,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_shared_kernel(MoeArgs a)
             r.row[j] = (uint32_t)(list[i + (row < rows ? row : rows - 1)] * a.f * 4);  // at most 4095 x 2^19
         }
         v4f acc[1][Rows::FM] = {};
-        r.run((int)(slice * pieces / a.ks), (int)((slice + 1) * pieces / a.ks), smem, acc, [] {});
+        r.run((int)(slice * pieces / a.ks), (int)((slice + 1) * pieces / a.ks), smem, acc);
 #pragma unroll
         for (int c = 0; c < Rows::FM; ++c)
             if (c * 16 + lane % 16 < rows) {
@@ -554,7 +555,7 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
 template <class T>
 static hipError_t moe_typed(const MoeArgs &a, const MoePlan &p, hipStream_t stream) {
     if (p.up_shared)
-        moe_up_shared_kernel<T, 32, 1><<<dim3((unsigned)(a.f / 128), (unsigned)p.slots), kMoeThreads, 0, stream>>>(a);
+        moe_up_shared_kernel<T><<<dim3((unsigned)(a.f / 128), (unsigned)p.slots), kMoeThreads, 0, stream>>>(a);
     else
         moe_up_kernel<T><<<dim3((unsigned)((a.f / 16 * p.up_waves + kMoeWaves - 1) / kMoeWaves), (unsigned)(p.slots + p.few)), kMoeThreads, 0,
                            stream>>>(a, p.slots, p.up_waves);

@@ -203,8 +203,7 @@ struct SharedRows {
     // Row of this thread's chunk j.
     static __device__ __forceinline__ int row_of(int j) { return (j * NT + (int)threadIdx.x) / 16 % XR; }
 
-    template <class F>
-    __device__ __forceinline__ void run(int p0, int p1, uint8_t *lds, v4f (&acc)[FN][FM], F &&between) const {
+    __device__ __forceinline__ void run(int p0, int p1, uint8_t *lds, v4f (&acc)[FN][FM]) const {
         const int tid = threadIdx.x, lane = tid % kWave, li = lane & 15, g = lane >> 4;
         const Codes<T> codes;
         const v4f zero = held_zero();
@@ -236,9 +235,8 @@ struct SharedRows {
             for (int f = 0; f < FN; ++f)
                 sn[f] = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(s[f]) + p * s_step + (q + soff));
         };
-        if (p0 >= p1) return between();
+        if (p0 >= p1) return;
         load(p0);
-        between();
         float *const scales = reinterpret_cast<float *>(lds + 2 * U * PIECE) + tid / kWave * FN * 64;
         int put[PER];
 #pragma unroll
