@@ -501,7 +501,9 @@ twq_status twq_linear_dx(const void *dy, const void *qw, const float *sw, const 
  *   qw, sw from twq_pack_weight_grouped;  l1t fp16 [r][m], l2t fp16 [n][r] (NULL iff r == 0)
  *   workspace: at least twq_linear_a16_workspace_bytes(b, m, n, r, g) bytes (0 where r == 0 and b
  *   is small: NULL is then allowed), rules as above
- * g must be 128 (TWQ_ERR_UNSUPPORTED otherwise); n at most 2^22.
+ * g must be 128 (TWQ_ERR_UNSUPPORTED otherwise); n at most 2^22, b n at most 2^37. y overlaps no
+ * input. A weight of twq_pack_weight (one scale a channel) serves with its scales repeated m / g times.
+ * A group's sum of products has to stay in binary32's range: |X| below 2^113 is always enough.
  */
 size_t twq_linear_a16_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r, int64_t g);
 twq_status twq_linear_a16(const void *x, const void *qw, const float *sw, const void *l1t, const void *l2t, int64_t r,
@@ -533,7 +535,8 @@ twq_status twq_linear_a16(const void *x, const void *qw, const float *sw, const 
  * the sum over the chosen if `norm` (all zero where that sum is), times `scale`.
  *   x [b][m], wr [experts][m] of `type`;  bias f32 [experts] or NULL;  k <= experts
  *   ids i32 [b][k] (out), weights f32 [b][k] (out)
- * With non-finite logits the choice is unspecified (ids still name k different experts).
+ * With non-finite logits the choice is unspecified (ids still name k different experts); a chosen NaN
+ * logit gives NaN weights. ids and weights overlap no input and not each other.
  */
 size_t twq_moe_route_workspace_bytes(int64_t b, int64_t m, int64_t experts, int64_t k);
 twq_status twq_moe_route(const void *x, const void *wr, const float *bias, int64_t b, int64_t m, int64_t experts, int64_t k,
@@ -542,7 +545,8 @@ twq_status twq_moe_route(const void *x, const void *wr, const float *bias, int64
 
 /*
  * The experts' products for a given choice: ids outside [0, experts) mean none (a token without
- * any gets zeros), an expert may be named more than once.
+ * any gets zeros; such a choice's weight is not used), an expert may be named more than once. Here
+ * and in twq_moe y overlaps no input.
  */
 size_t twq_moe_experts_workspace_bytes(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k);
 twq_status twq_moe_experts(const void *x, const int32_t *ids, const float *weights, const void *q1, const float *s1,

@@ -100,6 +100,43 @@ def test_extreme_and_non_finite_logits(b, e, k, score):
         assert all(len(set(r)) == k for r in ids2.tolist())
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("b,e", [(3, 64), (200, 96)])
+def test_nan_logits_give_nan_weights(b, e, score):
+    """A row of NaN logits has NaN weights, whether they are divided by their sum or not."""
+    x, wr, bias = _router(b, 256, e, torch.float16, 7)
+    x[b // 2, 5] = float("nan")
+    for kw in (dict(), dict(norm=False), dict(bias=bias), dict(bias=bias, norm=False)):
+        w = twq.moe_route(x, wr, 4, score=score, **kw)[1]
+        assert bool(w[b // 2].isnan().all()) and int(w.isnan().sum()) == 4, kw
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_experts_masked_by_the_bias(score):
+    """A bias of -inf, or of the type's lowest value, takes an expert out while others are left."""
+    for b, e, k in ((2, 20, 8), (150, 130, 8)):
+        x, wr, bias = _router(b, 256, e, torch.bfloat16, 8)
+        for low in (float("-inf"), torch.finfo(torch.float32).min):
+            bias[::2] = low
+            ids, w = twq.moe_route(x, wr, k, bias=bias, score=score)
+            want, ww = ref.route(x, wr, k, bias=bias, score=score)
+            assert torch.equal(ids.long(), want) and bool((ids % 2 == 1).all())
+            assert bool(((w.double() - ww).abs() <= 2.0 ** -23 * ww.abs() + 1e-37).all())
+
+
+@pytest.mark.parametrize("b", [1, 4, 5, 40])
+def test_weights_of_no_expert_are_not_used(b):
+    """Choices outside the range carry NaN weights, as a masked router's may."""
+    gate_up, down = _experts(256, 128, 6, 1)
+    g = _gen(b)
+    ids, w = _choice(b, 6, 4, "spread", g)
+    ids[:, 1], ids[:, 3] = -1, 6
+    x = torch.randn(b, 256, generator=g, device="cuda").half()
+    w2 = w.clone()
+    w[:, 1::2], w2[:, 1::2] = float("nan"), 0
+    assert torch.equal(twq.moe_experts(x, ids, w, gate_up, down), twq.moe_experts(x, ids, w2, gate_up, down))
+
+
 def _experts(m, f, e, seed):
     g = _gen(seed)
 

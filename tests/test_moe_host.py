@@ -55,6 +55,13 @@ def test_refused_shapes_and_types():
             assert call(**bad) == SHAPE, bad
 
 
+def test_outputs_of_one_call():
+    """b n at most 2^37."""
+    assert _a16(b=1 << 24, n=(1 << 13) + 16) == SHAPE and _a16(b=1 << 16, n=(1 << 21) + 16) == SHAPE
+    assert twq.lib().twq_linear_a16_workspace_bytes(1 << 24, 128, (1 << 13) + 16, 0, 128) == 0
+    assert twq.lib().twq_linear_a16_workspace_bytes(1 << 24, 128, 1 << 13, 0, 128) > 0
+
+
 def test_refused_pointers():
     for call, names, optional in ((_a16, ("x", "qw", "sw", "l1t", "l2t", "y"), ()),
                                   (_route, ("x", "wr", "ids", "w"), ("bias",)),

@@ -214,7 +214,7 @@ __device__ __forceinline__ void choose_experts(const RouteArgs &a, int64_t tok) 
     const double total = wave_sum_f64(w);
     if (lane < a.k) {
         a.ids[tok * a.k + lane] = mine;
-        a.weights[tok * a.k + lane] = (float)((a.norm ? (total > 0 ? w / total : 0.0) : w) * a.scale);
+        a.weights[tok * a.k + lane] = (float)((a.norm ? (total == 0 ? 0.0 : w / total) : w) * a.scale);
     }
 }
 

@@ -15,7 +15,8 @@ namespace {
 using namespace twq;
 
 constexpr int64_t kMaxA16N = int64_t(1) << 22;
-constexpr int64_t kMaxOutput = int64_t(1) << 40;
+// Outputs of one call: 256 GB, and fewer than 2^24 tiles, so that no grid dimension has 2^32 threads.
+constexpr int64_t kMaxOutput = int64_t(1) << 37;
 
 bool valid_type(int t) { return t == TWQ_F16 || t == TWQ_BF16; }
 bool valid_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
