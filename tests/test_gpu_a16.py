@@ -20,12 +20,22 @@ SHAPES = [
     (3, 1024, 28688, (0, 128)),
     (1, 512, 57360, (16,)),
     (5, 384, 80, (0, 48)),
+    (6, 128, 48, (0, 16)),
+    (10, 512, 32, (0, 16)),
+    (6, 128, 8208, (0, 16)),
+    (11, 1152, 8208, (0, 32)),
     (16, 4096, 4112, (0, 16, 128)),
     (9, 1152, 14352, (0, 64)),
     (13, 512, 28704, (0, 16)),
     (17, 256, 48, (0, 256)),
     (32, 4096, 4096, (0, 32)),
     (25, 896, 28704, (0, 48)),
+    (29, 1152, 6160, (0, 48)),
+    (21, 128, 6160, (0, 16)),
+    (50, 512, 24592, (0, 16)),
+    (37, 1152, 24592, (0, 16)),
+    (40, 128, 16400, (0, 16)),
+    (45, 1152, 528, (0, 32)),
     (33, 384, 112, (0, 16)),
     (61, 8192, 1040, (0, 64)),
     (64, 2048, 14352, (0, 128)),
@@ -33,6 +43,7 @@ SHAPES = [
     (70, 4224, 272, (0, 48)),
     (200, 1024, 1040, (0, 256)),
     (300, 256, 16400, (0, 32)),
+    (100, 1152, 65536, (0, 16)),
     (2100, 1152, 4112, (0, 16, 128)),
     (4200, 384, 4368, (0, 64)),
 ]

@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 
 # b, m, experts, k: both logit kernels, every number of keys a lane
 ROUTES = [(1, 128, 1, 1), (1, 2048, 64, 8), (3, 256, 5, 5), (5, 640, 65, 7), (17, 4096, 100, 16), (64, 1152, 256, 8),
-          (130, 512, 129, 4), (256, 384, 512, 16), (100, 7168, 250, 10), (256, 256, 64, 2), (33, 131072, 512, 3)]
+          (130, 512, 129, 4), (256, 384, 512, 16), (100, 7168, 250, 10), (256, 256, 64, 2), (33, 131072, 512, 3), (150, 2048, 130, 6)]
 
 
 def _router(b, m, e, dt, seed):
@@ -169,7 +169,9 @@ LAYERS = [
     (4, 384, 256, 8, 3, "one"), (5, 256, 384, 12, 4, "twice"), (3, 640, 128, 7, 5, "none"), (13, 1024, 384, 60, 4, "spread"),
     (16, 256, 256, 4, 4, "one"), (17, 128, 128, 20, 3, "none"), (30, 512, 256, 5, 2, "spread"), (64, 256, 256, 16, 8, "spread"),
     (37, 256, 128, 2, 16, "twice"), (100, 128, 384, 512, 2, "spread"), (256, 256, 128, 8, 2, "spread"), (256, 128, 128, 3, 16, "none"),
-    (200, 128, 256, 30, 4, "one"),
+    (200, 128, 256, 30, 4, "one"), (2, 1024, 128, 6, 2, "spread"), (3, 4096, 128, 9, 2, "twice"), (6, 2048, 128, 9, 3, "spread"),
+    (7, 4096, 256, 6, 2, "none"), (40, 128, 1024, 8, 2, "spread"), (128, 128, 1024, 8, 2, "spread"), (96, 256, 4096, 8, 2, "spread"),
+    (128, 128, 1024, 40, 2, "twice"), (130, 1024, 1152, 64, 4, "none"), (64, 2176, 2048, 16, 8, "one"),
 ]
 
 

@@ -194,16 +194,17 @@ __global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a, in
     a16_store<T, FN, 1>(a, acc, panel0, 0, kw, share);
 }
 
-// Up to 64 rows: the CTA's eight waves own FN panels each and share the rows and a slice of K.
-template <class T, int FN, int XR, int U>
+// Up to 64 rows: the CTA's eight waves, in groups of KG, own FN panels each and share the rows and a slice
+// of K.
+template <class T, int FN, int XR, int U, int KG>
 __global__ __launch_bounds__(kSharedWaves *kWave) void a16_shared_kernel(A16Args a) {
-    typedef SharedRows<T, FN, XR, 1, U> Rows;
+    typedef SharedRows<T, FN, XR, 1, U, KG> Rows;
     constexpr int FM = Rows::FM;
-    static_assert(Rows::LDS >= XR * 4 * 256 && kSharedWaves == kFewWaves, "T's parts of 256 ranks");
+    static_assert(Rows::LDS >= XR * 4 * 256 && Rows::LDS >= kSharedWaves * FN * FM * 1024 && kSharedWaves == kFewWaves, "T's parts of 256 ranks, sums");
     __shared__ __align__(16) uint8_t smem[Rows::LDS];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t panels = a.n / 16, pieces = a.m / 128, slice = blockIdx.y;
-    const int64_t panel0 = ((int64_t)blockIdx.x * kSharedWaves + wave) * FN;
+    const int64_t panel0 = ((int64_t)blockIdx.x * (kSharedWaves / KG) + wave / KG) * FN;
     Rows rows;
     int64_t chan[FN];
 #pragma unroll
@@ -224,9 +225,10 @@ __global__ __launch_bounds__(kSharedWaves *kWave) void a16_shared_kernel(A16Args
     rows.run((int)(slice * pieces / a.ks), (int)((slice + 1) * pieces / a.ks), smem, acc);
     if (a.r > 0 && slice == 0) {
         stage_t<XR>(a, smem);
-        few_lowrank<FN, FM>(a, smem, chan, 0, 1, acc);
+        few_lowrank<FN, FM>(a, smem, chan, wave % KG, KG, acc);
     }
-    a16_store<T, FN, FM>(a, acc, panel0, slice, 1, 0);
+    join_waves(smem, KG, wave, acc);
+    a16_store<T, FN, FM>(a, acc, panel0, slice, KG, wave % KG);
 }
 
 // Y = the slices' sums in slice order, rounded once.
@@ -253,11 +255,11 @@ static hipError_t a16_few(const A16Args &a, const A16Plan &p, hipStream_t stream
     return hipGetLastError();
 }
 
-template <class T, int FN, int XR, int U>
+template <class T, int FN, int XR, int U, int KG>
 static hipError_t a16_shared(const A16Args &a, hipStream_t stream) {
-    const int64_t groups = (a.n / 16 + FN - 1) / FN;
-    const dim3 grid((unsigned)((groups + kSharedWaves - 1) / kSharedWaves), (unsigned)a.ks);
-    a16_shared_kernel<T, FN, XR, U><<<grid, kSharedWaves * kWave, 0, stream>>>(a);
+    const int64_t groups = (a.n / 16 + FN - 1) / FN, per = kSharedWaves / KG;
+    const dim3 grid((unsigned)((groups + per - 1) / per), (unsigned)a.ks);
+    a16_shared_kernel<T, FN, XR, U, KG><<<grid, kSharedWaves * kWave, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || a.ks == 1 ? e : a16_join<T>(a, stream);
 }
@@ -266,8 +268,9 @@ template <class T>
 static hipError_t a16_rows(const A16Args &a, const A16Plan &p, hipStream_t stream) {
     if (p.rows == 4) return a16_few<T, 1, 4, 2>(a, p, stream);
     if (p.rows == 16) return p.fn == 1 ? a16_few<T, 1, 16, 1>(a, p, stream) : a16_few<T, 2, 16, 1>(a, p, stream);
-    if (p.rows == 32) return a16_shared<T, 1, 32, 2>(a, stream);
-    return p.fn == 1 ? a16_shared<T, 1, 64, 2>(a, stream) : a16_shared<T, 2, 64, 2>(a, stream);
+    if (p.rows == 32) return p.kw == 1 ? a16_shared<T, 1, 32, 2, 1>(a, stream) : a16_shared<T, 1, 32, 4, 2>(a, stream);
+    if (p.fn == 2) return a16_shared<T, 2, 64, 2, 1>(a, stream);
+    return p.kw == 1 ? a16_shared<T, 1, 64, 2, 1>(a, stream) : a16_shared<T, 1, 64, 2, 2>(a, stream);
 }
 
 // ---- many rows ---------------------------------------------------------------------------

@@ -462,7 +462,7 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_few_kernel(MoeArgs a) {
 template <class T>
 __global__ __launch_bounds__(kMoeThreads) void moe_up_shared_kernel(MoeArgs a) {
     constexpr int XR = 32;
-    typedef SharedRows<T, 2, XR, 1, 1> Rows;
+    typedef SharedRows<T, 2, XR, 1, 1, 1> Rows;
     __shared__ __align__(16) uint8_t smem[Rows::LDS];
     __shared__ uint16_t list[kMaxPairs];
     __shared__ int count[kMoeWaves];
@@ -497,7 +497,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_shared_kernel(MoeArgs a) {
 
 template <int XR>
 __global__ __launch_bounds__(kMoeThreads) void moe_down_shared_kernel(MoeArgs a) {
-    typedef SharedRows<BF16, 1, XR, 2, 1> Rows;
+    typedef SharedRows<BF16, 1, XR, 2, 1, 1> Rows;
     __shared__ __align__(16) uint8_t smem[Rows::LDS];
     __shared__ uint16_t list[kMaxPairs];
     __shared__ int count[kMoeWaves];

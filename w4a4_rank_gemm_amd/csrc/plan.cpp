@@ -176,7 +176,8 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
             while (p.kw < 8 && units * p.kw < (p.rows == 4 ? 3072 : 1536) && pieces >= p.kw * 2) p.kw *= 2;
         } else {
             p.fn = p.rows == 64 && panels >= 1536 ? 2 : 1;
-            const int64_t ctas = (panels + 8 * p.fn - 1) / (8 * p.fn);
+            p.kw = panels <= 1024 && (p.rows == 32 ? panels >= 384 : m <= 4096) ? 2 : 1;
+            const int64_t per = 8 / p.kw * p.fn, ctas = (panels + per - 1) / per;
             int64_t ks = 256 / ctas;
             if (ks > pieces / 4) ks = pieces / 4;
             p.ks = ks < 1 ? 1 : ks > 16 ? 16 : (int)ks;

@@ -182,12 +182,14 @@ struct FewRows {
 
 // The same product for the eight waves of a CTA that own neighbouring panel groups and share rows
 // and K: the rows' pieces p0 .. p1 - 1 go through LDS once for all of them, U at a time into one of
-// two buffers, with one barrier a step. All waves call it with the same pieces.
+// two buffers, with one barrier a step. All waves call it with the same pieces. KG neighbouring waves
+// own the same FN panels and take U / KG pieces of a step each (join_waves adds their sums).
 constexpr int kSharedWaves = 8;
 
-template <class T, int FN, int XR, int PARTS, int U>
+template <class T, int FN, int XR, int PARTS, int U, int KG>
 struct SharedRows {
-    static_assert(XR % 16 == 0 && U <= 4, "a batch's scales are one load");
+    static_assert(XR % 16 == 0 && U <= 4 && U % KG == 0, "a batch's scales are one load");
+    static constexpr int UW = U / KG;  // pieces of a step that are this wave's
     static constexpr int NT = kSharedWaves * kWave, FM = XR / 16;
     static constexpr int CHUNKS = U * PARTS * XR * 16, PER = CHUNKS / NT;  // 16-byte chunks of a step, and a thread's
     static_assert(CHUNKS % NT == 0, "every thread loads the same number of chunks");
@@ -207,7 +209,8 @@ struct SharedRows {
         const int tid = threadIdx.x, lane = tid % kWave, li = lane & 15, g = lane >> 4;
         const Codes<T> codes;
         const v4f zero = held_zero();
-        v4i wn[U][FN], xn[PER];
+        v4i wn[UW][FN], xn[PER];
+        const int mine = __builtin_amdgcn_readfirstlane(tid / kWave) % KG * UW;  // this wave's first
         float sn[FN];
         const uint32_t woff = li * 64 + g * 16, soff = li * 4;
         uint32_t xoff[PER];
@@ -222,8 +225,8 @@ struct SharedRows {
                 xn[j] = load16(xp + (xoff[j] + (U == 1 ? 0 : p + u < p1 ? u : p1 - 1 - p) * (256 * PARTS)));
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t q = p + u < p1 ? p + u : p1 - 1;
+            for (int u = 0; u < UW; ++u) {
+                const int64_t q = p + mine + u < p1 ? p + mine + u : p1 - 1;
 #pragma unroll
                 for (int f = 0; f < FN; ++f) {
                     const uint8_t *const a = w[f] + q * 1024;
@@ -247,12 +250,12 @@ struct SharedRows {
         const int get = g * SLOT + li * 16;
         uint8_t *buf = lds;
         for (int p = p0; p < p1; p += U) {
-            v4i wc[U][FN];
+            v4i wc[UW][FN];
             wave_fence();
 #pragma unroll
             for (int j = 0; j < PER; ++j) *reinterpret_cast<v4i *>(buf + put[j]) = Codes<T>::order(xn[j]);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int u = 0; u < UW; ++u)
 #pragma unroll
                 for (int f = 0; f < FN; ++f) wc[u][f] = wn[u][f];
 #pragma unroll
@@ -261,7 +264,8 @@ struct SharedRows {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             stage_barrier();  // this step's rows are written, and the other buffer is read
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < UW; ++u) {
+                const uint8_t *const rows = buf + (mine + u) * PIECE;
                 v4f t[FN][FM];
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
@@ -270,7 +274,7 @@ struct SharedRows {
                     for (int h = 0; h < PARTS; ++h)
 #pragma unroll
                         for (int c = 0; c < FM; ++c)
-                            xf[h][c] = load16(buf + u * PIECE + (h * 16 + d * 4) * SLOT + get + c * 256);
+                            xf[h][c] = load16(rows + (h * 16 + d * 4) * SLOT + get + c * 256);
 #pragma unroll
                     for (int f = 0; f < FN; ++f) {
                         const v4i wf = codes((uint32_t)wc[u][f][d]);
@@ -283,7 +287,7 @@ struct SharedRows {
                 }
 #pragma unroll
                 for (int f = 0; f < FN; ++f) {
-                    const v4f sc = *reinterpret_cast<const v4f *>(scales + f * 64 + u * 16 + g * 4);
+                    const v4f sc = *reinterpret_cast<const v4f *>(scales + f * 64 + (mine + u) * 16 + g * 4);
 #pragma unroll
                     for (int c = 0; c < FM; ++c)
 #pragma unroll

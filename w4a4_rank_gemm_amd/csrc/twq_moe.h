@@ -42,7 +42,7 @@ struct A16Args {
 struct A16Plan {
     int many;      // the tile kernel
     int rows;      // token rows a CTA
-    int fn, kw;    // few rows: panels of a wave; up to 16 rows: waves that share their K
+    int fn, kw;    // few rows: panels of a wave, and neighbouring waves that share their K
     int tks;       // K slices of X L1
     int ks;        // K slices of the product
     size_t t, x16, xe, mul, mask, unit, t16, te, part, total;
