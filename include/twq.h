@@ -499,8 +499,8 @@ twq_status twq_linear_dx(const void *dy, const void *qw, const float *sw, const 
  * bits, Y is rounded once. A non-finite element of X makes its row of Y non-finite and no other.
  *   x     [b][m], y [b][n] (out), both of `type`
  *   qw, sw from twq_pack_weight_grouped;  l1t fp16 [r][m], l2t fp16 [n][r] (NULL iff r == 0)
- *   workspace: at least twq_linear_a16_workspace_bytes(b, m, n, r, g) bytes (0 where r == 0 and b
- *   is small: NULL is then allowed), rules as above
+ *   workspace: at least twq_linear_a16_workspace_bytes(b, m, n, r, g) bytes (may be 0 where
+ *   b is small: NULL is then allowed), rules as above
  * g must be 128 (TWQ_ERR_UNSUPPORTED otherwise); n at most 2^22, b n at most 2^37. y overlaps no
  * input. A weight of twq_pack_weight (one scale a channel) serves with its scales repeated m / g times.
  * A group's sum of products has to stay in binary32's range: |X| below 2^113 is always enough.

@@ -25,22 +25,25 @@ def rules(tmp_path_factory):
 
 
 def _a16(rules, cases):
-    """(rows of a CTA, panels of a wave, waves that share K, one or more K slices, low-rank part) of each."""
+    """(rows of a CTA, panels of a wave, waves that share K, one or more K slices, low-rank part: none, T of a
+    launch before, T of the CTA's own) of each."""
     got = ask(rules, [("a16", *c) for c in cases])
     for (b, m, n, r), (many, rows, fn, kw, tks, ks) in zip(cases, got):
-        assert many == (b > 64) and (b <= rows or many) and 1 <= ks <= m // 128 and tks <= 64 and (tks >= 1) == (r > 0)
+        assert many == (b > 64) and (b <= rows or many) and 1 <= ks <= m // 128 and tks <= 64 and (tks == 0 or r > 0)
         assert many or m // 128 >= kw or rows > 16
-    return {(rows, fn, kw, ks > 1, r > 0) for (_, _, _, r), (many, rows, fn, kw, tks, ks) in zip(cases, got)}
+    return {(rows, fn, kw, ks > 1, 0 if r == 0 else 1 if tks else 2) for (_, _, _, r), (many, rows, fn, kw, tks, ks) in zip(cases, got)}
 
 
 def test_layer_variants(rules):
     reached = _a16(rules, test_gpu_a16.CASES)
     grid = [(b, m, n, r) for b in ROWS for m in (128, 256, 512, 1152, 4096, 5120, 8192, 14336, 131072)
-            for n in (16, 272, 1024, 4096, 6144, 8192, 14336, 16400, 22016, 28672, 65536, 1 << 20) for r in (0, 64)]
+            for n in (16, 272, 1024, 4096, 6144, 8192, 14336, 16400, 22016, 28672, 65536, 1 << 20) for r in (0, 16, 64)]
     chosen = _a16(rules, grid)
     assert {v[:4] for v in chosen} == {v[:4] for v in reached}
     assert {v[:2] for v in reached} == {(4, 1), (16, 1), (16, 2), (32, 1), (64, 1), (64, 2), (64, 0), (128, 0)}
-    assert {v[:2] for v in reached if v[4]} == {v[:2] for v in reached if not v[4]} == {v[:2] for v in reached}
+    for low in (0, 1):
+        assert {v[:2] for v in reached if v[4] == low} == {v[:2] for v in reached}
+    assert {v[:2] for v in reached if v[4] == 2} == {v[:2] for v in chosen if v[4] == 2} == {(4, 1), (16, 1), (16, 2)}
 
 
 def test_router_variants(rules):

@@ -16,6 +16,10 @@ SHAPES = [
     (1, 128, 16, (0, 16)),
     (1, 256, 48, (0, 48)),
     (2, 640, 400, (0, 16, 256)),
+    (3, 512, 96, (32, 64)),
+    (4, 2048, 272, (16,)),
+    (7, 256, 96, (80, 128)),
+    (16, 128, 8224, (112,)),
     (4, 4096, 4096, (0, 32)),
     (3, 1024, 28688, (0, 128)),
     (1, 512, 57360, (16,)),

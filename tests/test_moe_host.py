@@ -75,8 +75,9 @@ def test_refused_pointers():
 
 def test_workspaces():
     L = twq.lib()
-    assert L.twq_linear_a16_workspace_bytes(1, 4096, 4096, 0, 128) == 0  # nothing between the launches
-    for b, m, n, r in ((1, 4096, 4096, 16), (16, 512, 64, 32), (61, 14336, 4096, 0), (65, 256, 32, 0), (3000, 4096, 512, 64)):
+    assert L.twq_linear_a16_workspace_bytes(1, 4096, 4096, 0, 128) == 0  # one launch
+    assert L.twq_linear_a16_workspace_bytes(9, 512, 4096, 16, 128) == 0
+    for b, m, n, r in ((1, 4096, 4096, 16), (16, 4096, 64, 32), (61, 14336, 4096, 0), (65, 256, 32, 0), (3000, 4096, 512, 64)):
         need = L.twq_linear_a16_workspace_bytes(b, m, n, r, 128)
         assert need > 0 and _a16(b, m, n, r, wsb=need - 1) == WORKSPACE and _a16(b, m, n, r, ws=None) == WORKSPACE
     assert L.twq_linear_a16_workspace_bytes(65, 256, 32, 0, 128) >= 65 * 256 * 2

@@ -3,26 +3,24 @@
 //   y[i][j] = sum_G s_W[G][j] sum_{k in G} x[i][k] q[j][k] + sum_t (sum_k x[i][k] L1[k][t]) L2[t][j]
 //
 // G: groups of 128 input channels. X is fp16 or bf16 and used as it is; codes are exact in both
-// types, so the only roundings are those of the binary32 sums and the output's. T = X L1 comes from
-// a launch of its own (the adapters' shrink kernel), in partial sums over K slices.
+// types, so the only roundings are those of the binary32 sums, of T = X L1 to 16 (above 64 rows 22) bits and
+// the output's. T comes in partial sums over K slices from a launch of its own (up to 64 rows
+// a16_t_kernel, above the adapters' shrink kernel), or from the product's own CTAs where L1 is small.
 #include "twq_few_device.h"
 #include "twq_moe.h"
 
 namespace twq {
 
-// T = X L1 for few rows: a CTA owns 16 rows x 16 ranks over a slice of K, which its 16 waves
-// split; each wave's loads are all in flight before the first is used, and the waves' sums are
-// added in wave order. A fp16 L1 meets bf16 rows as two exact bf16 parts.
 constexpr int kFewWaves = 8;
 constexpr int kTWaves = 16, kTSteps = 4;
 
+// One wave's part of T = X L1 for 16 rows and 16 ranks: K steps s0 .. s1 - 1 of 32, a few steps'
+// loads in flight. A fp16 L1 meets bf16 rows as two exact bf16 parts. Result: lane (li, g)
+// holds row li, ranks 4 g .. 4 g + 3.
 template <class T>
-__global__ __launch_bounds__(kTWaves *kWave) void a16_t_kernel(A16Args a) {
-    __shared__ v4f red[kTWaves][kWave];
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, li = lane & 15, g = lane >> 4;
-    const int64_t rank0 = (int64_t)blockIdx.x * 16, row = (int64_t)blockIdx.y * 16 + li, slice = blockIdx.z;
-    const int steps = (int)(a.m / 32), parts = a.tks * kTWaves, part = (int)slice * kTWaves + wave;
-    const int s0 = (int)((int64_t)part * steps / parts), s1 = (int)((int64_t)(part + 1) * steps / parts);
+__device__ __forceinline__ v4f t_part(const A16Args &a, int64_t rank0, int64_t row0, int s0, int s1) {
+    const int lane = threadIdx.x % kWave, li = lane & 15, g = lane >> 4;
+    const int64_t row = row0 + li;
     const uint16_t *w = a.l1t + (rank0 + li) * a.m + g * 8, *x = a.x + (row < a.b ? row : a.b - 1) * a.m + g * 8;
     v4f acc = {0.f, 0.f, 0.f, 0.f};
     for (int s = s0; s < s1; s += kTSteps) {
@@ -46,6 +44,18 @@ __global__ __launch_bounds__(kTWaves *kWave) void a16_t_kernel(A16Args a) {
             }
         }
     }
+    return acc;
+}
+
+// T of up to 64 rows in a launch of its own: a CTA owns 16 rows x 16 ranks over a slice of K, which
+// its 16 waves split; their sums are added in wave order.
+template <class T>
+__global__ __launch_bounds__(kTWaves *kWave) void a16_t_kernel(A16Args a) {
+    __shared__ v4f red[kTWaves][kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, li = lane & 15, g = lane >> 4;
+    const int64_t rank0 = (int64_t)blockIdx.x * 16, row0 = (int64_t)blockIdx.y * 16, slice = blockIdx.z;
+    const int steps = (int)(a.m / 32), parts = a.tks * kTWaves, part = (int)slice * kTWaves + wave;
+    v4f acc = t_part<T>(a, rank0, row0, (int)((int64_t)part * steps / parts), (int)((int64_t)(part + 1) * steps / parts));
     red[wave][lane] = acc;
     __syncthreads();
     if (wave != 0) return;
@@ -55,7 +65,7 @@ __global__ __launch_bounds__(kTWaves *kWave) void a16_t_kernel(A16Args a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[e] += o[e];
     }
-    if (row < a.b) *reinterpret_cast<v4f *>(a.t + (slice * a.b + row) * a.r + rank0 + g * 4) = acc;
+    if (row0 + li < a.b) *reinterpret_cast<v4f *>(a.t + (slice * a.b + row0 + li) * a.r + rank0 + g * 4) = acc;
 }
 
 hipError_t launch_a16_t(const A16Args &a, hipStream_t stream) {
@@ -67,14 +77,21 @@ hipError_t launch_a16_t(const A16Args &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Partial sums of T: [slices][rows][r].
+struct TSums {
+    const float *t;
+    int64_t stride;  // rows r
+    int slices;
+};
+
 // Eight ranks k .. k + 7 of row `row` of T, summed over its slices in order, as two bf16 parts
 // (16 significant bits); zeros past the last rank.
-__device__ __forceinline__ void few_t(const A16Args &a, int64_t row, int k, v4i &hi, v4i &lo) {
-    const float *p = a.t + row * a.r + (k < a.r ? k : 0);
-    const v4f t[2] = {sum_slices(p, a.b * a.r, a.tks), sum_slices(p + 4, a.b * a.r, a.tks)};
+__device__ __forceinline__ void few_t(const TSums &ts, int r, int64_t row, int k, v4i &hi, v4i &lo) {
+    const float *p = ts.t + row * r + (k < r ? k : 0);
+    const v4f t[2] = {sum_slices(p, ts.stride, ts.slices), sum_slices(p + 4, ts.stride, ts.slices)};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float v0 = k < a.r ? t[e / 2][e % 2 * 2] : 0.f, v1 = k < a.r ? t[e / 2][e % 2 * 2 + 1] : 0.f;
+        const float v0 = k < r ? t[e / 2][e % 2 * 2] : 0.f, v1 = k < r ? t[e / 2][e % 2 * 2 + 1] : 0.f;
         const uint16_t h0 = BF16::from_f32(v0), h1 = BF16::from_f32(v1);
         const uint16_t l0 = BF16::from_f32(v0 - BF16::to_f32(h0)), l1 = BF16::from_f32(v1 - BF16::to_f32(h1));
         hi[e] = (int)((uint32_t)h0 | (uint32_t)h1 << 16);
@@ -83,10 +100,10 @@ __device__ __forceinline__ void few_t(const A16Args &a, int64_t row, int k, v4i 
 }
 
 // acc += T L2 for 16 FM rows and FN panels, a wave's blocks of 32 ranks share, share + shares, .. L2
-// is taken as its two exact bf16 parts: the four products are T L2 up to 2^-18 of T. Up to four rows
-// a wave sums the slices of T for itself (staged is NULL); more rows share what stage_t left.
-template <int FN, int FM>
-__device__ __forceinline__ void few_lowrank(const A16Args &a, const uint8_t *staged, const int64_t (&chan)[FN], int share, int shares,
+// is taken as its two exact bf16 parts: the four products are T L2 up to 2^-18 of T. `rank8` gives
+// eight ranks of a row (few_t, or what stage_t left).
+template <int FN, int FM, class F>
+__device__ __forceinline__ void few_lowrank(const A16Args &a, F &&rank8, const int64_t (&chan)[FN], int share, int shares,
                                             v4f (&acc)[FN][FM]) {
     const int lane = threadIdx.x % kWave, li = lane & 15, g = lane >> 4;
     for (int rb = share; rb * 32 < a.r; rb += shares) {
@@ -97,14 +114,7 @@ __device__ __forceinline__ void few_lowrank(const A16Args &a, const uint8_t *sta
 #pragma unroll
         for (int c = 0; c < FM; ++c) {
             v4i th, tl;
-            if (staged) {
-                const uint8_t *p = staged + (kc / 8 * (16 * FM) + c * 16 + li) * 32;
-                const v4i zero = {0, 0, 0, 0};
-                th = k < a.r ? load16(p) : zero;
-                tl = k < a.r ? load16(p + 16) : zero;
-            } else {
-                few_t(a, li < a.b ? li : a.b - 1, k, th, tl);
-            }
+            rank8(c * 16 + li, k, th, tl);
 #pragma unroll
             for (int f = 0; f < FN; ++f) {
                 acc[f][c] = BF16::mfma(wl[f], tl, acc[f][c]);
@@ -125,11 +135,32 @@ __device__ __forceinline__ void stage_t(const A16Args &a, uint8_t *lds) {
     for (int i = threadIdx.x; i < (int)a.b * eights; i += kFewWaves * kWave) {
         const int row = i / eights, k8 = i % eights;
         v4i hi, lo;
-        few_t(a, row, k8 * 8, hi, lo);
+        few_t({a.t, a.b * a.r, a.tks}, a.r, row, k8 * 8, hi, lo);
         *reinterpret_cast<v4i *>(lds + (k8 * R + row) * 32) = hi;
         *reinterpret_cast<v4i *>(lds + (k8 * R + row) * 32 + 16) = lo;
     }
     __syncthreads();
+}
+template <int R>
+__device__ __forceinline__ void staged_t(const uint8_t *lds, int r, int row, int k, v4i &hi, v4i &lo) {
+    const uint8_t *p = lds + ((k < r ? k : r - 8) / 8 * R + row) * 32;
+    const v4i zero = {0, 0, 0, 0};
+    hi = k < r ? load16(p) : zero;
+    lo = k < r ? load16(p + 16) : zero;
+}
+
+// T of at most 16 rows and kOwnRanks ranks by the CTA's eight waves: a wave takes 16 ranks and a share
+// of K, its sums go to t [slices][b][r].
+template <class T>
+__device__ __forceinline__ TSums own_t(const A16Args &a, float *t, int wave) {
+    const int blocks = a.r / 16, lane = threadIdx.x % kWave, li = lane & 15, g = lane >> 4;
+    const int slices = blocks > 4 ? 1 : blocks > 2 ? 2 : blocks > 1 ? 4 : 8, per = kFewWaves / slices;
+    const int block = wave & (per - 1), slice = wave / per, steps = (int)(a.m / 32);
+    if (block < blocks) {
+        const v4f s = t_part<T>(a, block * 16, 0, slice * steps / slices, (slice + 1) * steps / slices);
+        if (li < a.b) *reinterpret_cast<v4f *>(t + (slice * a.b + li) * a.r + block * 16 + g * 4) = s;
+    }
+    return {t, a.b * a.r, slices};
 }
 
 // Stores the row blocks c = share, share + shares, .. of FN panels: Y, or this slice's sums.
@@ -163,6 +194,7 @@ __global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a, in
     typedef FewRows<T, FN, XR, 1, U> Rows;
     static_assert(Rows::FM == 1 && kFewWaves * Rows::LDS >= XR * 4 * 256, "T's parts of 256 ranks");
     __shared__ __align__(16) uint8_t smem[kFewWaves * Rows::LDS];
+    __shared__ __align__(16) float tsums[XR * kOwnRanks];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), share = wave & (kw - 1);
     const int64_t panels = a.n / 16, pieces = a.m / 128, panel0 = ((int64_t)blockIdx.x * kFewWaves + wave) / kw * FN;
     Rows rows;
@@ -182,13 +214,24 @@ __global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a, in
         rows.row[j] = (uint32_t)((row < a.b ? row : a.b - 1) * a.m * 2);
     }
     v4f acc[FN][1] = {};
+    const bool own = a.r > 0 && a.tks == 0;
+    TSums ts = {a.t, a.b * a.r, a.tks};
+    auto rank8 = [&](int row, int k, v4i &hi, v4i &lo) { few_t(ts, a.r, row < a.b ? row : a.b - 1, k, hi, lo); };
+    auto between = [&] {
+        if (own) ts = own_t<T>(a, tsums, wave);
+        if (XR == 4 && a.r > 0 && !own) few_lowrank<FN, 1>(a, rank8, chan, share, kw, acc);
+    };
     if (panel0 < panels)
-        rows.run((int)(share * pieces / kw), (int)((share + 1) * pieces / kw), smem + wave * Rows::LDS, acc, [&] {
-            if (XR == 4 && a.r > 0) few_lowrank<FN, 1>(a, nullptr, chan, share, kw, acc);
-        });
-    if (XR > 4 && a.r > 0) {
+        rows.run((int)(share * pieces / kw), (int)((share + 1) * pieces / kw), smem + wave * Rows::LDS, acc, between);
+    else if (own)
+        own_t<T>(a, tsums, wave);
+    if (own) {
+        __syncthreads();
+        if (panel0 < panels) few_lowrank<FN, 1>(a, rank8, chan, share, kw, acc);
+    } else if (XR > 4 && a.r > 0) {
         stage_t<16>(a, smem);
-        if (panel0 < panels) few_lowrank<FN, 1>(a, smem, chan, share, kw, acc);
+        auto staged = [&](int row, int k, v4i &hi, v4i &lo) { staged_t<16>(smem, a.r, row, k, hi, lo); };
+        if (panel0 < panels) few_lowrank<FN, 1>(a, staged, chan, share, kw, acc);
     }
     join_waves(smem, kw, wave, acc);
     a16_store<T, FN, 1>(a, acc, panel0, 0, kw, share);
@@ -200,7 +243,9 @@ template <class T, int FN, int XR, int U, int KG>
 __global__ __launch_bounds__(kSharedWaves *kWave) void a16_shared_kernel(A16Args a) {
     typedef SharedRows<T, FN, XR, 1, U, KG> Rows;
     constexpr int FM = Rows::FM;
-    static_assert(Rows::LDS >= XR * 4 * 256 && Rows::LDS >= kSharedWaves * FN * FM * 1024 && kSharedWaves == kFewWaves, "T's parts of 256 ranks, sums");
+    static_assert(Rows::LDS >= XR * 4 * 256, "T's parts of 256 ranks");
+    static_assert(KG == 1 || Rows::LDS >= kSharedWaves * FN * FM * 1024, "sums of wave pairs");
+    static_assert(kSharedWaves == kFewWaves, "stage_t's threads");
     __shared__ __align__(16) uint8_t smem[Rows::LDS];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t panels = a.n / 16, pieces = a.m / 128, slice = blockIdx.y;
@@ -225,7 +270,8 @@ __global__ __launch_bounds__(kSharedWaves *kWave) void a16_shared_kernel(A16Args
     rows.run((int)(slice * pieces / a.ks), (int)((slice + 1) * pieces / a.ks), smem, acc);
     if (a.r > 0 && slice == 0) {
         stage_t<XR>(a, smem);
-        few_lowrank<FN, FM>(a, smem, chan, wave % KG, KG, acc);
+        auto staged = [&](int row, int k, v4i &hi, v4i &lo) { staged_t<XR>(smem, a.r, row, k, hi, lo); };
+        few_lowrank<FN, FM>(a, staged, chan, wave % KG, KG, acc);
     }
     join_waves(smem, KG, wave, acc);
     a16_store<T, FN, FM>(a, acc, panel0, slice, KG, wave % KG);

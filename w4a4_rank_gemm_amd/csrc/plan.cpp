@@ -157,12 +157,15 @@ DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
 
 // ---- the layer with 16-bit activations ----
 
+// Every CTA of the few-row kernels forms T for itself instead of reading what a launch before it left.
+static bool a16_own_t(int64_t b, int64_t m, int64_t r) { return b <= 16 && r <= kOwnRanks && m * r <= 32768; }
+
 A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     A16Plan p{};
     p.many = b > kFewTokens;
     if (r > 0 && p.many) p.tks = shrink_slices(b, m, r, (b + tile_rows(b) - 1) / tile_rows(b), 4);
-    if (r > 0 && !p.many) p.tks = m >= 16384 ? 16 : (int)((m + 1023) / 1024);
+    if (r > 0 && !p.many && !a16_own_t(b, m, r)) p.tks = m >= 16384 ? 16 : (int)((m + 1023) / 1024);
     p.ks = 1;
     p.x16 = up((size_t)p.tks * b * r * 4);
     p.total = p.x16;

@@ -13,6 +13,7 @@ namespace twq {
 // matrix cores (a tile kernel, which wants X in fp16 in the order of the expanded codes, and
 // the scales as ratios of neighbouring groups).
 constexpr int64_t kFewTokens = 64;
+constexpr int kOwnRanks = 128;  // of X L1 that a few-row CTA may form for itself
 constexpr int kA16N = 256;  // channels of a tile CTA: 64 a wave
 
 struct A16Args {
@@ -43,7 +44,7 @@ struct A16Plan {
     int many;      // the tile kernel
     int rows;      // token rows a CTA
     int fn, kw;    // few rows: panels of a wave, and neighbouring waves that share their K
-    int tks;       // K slices of X L1
+    int tks;       // K slices of X L1, 0: formed by the product's CTAs (or r = 0)
     int ks;        // K slices of the product
     size_t t, x16, xe, mul, mask, unit, t16, te, part, total;
 };
