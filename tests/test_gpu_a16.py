@@ -49,6 +49,7 @@ SHAPES = [
     (300, 256, 16400, (0, 32)),
     (100, 1152, 65536, (0, 16)),
     (2100, 1152, 4112, (0, 16, 128)),
+    (3000, 1152, 4112, (0, 16, 256)),
     (4200, 384, 4368, (0, 64)),
 ]
 CASES = [(b, m, n, r) for b, m, n, ranks in SHAPES for r in ranks]

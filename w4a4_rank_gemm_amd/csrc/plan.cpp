@@ -158,6 +158,9 @@ DxPlan plan_dx(int64_t b, int64_t m, int64_t n, int64_t r) {
 // ---- the layer with 16-bit activations ----
 
 // Every CTA of the few-row kernels forms T for itself instead of reading what a launch before it left.
+// With m r = 8192, 16384, 32768 and 65536 (m = n = 512, 1024, 2048, 2048; one token, fp16) 5.2, 6.1, 7.6
+// and 10.2 us, with the launch 6.9, 7.3, 7.7 and 7.8; 16 tokens 5.9, 6.9, 9.8, 13.3 and 7.8, 8.6, 10.2,
+// 10.0. A launch also costs the host 4 us.
 static bool a16_own_t(int64_t b, int64_t m, int64_t r) { return b <= 16 && r <= kOwnRanks && m * r <= 32768; }
 
 A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
@@ -165,6 +168,8 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
     A16Plan p{};
     p.many = b > kFewTokens;
     if (r > 0 && p.many) p.tks = shrink_slices(b, m, r, (b + tile_rows(b) - 1) / tile_rows(b), 4);
+    // T of few rows in slices of 1024: one token, 8192 -> 28672, 128 ranks 38.1 us; slices of 512, 2048 and
+    // 4096: 41.7, 38.8, 40.6 (16 tokens, 4096 -> 4096, 32 ranks: 12.1; 11.3, 13.6, 17.1)
     if (r > 0 && !p.many && !a16_own_t(b, m, r)) p.tks = m >= 16384 ? 16 : (int)((m + 1023) / 1024);
     p.ks = 1;
     p.x16 = up((size_t)p.tks * b * r * 4);
@@ -173,14 +178,26 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
         const int64_t panels = n / 16, pieces = m / 128;
         p.rows = b <= 4 ? 4 : b <= 16 ? 16 : b <= 32 ? 32 : 64;
         if (p.rows <= 16) {
+            // 5 to 16 rows: two panels a wave from 512 on (8192 channels). 4096 -> 8192: 9.7 us, one panel 9.9;
+            // 4096 -> 14336: 11.7 and 15.4; 14336 -> 4096: 17.1 and 14.5; 8 rows 4096 -> 4096: 8.1 and 6.9.
+            // Waves that share K: until there are 12 (6 of the 16-row kernel) a compute unit. One row,
+            // 4096 -> 14336 with 1, 2, 4, 8: 14.1, 10.9, 10.0, 10.9; 8192 -> 28672 32.7, 28.0, 31.0 (1, 2, 4);
+            // 14336 -> 4096 14.7, 10.8 (4, 8); 16 rows, 8192 -> 28672 56.5, 35.3, 36.0 (1, 2, 4).
             p.fn = p.rows == 4 || panels < 512 ? 1 : 2;
             const int64_t units = (panels + p.fn - 1) / p.fn;
             p.kw = 1;
             while (p.kw < 8 && units * p.kw < (p.rows == 4 ? 3072 : 1536) && pieces >= p.kw * 2) p.kw *= 2;
         } else {
+            // 64 rows, 8192 -> 28672: two panels a wave 50.8 us, one 57.5. Wave pairs that split K make CTAs of
+            // four panels, so that fewer K slices and no join fill the GPU: 32 rows, 4096 -> 6144, 8192, 14336
+            // 11.3, 11.7, 13.4 us, without 11.5, 12.2, 15.8 (4096 -> 4096 9.1 and 9.0; 14336 -> 4096 16.1 and
+            // 15.2; 4096 -> 22016 22.0 and 19.3); 64 rows 4096 -> 1024, 8192, 14336 8.9, 16.4, 20.0 and 9.6,
+            // 17.2, 22.8 (8192 -> 14336 36.6 and 35.3; 14336 -> 4096 22.9 and 21.6; 4096 -> 22016 33 and 28.5).
             p.fn = p.rows == 64 && panels >= 1536 ? 2 : 1;
             p.kw = panels <= 1024 && (p.rows == 32 ? panels >= 384 : m <= 4096) ? 2 : 1;
             const int64_t per = 8 / p.kw * p.fn, ctas = (panels + per - 1) / per;
+            // K slices: as many as leave one CTA a compute unit. 61 rows, 14336 -> 4096 with 4, 8, 16 (rule: 8)
+            // 28.7, 21.4, 25.1 us; 32 rows, 4096 -> 4096 with 4, 8 (8) 10.2, 9.8.
             int64_t ks = 256 / ctas;
             if (ks > pieces / 4) ks = pieces / 4;
             p.ks = ks < 1 ? 1 : ks > 16 ? 16 : (int)ks;
@@ -191,9 +208,14 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
     }
     const int64_t groups = m / 128, ntiles = (n + kA16N - 1) / kA16N;
     p.rows = 128;
-    if ((b + 127) / 128 * ntiles < 256) p.rows = 64;
+    // Tiles of 64 rows while those of 128 give a compute unit at most 1.5 on average (two fit): 1024 x 4096 ->
+    // 4096 59 and 69 us, 2048 x 4096 -> 4096 83 and 100 (256 tiles of 128), 1536 x 4096 -> 8192 124 and 127
+    // (384); 1024 x 4096 -> 14336 141 and 137 (448), 2048 x 4096 -> 8192 152 and 140 (512).
+    if ((b + 127) / 128 * ntiles <= 384) p.rows = 64;
     const int64_t ctas = (b + p.rows - 1) / p.rows * ntiles;
-    int64_t ks = 512 / ctas;
+    // K slices as many as leave one tile a compute unit: 256 x 4096 -> 4096 with 2, 4, 8 (rule: 4) 39.7, 32.1,
+    // 34.7 us; 128 x 14336 -> 4096 with 4, 8 (8) 61.6, 52.5; 1024 x 4096 -> 4096 with 1, 2, 4 (1) 57, 59, 71.
+    int64_t ks = 256 / ctas;
     if (ks > groups / 4) ks = groups / 4;
     if (ks > 8) ks = 8;
     p.ks = ks < 1 ? 1 : (int)ks;
@@ -211,10 +233,15 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
 RoutePlan plan_route(int64_t b, int64_t m, int64_t experts) {
     RoutePlan p{};
     p.slices = 1;
-    p.tiled = b * experts >= 16384;
+    // Tokens, experts, m: 128, 128, 4096 17.0 us tiled, 19.2 else; 256, 64, 4096 14.3 and 19.2; 96, 256, 4096
+    // 21.4 and 25.6; 256, 256, 7168 32 and 78; 64, 256, 4096 (the smallest) 22.2 and 21.1; below: 64, 128,
+    // 2048 14.0 and 12.1, 32, 512, 4096 26.2 and 22.5.
+    p.tiled = b >= 64 && b * experts >= 16384;
     if (p.tiled) {
         const int64_t tiles = (experts + 31) / 32 * ((b + 31) / 32);
-        while (p.slices < 8 && tiles * p.slices < 256 && m / 512 >= p.slices * 2) p.slices *= 2;
+        // one tile a compute unit, and few enough numbers for the choice to add: 256, 4096, 64 with 2, 4, 8 (rule:
+        // 8) 25.4, 17.6, 14.3; 72, 4096, 512 (4) 30.7, 27.6, 38.9; 256, 2048, 64 (4) 16.8, 12.9, 14.4
+        while (p.slices < 8 && tiles * p.slices < 256 && m / 512 >= p.slices * 2 && p.slices * experts <= 1024) p.slices *= 2;
     }
     p.total = ((size_t)(p.slices * b * experts) * 8 + 255) & ~size_t(255);
     return p;
@@ -224,11 +251,21 @@ MoePlan plan_moe(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k) {
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     MoePlan p{};
     const int64_t pairs = b * k, slots = pairs < experts ? pairs : experts;
+    // The down kernel that sums a token's outputs itself against the shared one with its join: 1 token, 8 of
+    // 64 experts 22.5 and 26 us, 2 of 8 wide ones 53 and 62; 2 tokens 26.5 and 29.7; 4 37.4 and 37.2;
+    // 13 54.3 and 52.2.
     p.few = b <= kFewMoe;
     p.slots = (int)slots;
+    // CTAs that share an expert's rows from 4 rows an expert on average: 128 tokens, 8 of 128 experts 314 us,
+    // waves with rows of their own 334; 256, 8 of 64 381 and 472; 64, 2 of 8 119 and 143; with 2 rows an
+    // expert (32, 8 of 128) 119 and 115, with 1 (13, 4 of 60) 55.6 and 51.9.
     p.up_shared = !p.few && pairs >= experts * 4 && f / 128 * slots >= 256;
+    // Waves that share K, 1, 2, 4, 8: one token, 8 of 64 experts 28.8, 24.5, 22.0, 22.5 us (rule: 4); 2 of 8 wide
+    // ones 55.6, 53.1, 54.5 (2); 13 tokens, 4 of 60 56.0, 52.2, 52.8 (2).
     p.up_waves = 1;
     while (p.up_waves < 8 && f / 16 * slots * p.up_waves < 5000 && m / 128 >= p.up_waves * 8) p.up_waves *= 2;
+    // Rows of a down tile, 16 or 32: 8 an expert (128 tokens, 8 of 128) 296 and 337 us; 16 (64, 2 of 8) 110 and
+    // 100; 32 (256, 8 of 64) 421 and 408.
     p.down_rows = pairs >= experts * 12 ? 32 : 16;
     p.ks = 1;
     if (!p.few)
