@@ -60,6 +60,14 @@ __device__ __forceinline__ v4f held_zero() {
     return z;
 }
 
+// LDS holds a piece of 16 or more rows as 16 slots, one for each (instruction d, quarter g), with 16
+// bytes a row; within 16 rows a row's place is XORed with this, and a step of d has 16 bytes more. A
+// 16-byte access serves 16 lanes in one pass, 0-3, 12-15, 20-23, 24-27 or 4-11, 16-19, 28-31 of each
+// half: reading, those are the 16 rows of two neighbouring quarters, in 16 different places. Neither
+// reads nor writes conflict (slots of 16 bytes more instead: half of the LDS cycles; 64 x 4096 -> 14336 20.4
+// and 19.5 us, 61 x 14336 -> 4096 21.7 and 20.9).
+__device__ __forceinline__ int row_turn(int g) { return ((g ^ g >> 1) & 1) << 2 | (g & 1) << 3; }
+
 // One wave's share of Y = X W^T for up to XR rows and FN panels of 16 channels: pieces (groups
 // of 128 elements of K) p0 .. p1 - 1, U in flight at a time. For each piece
 //
@@ -78,8 +86,8 @@ struct FewRows {
     static_assert(XR % 4 == 0 && U <= 4, "rows in fours; a batch's scales are one load");
     static constexpr int FM = (XR + 15) / 16;
     static constexpr int XL = XR / 4;                 // row loads of a piece and part
-    static constexpr int SLOT = XR * 16 + 16;         // one (instruction, quarter): 16 bytes a row, padded against bank conflicts
-    static constexpr int PIECE = PARTS * 16 * SLOT;
+    static constexpr int SLOT = XR * 16 + (XR < 16 ? 16 : 0);  // of one instruction and quarter
+    static constexpr int STEP = 4 * SLOT + (XR < 16 ? 0 : 16), PIECE = PARTS * 4 * STEP;
     static constexpr int LDS = U * PIECE + FN * 256;  // bytes of a wave
 
     // Pointers are the same in all lanes, and lanes add 32-bit offsets, so that a piece's addresses
@@ -126,8 +134,13 @@ struct FewRows {
         load(p0);
         between();
         float *const scales = reinterpret_cast<float *>(lds + U * PIECE);
-        const int put = ((lane & 3) * 4 + ((lane >> 2) & 3)) * SLOT + g * 16;  // chunk lane % 16 = 4 quarter + instruction
-        const int get = g * SLOT + (XR < 16 && li >= XR ? XR - 1 : li) * 16;
+        int put[XL];
+#pragma unroll
+        for (int j = 0; j < XL; ++j) {
+            const int d = lane & 3, q = lane >> 2 & 3;  // chunk lane % 16 = 4 quarter + instruction
+            put[j] = d * STEP + q * SLOT + ((j * 4 + g) ^ (XR < 16 ? 0 : row_turn(q))) * 16;
+        }
+        const int get = g * SLOT + (XR < 16 ? li < XR ? li : XR - 1 : li ^ row_turn(g)) * 16;
         for (int p = p0; p < p1; p += U) {
             v4i wc[U][FN];
             wave_fence();
@@ -139,7 +152,7 @@ struct FewRows {
                 for (int h = 0; h < PARTS; ++h)
 #pragma unroll
                     for (int j = 0; j < XL; ++j)
-                        *reinterpret_cast<v4i *>(lds + u * PIECE + h * 16 * SLOT + put + j * 64) = Codes<T>::order(xn[u][h][j]);
+                        *reinterpret_cast<v4i *>(lds + u * PIECE + h * 4 * STEP + put[j]) = Codes<T>::order(xn[u][h][j]);
             }
 #pragma unroll
             for (int f = 0; f < FN; ++f) scales[f * 64 + lane] = p + g < p1 ? sn[f] * (1.f / Codes<T>::kTimes) : 0.f;
@@ -155,7 +168,7 @@ struct FewRows {
                     for (int h = 0; h < PARTS; ++h)
 #pragma unroll
                         for (int c = 0; c < FM; ++c)
-                            xf[h][c] = load16(lds + u * PIECE + (h * 16 + d * 4) * SLOT + get + c * 256);
+                            xf[h][c] = load16(lds + u * PIECE + (h * 4 + d) * STEP + get + c * 256);
 #pragma unroll
                     for (int f = 0; f < FN; ++f) {
                         const v4i wf = codes((uint32_t)wc[u][f][d]);
@@ -193,7 +206,7 @@ struct SharedRows {
     static constexpr int NT = kSharedWaves * kWave, FM = XR / 16;
     static constexpr int CHUNKS = U * PARTS * XR * 16, PER = CHUNKS / NT;  // 16-byte chunks of a step, and a thread's
     static_assert(CHUNKS % NT == 0, "every thread loads the same number of chunks");
-    static constexpr int SLOT = XR * 16 + 16, PIECE = PARTS * 16 * SLOT;
+    static constexpr int SLOT = XR * 16, STEP = 4 * SLOT + 16, PIECE = PARTS * 4 * STEP;
     static constexpr int LDS = 2 * U * PIECE + kSharedWaves * FN * 256;
 
     const uint8_t *w[FN];    // this wave's panels, at piece 0
@@ -244,10 +257,10 @@ struct SharedRows {
         int put[PER];
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int c = tid % 16, q = (j * NT + tid) / 16;  // chunk 4 quarter + instruction of row q % XR
-            put[j] = (q / XR) * (16 * SLOT) + ((c & 3) * 4 + (c >> 2)) * SLOT + q % XR * 16;
+            const int d = tid & 3, quarter = tid >> 2 & 3, q = (j * NT + tid) / 16;  // chunk 4 quarter + instruction of row q % XR
+            put[j] = (q / XR * 4 + d) * STEP + quarter * SLOT + ((q % XR) ^ row_turn(quarter)) * 16;
         }
-        const int get = g * SLOT + li * 16;
+        const int get = g * SLOT + (li ^ row_turn(g)) * 16;
         uint8_t *buf = lds;
         for (int p = p0; p < p1; p += U) {
             v4i wc[UW][FN];
@@ -274,7 +287,7 @@ struct SharedRows {
                     for (int h = 0; h < PARTS; ++h)
 #pragma unroll
                         for (int c = 0; c < FM; ++c)
-                            xf[h][c] = load16(rows + (h * 16 + d * 4) * SLOT + get + c * 256);
+                            xf[h][c] = load16(rows + (h * 4 + d) * STEP + get + c * 256);
 #pragma unroll
                     for (int f = 0; f < FN; ++f) {
                         const v4i wf = codes((uint32_t)wc[u][f][d]);
