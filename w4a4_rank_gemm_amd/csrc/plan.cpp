@@ -233,15 +233,15 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
 RoutePlan plan_route(int64_t b, int64_t m, int64_t experts) {
     RoutePlan p{};
     p.slices = 1;
-    // Tokens, experts, m: 128, 128, 4096 17.0 us tiled, 19.2 else; 256, 64, 4096 14.3 and 19.2; 96, 256, 4096
-    // 21.4 and 25.6; 256, 256, 7168 32 and 78; 64, 256, 4096 (the smallest) 22.2 and 21.1; below: 64, 128,
-    // 2048 14.0 and 12.1, 32, 512, 4096 26.2 and 22.5.
-    p.tiled = b >= 64 && b * experts >= 16384;
+    // Tokens, experts, m: 128, 128, 4096 13.7 us tiled, 19.2 else; 64, 256, 4096 14.7 and 20.3; 32, 512, 4096
+    // 16.3 and 21.2; 256, 256, 7168 29 and 75; below: 64, 128, 2048 12.6 and 12.1, 32, 256, 7168 18.6 and 17.2.
+    p.tiled = b * experts >= 16384;
     if (p.tiled) {
         const int64_t tiles = (experts + 31) / 32 * ((b + 31) / 32);
-        // one tile a compute unit, and few enough numbers for the choice to add: 256, 4096, 64 with 2, 4, 8 (rule:
-        // 8) 25.4, 17.6, 14.3; 72, 4096, 512 (4) 30.7, 27.6, 38.9; 256, 2048, 64 (4) 16.8, 12.9, 14.4
-        while (p.slices < 8 && tiles * p.slices < 256 && m / 512 >= p.slices * 2 && p.slices * experts <= 1024) p.slices *= 2;
+        // at most one tile a compute unit: 256, 64, 4096 with 2, 4, 8 (rule: 8) 25.4, 17.2, 13.2; 256, 256, 7168 (4)
+        // 39.6, 28.6, 31.4; 72, 512, 4096 (4) 28.4, 20.5, 23.4; and 512 elements a slice: 256, 64, 2048 (4) 16.9,
+        // 12.5, 13.2
+        while (p.slices < 8 && tiles * p.slices * 2 <= 256 && m / 512 >= p.slices * 2) p.slices *= 2;
     }
     p.total = ((size_t)(p.slices * b * experts) * 8 + 255) & ~size_t(255);
     return p;
