@@ -495,8 +495,9 @@ twq_status twq_linear_dx(const void *dy, const void *qw, const float *sw, const 
  *
  *   Y[i][j] = sum_G s_W[G][j] sum_{k in G} X[i][k] Q_W[j][k] + sum_t T[i][t] L2[t][j],  T = X L1
  *
- * X and the codes enter the products as they are; sums are binary32, T is taken to 16 significant
- * bits, Y is rounded once. A non-finite element of X makes its row of Y non-finite and no other.
+ * X and the codes enter the products as they are (above 64 rows bf16 elements below 2^-28 of their row's
+ * largest are off by 2^-39 of it); sums are binary32, T is taken to at least 16 significant bits, Y is
+ * rounded once. A non-finite element of X makes its row of Y non-finite and no other.
  *   x     [b][m], y [b][n] (out), both of `type`
  *   qw, sw from twq_pack_weight_grouped;  l1t fp16 [r][m], l2t fp16 [n][r] (NULL iff r == 0)
  *   workspace: at least twq_linear_a16_workspace_bytes(b, m, n, r, g) bytes (may be 0 where
@@ -523,7 +524,8 @@ twq_status twq_linear_a16(const void *x, const void *qw, const float *sw, const 
  * Sums are binary32, the inner rows are taken to 16 significant bits, Y is rounded once. Every sum has a fixed
  * order: equal calls give equal bits. A non-finite element of x_i makes y_i non-finite and no other row.
  * m, f: multiples of 128 up to 131072. experts: 1..512, k: 1..16, experts 2 f and experts m at
- * most 2^24. b == 0 is a valid empty call; more than 256 tokens are TWQ_ERR_SHAPE.
+ * most 2^24. b == 0 is a valid empty call; more than 256 tokens are TWQ_ERR_SHAPE. Pointers are 16-byte
+ * aligned, those of ids, weights and bias 4-byte.
  */
 #define TWQ_SOFTMAX 0
 #define TWQ_SIGMOID 1

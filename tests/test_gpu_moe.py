@@ -137,6 +137,31 @@ def test_weights_of_no_expert_are_not_used(b):
     assert torch.equal(twq.moe_experts(x, ids, w, gate_up, down), twq.moe_experts(x, ids, w2, gate_up, down))
 
 
+@pytest.mark.parametrize("k", [1, 3, 8])
+def test_rows_of_a_larger_batch(k):
+    """Slices of a batch's ids and weights start at no multiple of 16 bytes."""
+    gate_up, down = _experts(256, 128, 9, 1)
+    g = _gen(k)
+    b = 21
+    ids, w = _choice(b, 9, k, "spread", g)
+    x = torch.randn(b, 256, generator=g, device="cuda").half()
+    for lo, hi in ((3, 20), (5, 6)):
+        args = [t[lo:hi] for t in (x, ids, w)]
+        out = twq.moe_experts(*args, gate_up, down)
+        check(out, ref.experts(*args, gate_up, down), "y")
+        assert torch.equal(out, twq.moe_experts(*[t.clone() for t in args], gate_up, down))
+
+
+def test_packing_refusals():
+    for shape in ((2, 24, 128), (2, 32, 100)):
+        with pytest.raises(ValueError):
+            twq.pack_experts(torch.zeros(shape, device="cuda"))
+    with pytest.raises(ValueError):
+        twq.pack_experts(torch.zeros(2, 128, 32, device="cuda").transpose(1, 2))
+    with pytest.raises(TypeError):
+        twq.pack_experts(torch.zeros(2, 32, 128, device="cuda").half())
+
+
 def _experts(m, f, e, seed):
     g = _gen(seed)
 

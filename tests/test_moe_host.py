@@ -15,6 +15,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 OK, NULL, SHAPE, ALIGN, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3, 4, 6
 A = ctypes.c_void_p(4096)
 MIS = ctypes.c_void_p(4096 + 8)
+MIS4 = ctypes.c_void_p(4096 + 2)  # ids, weights and bias need 4 bytes
 BIG = 1 << 46
 
 
@@ -70,7 +71,7 @@ def test_refused_pointers():
         for name in names:
             assert call(**{name: None}) == NULL, (call, name)
         for name in names + optional + ("ws",):
-            assert call(**{name: MIS}) == ALIGN, (call, name)
+            assert call(**{name: MIS4 if name in ("ids", "w", "bias") else MIS}) == ALIGN, (call, name)
 
 
 def test_workspaces():

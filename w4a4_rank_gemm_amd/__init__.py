@@ -857,7 +857,7 @@ def linear_a16(x: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor, l1t=None, l2
                out: torch.Tensor | None = None, g: int = GROUP) -> torch.Tensor:
     """The group-wise layer with unquantized activations (W4A16): Y [b][n] = X (s_W Q_W)^T +
     (X L1) L2, with the packed weight of pack_weight_grouped and the fp16 pair of linear; X and Y
-    fp16 or bf16."""
+    fp16 or bf16. As elsewhere here no autograd graph is recorded."""
     ty = _type(x, "x")
     _need(qw, "qw", torch.uint8, 2)
     dt, gpu = x.dtype, x.get_device()
@@ -889,8 +889,8 @@ def pack_experts(w: torch.Tensor):
     expert's matrix as pack_weight_grouped packs it, the scales of all experts side by side."""
     _need(w, "w", torch.float32, 3)
     e, n, m = w.shape
-    if n % 16:
-        raise ValueError(f"n must be a multiple of 16 (got {n})")
+    if n % 16 or m % GROUP:
+        raise ValueError(f"n must be a multiple of 16 and m of {GROUP} (got {n}, {m})")
     with torch.cuda.device(w.device):
         qw, sw = pack_weight_grouped(w.view(e * n, m))
     return qw.view(e, n, m // 2), sw

@@ -190,7 +190,7 @@ __device__ __forceinline__ void a16_store(const A16Args &a, const v4f (&acc)[FN]
 
 // Up to 16 rows: groups of kw waves (a power of two) own FN panels of 16 channels each and split their
 // K; the waves' sums are added in wave order. Bound by the weights' read: 1 x 8192 -> 28672, 128 ranks
-// (132 MB) 35-36 us, 3.7 TB/s; 16 x 4096 -> 4096, 32 ranks (11 MB) 8.0 us, start and drain.
+// (132 MB) 35-38 us, 3.6 TB/s; 16 x 4096 -> 4096, 32 ranks (11 MB) 8.0 us, start and drain.
 template <class T, int FN, int XR, int U>
 __global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a, int kw) {
     typedef FewRows<T, FN, XR, 1, U> Rows;
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a, in
 
 // Up to 64 rows: the CTA's eight waves, in groups of KG, own FN panels each and share the rows and a slice
 // of K. 32 x 8192 -> 28672 37.3 us (3.3 TB/s of weights), 64 rows 54: expansion and matrix
-// instructions beside the read. 61 x 14336 -> 4096 16.5 us and 4.7 to join eight slices: bound by the
+// instructions beside the read. 61 x 14336 -> 4096 16.4 us and 4.6 to join eight slices: bound by the
 // steps' latency (LDS is in use for 30% of the cycles; reading row operands for two panels at once, or
 // two steps ahead, gained nothing).
 template <class T, int FN, int XR, int U, int KG>
@@ -476,7 +476,7 @@ __device__ __forceinline__ void a16_read(uint32_t a0, uint32_t a1, v4i (&r)[2][T
 // channel l % 32, and of each half group the 32 codes of K quarter l / 32. Tokens are the
 // rows of the result and channels its columns, so that a group's scale is one register a lane.
 // A wave's group is 64 matrix instructions (2048 cycles) and beside them 128 multiplications by scale
-// ratios and 144 operations of expansion (1090 cycles). 4001 x 8192 -> 28672 1.68-1.85 ms, 1.1 PFLOP/s:
+// ratios and 144 operations of expansion (1090 cycles). 4001 x 8192 -> 28672 1.67-1.85 ms, 1.1 PFLOP/s:
 // matrix cores busy 60% of the cycles at about 1.9 GHz, no LDS conflicts. 2048 x 4096 -> 14336 265-291 us:
 // 896 tiles on 512 places, 51%. Interleaving the multiplications with the matrix instructions by
 // hand was 3-10% slower than leaving it to two waves a SIMD.

@@ -69,7 +69,7 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_logits_kernel(RouteA
 // wave, so that an element is converted for two of them), K split over slices and the CTA's 16
 // waves, whose sums are added in wave order. Element e of a lane's eight goes to instruction e, for both
 // operands. Result: lane (li, g) holds token li, experts 4 v + g of a 16 x 16 block. 256 tokens, 256
-// experts of 7168: 24.6 us, of which the binary64 matrix instructions alone take 12.6; they are busy
+// experts of 7168: 24.4 us, of which the binary64 matrix instructions alone take 12.6; they are busy
 // 57% of the cycles, and each element takes two conversions on the way.
 typedef double v4d __attribute__((ext_vector_type(4)));
 constexpr int kTileWaves = 16;
@@ -147,7 +147,7 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
 // unsigned order is the order of the values (0: none or taken, 1: NaN). Each round takes the largest
 // key, the lowest index among equals. Probabilities of all experts are formed only where they
 // are asked for: with a bias, or softmax weights that are not divided by their sum. Bound by the rounds'
-// dependent maxima over lanes: k = 8 of 64 experts 4-5 us, of 256 over four slices 6.5.
+// dependent maxima over lanes: k = 8 of 64 experts 4-5 us, of 256 over four slices 6.8.
 __device__ __forceinline__ uint64_t order_key(double v) {
     const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 to 0
     return v == v ? u ^ ((u >> 63) ? ~uint64_t(0) : uint64_t(1) << 63) : 1;
@@ -478,7 +478,7 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_few_kernel(MoeArgs a) {
 
 // Many rows an expert, or many experts: the CTA's eight waves share an expert's rows and K, and own
 // eight panels of inner (output) channels together. 128 tokens, 8 of 128 experts of 4096 and 1408: gate and
-// up 155-187 us for 798 MB (4.3-5.1 TB/s), down 105-130 for 444 MB (3.4-4.2): its CTAs have 11 steps only,
+// up 158-189 us for 798 MB (4.2-5.0 TB/s), down 104-130 for 444 MB (3.4-4.3): its CTAs have 11 steps only,
 // and finding the expert's rows and the first loads are a larger part of them. Two panels a wave, wave
 // pairs that split K and two pieces a step were all slower there (1-7%).
 template <class T>

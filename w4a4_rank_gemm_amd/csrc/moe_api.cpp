@@ -18,6 +18,9 @@ constexpr int64_t kMaxA16N = int64_t(1) << 22;
 // Outputs of one call: 256 GB, and fewer than 2^24 tiles, so that no grid dimension has 2^32 threads.
 constexpr int64_t kMaxOutput = int64_t(1) << 37;
 
+// ids, weights and bias are read and written one by one: rows of a larger batch's may be passed.
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
 bool valid_type(int t) { return t == TWQ_F16 || t == TWQ_BF16; }
 bool valid_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
     return valid_b(b) && valid_m(m) && n >= 0 && n % 16 == 0 && n <= kMaxA16N && b * n <= kMaxOutput && valid_r(r);
@@ -166,7 +169,7 @@ twq_status twq_moe_route(const void *x, const void *wr, const float *bias, int64
     if (!valid_route(b, m, experts, k)) return TWQ_ERR_SHAPE;
     if (b == 0) return TWQ_OK;
     if (!x || !wr || !ids || !weights) return TWQ_ERR_NULL;
-    if (!aligned16(x) || !aligned16(wr) || !aligned16(bias) || !aligned16(ids) || !aligned16(weights)) return TWQ_ERR_ALIGN;
+    if (!aligned16(x) || !aligned16(wr) || !aligned4(bias) || !aligned4(ids) || !aligned4(weights)) return TWQ_ERR_ALIGN;
     const size_t need = plan_route(b, m, experts).total;
     if (!workspace || workspace_bytes < need) return TWQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return TWQ_ERR_ALIGN;
@@ -187,7 +190,7 @@ twq_status twq_moe_experts(const void *x, const int32_t *ids, const float *weigh
     if (!valid_experts(b, m, f, experts, k)) return TWQ_ERR_SHAPE;
     if (b == 0) return TWQ_OK;
     if (!x || !ids || !weights || !q1 || !s1 || !q2 || !s2 || !y) return TWQ_ERR_NULL;
-    if (!aligned16(x) || !aligned16(ids) || !aligned16(weights) || !aligned16(q1) || !aligned16(s1) || !aligned16(q2) ||
+    if (!aligned16(x) || !aligned4(ids) || !aligned4(weights) || !aligned16(q1) || !aligned16(s1) || !aligned16(q2) ||
         !aligned16(s2) || !aligned16(y))
         return TWQ_ERR_ALIGN;
     const MoePlan p = plan_moe(b, m, f, experts, k);
@@ -209,7 +212,7 @@ twq_status twq_moe(const void *x, const void *wr, const float *bias, const void 
     if (!valid_experts(b, m, f, experts, k) || !valid_route(b, m, experts, k)) return TWQ_ERR_SHAPE;
     if (b == 0) return TWQ_OK;
     if (!x || !wr || !q1 || !s1 || !q2 || !s2 || !y) return TWQ_ERR_NULL;
-    if (!aligned16(x) || !aligned16(wr) || !aligned16(bias) || !aligned16(q1) || !aligned16(s1) || !aligned16(q2) ||
+    if (!aligned16(x) || !aligned16(wr) || !aligned4(bias) || !aligned16(q1) || !aligned16(s1) || !aligned16(q2) ||
         !aligned16(s2) || !aligned16(y))
         return TWQ_ERR_ALIGN;
     const MoePlan p = plan_moe(b, m, f, experts, k);

@@ -186,7 +186,7 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
             p.fn = p.rows == 4 || panels < 512 ? 1 : 2;
             const int64_t units = (panels + p.fn - 1) / p.fn;
             p.kw = 1;
-            while (p.kw < 8 && units * p.kw < (p.rows == 4 ? 3072 : 1536) && pieces >= p.kw * 2) p.kw *= 2;
+            while (p.kw < 8 && units * p.kw < 256 * (p.rows == 4 ? 12 : 6) && pieces >= p.kw * 2) p.kw *= 2;
         } else {
             // 64 rows, 8192 -> 28672: two panels a wave 50.8 us, one 57.5. Wave pairs that split K make CTAs of
             // four panels, so that fewer K slices and no join fill the GPU: 32 rows, 4096 -> 6144, 8192, 14336
