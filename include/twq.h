@@ -495,8 +495,8 @@ twq_status twq_linear_dx(const void *dy, const void *qw, const float *sw, const 
  *
  *   Y[i][j] = sum_G s_W[G][j] sum_{k in G} X[i][k] Q_W[j][k] + sum_t T[i][t] L2[t][j],  T = X L1
  *
- * X and the codes enter the products as they are (above 64 rows bf16 elements below 2^-28 of their row's
- * largest are off by 2^-39 of it); sums are binary32, T is taken to at least 16 significant bits, Y is
+ * X and the codes enter the products as they are (with many rows bf16 elements below 2^-28 of their row's
+ * largest may be off by 2^-39 of it); sums are binary32, T is taken to at least 16 significant bits, Y is
  * rounded once. A non-finite element of X makes its row of Y non-finite and no other.
  *   x     [b][m], y [b][n] (out), both of `type`
  *   qw, sw from twq_pack_weight_grouped;  l1t fp16 [r][m], l2t fp16 [n][r] (NULL iff r == 0)

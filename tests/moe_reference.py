@@ -10,7 +10,11 @@ import torch
 from tests.adapter_reference import F64, U, rounded
 
 BF_PARTS, F16_PARTS = 2.0 ** -18, 2.0 ** -22
-FEW = 64  # tokens of the few-row kernels
+
+
+def few(b, n):
+    """The few-row kernels: up to 64 rows, or up to 512 blocks of 64 rows x 128 channels."""
+    return b <= 64 or -(-n // 128) * -(-b // 64) <= 512
 
 
 def codes_of(qw):
@@ -41,12 +45,13 @@ def _product(x, w, parts=1):
     return x @ w.T, (128 * parts + m // 128 + 40) * U * (x.abs() @ w.abs().T)
 
 
-def linear_a16(x, qw, sw, l1t, l2t, tokens=None):
-    """(Y, bound) of rows of a batch of `tokens` (all of it if not given)."""
+def linear_a16(x, qw, sw, l1t, l2t, tokens=None, channels=None):
+    """(Y, bound) of rows of a batch of `tokens` and `channels` (all of them if not given)."""
     dtype, (b, m) = x.dtype, x.shape
     b = tokens or b
     x64, w = x.to(F64), dense(qw, sw)
-    if b <= FEW:
+    is_few = few(b, channels or qw.shape[0])
+    if is_few:
         v, e = _product(x64, w)
     else:
         # sums over all of K, multiplied by a ratio (itself rounded) once a group
@@ -60,7 +65,7 @@ def linear_a16(x, qw, sw, l1t, l2t, tokens=None):
     if l1t is not None:
         l1, l2 = l1t.to(F64), l2t.to(F64)
         t, et = x64 @ l1.T, 2 * m * U * (x64.abs() @ l1.abs().T)
-        if b <= FEW:
+        if is_few:
             et = et + BF_PARTS * (t.abs() + et)
         else:
             et = et + F16_PARTS * (t.abs() + et) + 2.0 ** -38 * t.abs().amax(1, keepdim=True)

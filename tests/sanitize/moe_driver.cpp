@@ -60,7 +60,7 @@ hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t) {
 }
 
 hipError_t launch_a16_t(const A16Args &a, hipStream_t) {
-    if (a.tks < 1 || a.b > kFewTokens) return hipErrorInvalidValue;
+    if (a.tks < 1 || a.b * a.r > 65536) return hipErrorInvalidValue;
     rd(a.x, a.b * a.m * 2);
     rd(a.l1t, a.r * a.m * 2);
     wr(a.t, (size_t)a.tks * a.b * a.r * 4);
@@ -68,7 +68,7 @@ hipError_t launch_a16_t(const A16Args &a, hipStream_t) {
 }
 
 hipError_t launch_a16(const A16Args &a, const A16Plan &p, hipStream_t) {
-    if (a.ks < 1 || p.many != (a.b > kFewTokens)) return hipErrorInvalidValue;
+    if (a.ks < 1 || (p.many && (a.b <= kFewTokens || a.ks > 1))) return hipErrorInvalidValue;
     rd(a.x, a.b * a.m * 2);
     rd(a.qw, a.n * a.m / 2);
     rd(a.sw, a.m / 128 * a.n * 4);
@@ -81,7 +81,7 @@ hipError_t launch_a16(const A16Args &a, const A16Plan &p, hipStream_t) {
         wr(a.xe, a.b * 4);
         wr(a.mul, a.m / 128 * a.n * 4);
         wr(a.mask, a.m / 128 * a.n * 4);
-        wr(a.unit, a.ks * a.n * 4);
+        wr(a.unit, a.n * 4);
         if (a.r > 0) {
             wr(a.t16, a.b * a.r * 4);
             wr(a.te, a.b * 4);
@@ -173,7 +173,7 @@ void routed(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k, int typ
 int main() {
     const int64_t layers[][4] = {{0, 256, 32, 16},    {1, 128, 16, 0},    {1, 512, 512, 16},   {4, 8192, 2048, 128}, {5, 256, 8208, 48},
                                  {16, 4096, 256, 32}, {17, 384, 48, 0},   {32, 4096, 4096, 16}, {33, 256, 80, 256},   {64, 14336, 512, 0},
-                                 {65, 256, 16, 16},   {129, 1024, 272, 0}, {600, 128, 1040, 32}, {2050, 256, 4112, 16}, {4100, 512, 288, 0}};
+                                 {65, 256, 16, 16},   {129, 1024, 272, 0}, {600, 128, 1040, 32}, {2050, 256, 4112, 16}, {4100, 512, 288, 0}, {600, 256, 16384, 16}, {500, 128, 16400, 256}};
     for (const auto &c : layers)
         for (int type : {TWQ_F16, TWQ_BF16}) layer(c[0], c[1], c[2], c[3], type);
     const int64_t moes[][5] = {{0, 256, 128, 4, 2}, {1, 128, 128, 1, 1}, {1, 512, 384, 64, 8}, {3, 256, 256, 5, 5}, {17, 384, 128, 60, 4},

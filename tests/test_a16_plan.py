@@ -7,6 +7,7 @@ import subprocess
 import pytest
 
 from tests import test_gpu_a16, test_gpu_moe
+from tests.moe_reference import few
 from tests.plan_rules import ROOT, ask
 
 pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="g++ is not installed")
@@ -29,7 +30,7 @@ def _a16(rules, cases):
     launch before, T of the CTA's own) of each."""
     got = ask(rules, [("a16", *c) for c in cases])
     for (b, m, n, r), (many, rows, fn, kw, tks, ks) in zip(cases, got):
-        assert many == (b > 64) and (b <= rows or many) and 1 <= ks <= m // 128 and tks <= 64 and (tks == 0 or r > 0)
+        assert many == (not few(b, n)) and (b <= rows or rows >= 64) and 1 <= ks <= m // 128 and tks <= 64 and (tks == 0 or r > 0)
         assert many or m // 128 >= kw or rows > 16
     return {(rows, fn, kw, ks > 1, 0 if r == 0 else 1 if tks else 2) for (_, _, _, r), (many, rows, fn, kw, tks, ks) in zip(cases, got)}
 

@@ -34,18 +34,25 @@ SHAPES = [
     (17, 256, 48, (0, 256)),
     (32, 4096, 4096, (0, 32)),
     (25, 896, 28704, (0, 48)),
-    (29, 1152, 6160, (0, 48)),
+    (29, 2176, 6160, (0, 48)),
     (21, 128, 6160, (0, 16)),
     (50, 512, 24592, (0, 16)),
-    (37, 1152, 24592, (0, 16)),
+    (37, 2176, 24592, (0, 16)),
     (40, 128, 16400, (0, 16)),
-    (45, 1152, 528, (0, 32)),
+    (45, 2176, 528, (0, 32)),
     (33, 384, 112, (0, 16)),
     (61, 8192, 1040, (0, 64)),
     (64, 2048, 14352, (0, 128)),
     (65, 128, 16, (0, 16)),
     (70, 4224, 272, (0, 48)),
     (200, 1024, 1040, (0, 256)),
+    (130, 384, 4112, (0, 48)),
+    (450, 256, 4096, (0, 64)),
+    (700, 1152, 4112, (0, 16)),
+    (600, 256, 272, (128,)),
+    (1000, 8320, 400, (0, 16)),
+    (5000, 128, 16, (0, 16)),
+    (33000, 256, 32, (0, 16)),
     (300, 256, 16400, (0, 32)),
     (100, 1152, 65536, (0, 16)),
     (2100, 1152, 4112, (0, 16, 128)),
@@ -123,7 +130,7 @@ def test_packed_weights_of_the_library():
     assert bool((step <= sw.double().T.repeat_interleave(128, dim=1) * 0.5 * (1 + 1e-6)).all())
 
 
-@pytest.mark.parametrize("b", [1, 7, 40, 90, 300])
+@pytest.mark.parametrize("b", [1, 7, 40, 90, 300, 11000])
 @pytest.mark.parametrize("dt", TYPES)
 def test_non_finite_rows_stay_alone(b, dt):
     g = _gen(b)
@@ -140,7 +147,7 @@ def test_non_finite_rows_stay_alone(b, dt):
     assert torch.equal(out[keep], want[keep]) and not bool(out[~keep].isfinite().any())
 
 
-@pytest.mark.parametrize("b", [1, 16, 64, 65, 200])
+@pytest.mark.parametrize("b", [1, 16, 64, 65, 200, 11000])
 @pytest.mark.parametrize("dt", TYPES)
 def test_scales_of_any_size(b, dt):
     """Groups of scale zero (whatever their codes), channels of zeros, scales 2^80 apart within a
@@ -165,7 +172,7 @@ def test_scales_of_any_size(b, dt):
     check(twq.linear_a16(x, qw, sw), ref.linear_a16(x, qw, sw, None, None), "y")
 
 
-@pytest.mark.parametrize("b", [3, 16, 64, 130])
+@pytest.mark.parametrize("b", [3, 16, 64, 130, 16500])
 def test_bf16_ranges(b):
     """bf16 rows from 2^-90 to 2^100, rows of zeros, and elements 2^-20 of their row's largest, whose
     codes are the only ones."""
@@ -192,7 +199,7 @@ def test_bf16_ranges(b):
 def test_fp16_subnormals():
     """fp16 rows below the normal range count."""
     g = _gen(8)
-    for b in (2, 20, 100):
+    for b in (2, 20, 100, 33000):
         qw, sw, _, _ = _layer(256, 48, 0, g)
         x = (torch.randn(b, 256, generator=g, device="cuda") * 2.0 ** -20).half()
         sw = sw * 2.0 ** 14
@@ -215,7 +222,7 @@ def test_largest_sizes():
         y = twq.linear_a16(x, qw, sw)
         for c in (slice(0, 64), slice(n - 64, n)):
             part = qw.view(n // 16, -1)[c.start // 16:c.stop // 16].reshape(64, -1)
-            check(y[-3:, c], ref.linear_a16(x[-3:], part, sw[:, c], None, None, tokens=b), f"n=2^22 {c}")
+            check(y[-3:, c], ref.linear_a16(x[-3:], part, sw[:, c], None, None, tokens=b, channels=n), f"n=2^22 {c}")
         del y
     b = 1 << 20
     _say("linear_a16 b=2^20")
@@ -223,7 +230,7 @@ def test_largest_sizes():
     x = torch.randn(b, 256, generator=g, device="cuda").half()
     y = twq.linear_a16(x, qw, sw, l1t, l2t)
     for rows in (slice(0, 130), slice(b - 130, b)):
-        check(y[rows], ref.linear_a16(x[rows], qw, sw, l1t, l2t), f"rows {rows}")
+        check(y[rows], ref.linear_a16(x[rows], qw, sw, l1t, l2t, tokens=b), f"rows {rows}")
 
 
 def test_refusals():

@@ -78,11 +78,11 @@ def test_workspaces():
     L = twq.lib()
     assert L.twq_linear_a16_workspace_bytes(1, 4096, 4096, 0, 128) == 0  # one launch
     assert L.twq_linear_a16_workspace_bytes(9, 512, 4096, 16, 128) == 0
-    for b, m, n, r in ((1, 4096, 4096, 16), (16, 4096, 64, 32), (61, 14336, 4096, 0), (65, 256, 32, 0), (3000, 4096, 512, 64)):
+    for b, m, n, r in ((1, 4096, 4096, 16), (16, 4096, 64, 32), (61, 14336, 4096, 0), (500, 256, 16384, 0), (3000, 4096, 512, 64)):
         need = L.twq_linear_a16_workspace_bytes(b, m, n, r, 128)
         assert need > 0 and _a16(b, m, n, r, wsb=need - 1) == WORKSPACE and _a16(b, m, n, r, ws=None) == WORKSPACE
-    assert L.twq_linear_a16_workspace_bytes(65, 256, 32, 0, 128) >= 65 * 256 * 2
-    assert L.twq_linear_a16_workspace_bytes(65, 256, 32, 0, 64) == 0 and L.twq_linear_a16_workspace_bytes(4, 100, 32, 0, 128) == 0
+    assert L.twq_linear_a16_workspace_bytes(500, 256, 16384, 0, 128) >= 500 * 256 * 2
+    assert L.twq_linear_a16_workspace_bytes(500, 256, 16384, 0, 64) == 0 and L.twq_linear_a16_workspace_bytes(4, 100, 32, 0, 128) == 0
     need = L.twq_moe_route_workspace_bytes(9, 4096, 77, 3)
     assert need >= 9 * 77 * 8 and _route(9, 4096, 77, 3, wsb=need - 1) == WORKSPACE and _route(9, 4096, 77, 3, ws=None) == WORKSPACE
     part = L.twq_moe_experts_workspace_bytes(9, 256, 384, 77, 3)

@@ -3,9 +3,9 @@
 //   y[i][j] = sum_G s_W[G][j] sum_{k in G} x[i][k] q[j][k] + sum_t (sum_k x[i][k] L1[k][t]) L2[t][j]
 //
 // G: groups of 128 input channels. X is fp16 or bf16 and used as it is; codes are exact in both
-// types, so the only roundings are those of the binary32 sums, of T = X L1 to 16 (above 64 rows 22) bits and
-// the output's. T comes in partial sums over K slices from a launch of its own (up to 64 rows
-// a16_t_kernel, above the adapters' shrink kernel), or from the product's own CTAs where L1 is small.
+// types, so the only roundings are those of the binary32 sums, of T = X L1 to 16 (tile kernel: 22) bits and
+// the output's. T comes in partial sums over K slices from a launch of its own (with few sums
+// a16_t_kernel, otherwise the adapters' shrink kernel), or from the product's own CTAs where L1 is small.
 #include "twq_few_device.h"
 #include "twq_moe.h"
 
@@ -47,7 +47,7 @@ __device__ __forceinline__ v4f t_part(const A16Args &a, int64_t rank0, int64_t r
     return acc;
 }
 
-// T of up to 64 rows in a launch of its own: a CTA owns 16 rows x 16 ranks over a slice of K, which
+// T in a launch of its own, with few sums: a CTA owns 16 rows x 16 ranks over a slice of K, which
 // its 16 waves split; their sums are added in wave order. Bound by its start and one round of loads:
 // 4.8 us for one token of 8192 with 128 ranks and for 16 of 4096 with 32.
 template <class T>
@@ -127,16 +127,16 @@ __device__ __forceinline__ void few_lowrank(const A16Args &a, F &&rank8, const i
     }
 }
 
-// T's parts of all rows to LDS, [r / 8][R rows][hi, lo], by the whole CTA: each of its waves would
+// T's parts of the R rows from row0 on to LDS, [r / 8][R rows][hi, lo], by the whole CTA: each of its waves would
 // otherwise read T's slices again (64 tokens, 4096 -> 14336, 64 ranks: 44 us, this way 31).
 template <int R>
-__device__ __forceinline__ void stage_t(const A16Args &a, uint8_t *lds) {
+__device__ __forceinline__ void stage_t(const A16Args &a, int64_t row0, uint8_t *lds) {
     __syncthreads();
-    const int eights = a.r / 8;
-    for (int i = threadIdx.x; i < (int)a.b * eights; i += kFewWaves * kWave) {
+    const int eights = a.r / 8, rows = (int)(a.b - row0 < R ? a.b - row0 : R);
+    for (int i = threadIdx.x; i < rows * eights; i += kFewWaves * kWave) {
         const int row = i / eights, k8 = i % eights;
         v4i hi, lo;
-        few_t({a.t, a.b * a.r, a.tks}, a.r, row, k8 * 8, hi, lo);
+        few_t({a.t, a.b * a.r, a.tks}, a.r, row0 + row, k8 * 8, hi, lo);
         *reinterpret_cast<v4i *>(lds + (k8 * R + row) * 32) = hi;
         *reinterpret_cast<v4i *>(lds + (k8 * R + row) * 32 + 16) = lo;
     }
@@ -166,13 +166,13 @@ __device__ __forceinline__ TSums own_t(const A16Args &a, float *t, int wave) {
 
 // Stores the row blocks c = share, share + shares, .. of FN panels: Y, or this slice's sums.
 template <class T, int FN, int FM>
-__device__ __forceinline__ void a16_store(const A16Args &a, const v4f (&acc)[FN][FM], int64_t panel0, int64_t slice, int shares,
-                                          int share) {
+__device__ __forceinline__ void a16_store(const A16Args &a, const v4f (&acc)[FN][FM], int64_t row0, int64_t panel0, int64_t slice,
+                                          int shares, int share) {
     const int64_t panels = a.n / 16;
     const int lane = threadIdx.x % kWave, li = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int c = 0; c < FM; ++c) {
-        const int64_t row = c * 16 + li;
+        const int64_t row = row0 + c * 16 + li;
         if (c % shares != share || row >= a.b) continue;
 #pragma unroll
         for (int f = 0; f < FN; ++f) {
@@ -231,16 +231,16 @@ __global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a, in
         __syncthreads();
         if (panel0 < panels) few_lowrank<FN, 1>(a, rank8, chan, share, kw, acc);
     } else if (XR > 4 && a.r > 0) {
-        stage_t<16>(a, smem);
+        stage_t<16>(a, 0, smem);
         auto staged = [&](int row, int k, v4i &hi, v4i &lo) { staged_t<16>(smem, a.r, row, k, hi, lo); };
         if (panel0 < panels) few_lowrank<FN, 1>(a, staged, chan, share, kw, acc);
     }
     join_waves(smem, kw, wave, acc);
-    a16_store<T, FN, 1>(a, acc, panel0, 0, kw, share);
+    a16_store<T, FN, 1>(a, acc, 0, panel0, 0, kw, share);
 }
 
-// Up to 64 rows: the CTA's eight waves, in groups of KG, own FN panels each and share the rows and a slice
-// of K. 32 x 8192 -> 28672 37.3 us (3.3 TB/s of weights), 64 rows 54: expansion and matrix
+// From 17 rows on, in blocks of XR: the CTA's eight waves, in groups of KG, own FN panels each and share the
+// rows and a slice of K. 32 x 8192 -> 28672 37.3 us (3.3 TB/s of weights), 64 rows 50, 128 rows 77, 1024 x 4096 -> 4096 42 (0.8 PFLOP/s): expansion and matrix
 // instructions beside the read. 61 x 14336 -> 4096 16.4 us and 4.6 to join eight slices: bound by the
 // steps' latency (LDS is in use for 30% of the cycles; reading row operands for two panels at once, or
 // two steps ahead, gained nothing).
@@ -254,7 +254,11 @@ __global__ __launch_bounds__(kSharedWaves *kWave) void a16_shared_kernel(A16Args
     __shared__ __align__(16) uint8_t smem[Rows::LDS];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t panels = a.n / 16, pieces = a.m / 128, slice = blockIdx.y;
-    const int64_t panel0 = ((int64_t)blockIdx.x * (kSharedWaves / KG) + wave / KG) * FN;
+    // Row blocks of the same panels are neighbours on an XCD and share their weights' read in its L2 (128 x 8192 ->
+    // 28672 95 us one block after the other, 77 so).
+    const uint32_t id = (uint32_t)xcd_range(blockIdx.x, gridDim.x), blocks = (uint32_t)((a.b + XR - 1) / XR);
+    const int64_t row0 = (int64_t)(id % blocks) * XR;
+    const int64_t panel0 = ((int64_t)(id / blocks) * (kSharedWaves / KG) + wave / KG) * FN;
     Rows rows;
     int64_t chan[FN];
 #pragma unroll
@@ -265,21 +269,21 @@ __global__ __launch_bounds__(kSharedWaves *kWave) void a16_shared_kernel(A16Args
         rows.s[f] = a.sw + p * 16;
     }
     rows.s_stride = a.n;
-    rows.x = a.x;
+    rows.x = a.x + row0 * a.m;
 #pragma unroll
     for (int j = 0; j < Rows::PER; ++j) {
-        const int row = Rows::row_of(j);
-        rows.row[j] = (uint32_t)((row < a.b ? row : a.b - 1) * a.m * 2);
+        const int64_t row = Rows::row_of(j);
+        rows.row[j] = (uint32_t)((row < a.b - row0 ? row : a.b - row0 - 1) * a.m * 2);
     }
     v4f acc[FN][FM] = {};
     rows.run((int)(slice * pieces / a.ks), (int)((slice + 1) * pieces / a.ks), smem, acc);
     if (a.r > 0 && slice == 0) {
-        stage_t<XR>(a, smem);
+        stage_t<XR>(a, row0, smem);
         auto staged = [&](int row, int k, v4i &hi, v4i &lo) { staged_t<XR>(smem, a.r, row, k, hi, lo); };
         few_lowrank<FN, FM>(a, staged, chan, wave % KG, KG, acc);
     }
     join_waves(smem, KG, wave, acc);
-    a16_store<T, FN, FM>(a, acc, panel0, slice, KG, wave % KG);
+    a16_store<T, FN, FM>(a, acc, row0, panel0, slice, KG, wave % KG);
 }
 
 // Y = the slices' sums in slice order, rounded once.
@@ -309,7 +313,7 @@ static hipError_t a16_few(const A16Args &a, const A16Plan &p, hipStream_t stream
 template <class T, int FN, int XR, int U, int KG>
 static hipError_t a16_shared(const A16Args &a, hipStream_t stream) {
     const int64_t groups = (a.n / 16 + FN - 1) / FN, per = kSharedWaves / KG;
-    const dim3 grid((unsigned)((groups + per - 1) / per), (unsigned)a.ks);
+    const dim3 grid((unsigned)((groups + per - 1) / per * ((a.b + XR - 1) / XR)), (unsigned)a.ks);
     a16_shared_kernel<T, FN, XR, U, KG><<<grid, kSharedWaves * kWave, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || a.ks == 1 ? e : a16_join<T>(a, stream);
@@ -386,8 +390,7 @@ __device__ __forceinline__ void prepare_scales(const A16Args &a, int64_t block, 
         const float s = a.sw[g * a.n + c], before = a.sw[(g > 0 ? g - 1 : 0) * a.n + c];
         a.mul[g * a.n + c] = unit(before) / unit(s);
         a.mask[g * a.n + c] = on(s) ? 0xFFFFFFFFu : 0u;
-        for (int q = 0; q < a.ks; ++q)
-            if (g + 1 == (q + 1) * groups / a.ks) a.unit[q * a.n + c] = unit(s);
+        if (g + 1 == groups) a.unit[c] = unit(s);
     }
 }
 
@@ -468,7 +471,7 @@ __device__ __forceinline__ void a16_read(uint32_t a0, uint32_t a1, v4i (&r)[2][T
             : "memory");
 }
 
-// A CTA owns 32 TB tokens x 256 channels over a slice of the groups; its four waves take 64
+// A CTA owns 32 TB tokens x 256 channels; its four waves take 64
 // channels each and share the tokens' operands. A group of X (8 TB KB) goes to LDS by direct
 // loads, one group ahead, in 256-byte lines with the 16-byte chunk index XORed by row % 8 and 8
 // ((row / 16) % 2) (one 16-byte read serves lanes 0-7 with 16-23 in a pass). Each wave reads its own
@@ -490,7 +493,7 @@ __global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t nti
     const int64_t id = xcd_range(blockIdx.x, ntiles * ttiles), band = id / (8 * ntiles), in = id % (8 * ntiles);
     const int64_t deep = ttiles - band * 8 < 8 ? ttiles - band * 8 : 8;
     const int64_t tok0 = (band * 8 + in % deep) * ROWS, n0 = in / deep * kA16N + wave * 64;
-    const int64_t groups = a.m / 128, slice = blockIdx.y, g0 = slice * groups / a.ks, g1 = (slice + 1) * groups / a.ks;
+    const int64_t groups = a.m / 128;
 
     const int panels = (int)(a.n / 16), panel0 = (int)(n0 / 16) < panels ? (int)(n0 / 16) : panels - 1;
     uint32_t chan[2], woff[2];
@@ -541,12 +544,12 @@ __global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t nti
 #pragma unroll
     for (int s = 0; s < 4; ++s) at[s] = lds_offset(ring) + col * 256 + ((half * 4 + s) ^ swz) * 16;
 
-    fetch(g0, 0);
-    for (int64_t c0 = g0; c0 < g1; c0 += 2) {
+    fetch(0, 0);
+    for (int64_t c0 = 0; c0 < groups; c0 += 2) {
         static_for(std::make_integer_sequence<int, 2>{}, [&](auto u) {
             constexpr int U = decltype(u)::value, OFF = U * XBYTES;
             const int64_t g = c0 + U;
-            if (g >= g1) return;
+            if (g >= groups) return;
             wait_vmcnt<0>();  // issued a group ago
             stage_barrier();  // group g has landed for every wave, and group g - 1 is read
             v4i w[2][2];
@@ -565,7 +568,7 @@ __global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t nti
 #pragma unroll
                         for (int e = 0; e < 4; ++e) w[q][h][e] &= (int)kn[q];
             }
-            if (g + 1 < g1) fetch(g + 1, 1 - U);
+            if (g + 1 < groups) fetch(g + 1, 1 - U);
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -603,11 +606,11 @@ __global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t nti
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const float u = a.unit[slice * a.n + chan[q]];
+            const float u = a.unit[chan[q]];
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[q][t][v] = acc[q][t][v] * u * f[v];
         }
-        if (a.r > 0 && slice == 0) {
+        if (a.r > 0) {
             v16f low[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q)
@@ -637,15 +640,9 @@ __global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t nti
 #pragma unroll
             for (int v = 0; v < 16; ++v) {
                 const int row = t * 32 + half * 4 + v / 4 * 8 + v % 4;
-                if (a.ks > 1) {
-                    if (tok0 + row < a.b && n0 + q * 32 + col < a.n)
-                        a.part[(slice * a.b + tok0 + row) * a.n + n0 + q * 32 + col] = acc[q][t][v];
-                } else {
-                    turn[row * 64 + q * 32 + col] = T::from_f32(acc[q][t][v]);
-                }
+                turn[row * 64 + q * 32 + col] = T::from_f32(acc[q][t][v]);
             }
     }
-    if (a.ks > 1) return;
     wave_fence();
 #pragma unroll
     for (int j = 0; j < ROWS / 8; ++j) {
@@ -664,13 +661,12 @@ static hipError_t a16_many(const A16Args &a, const A16Plan &p, hipStream_t strea
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t ntiles = (a.n + kA16N - 1) / kA16N, ttiles = (a.b + p.rows - 1) / p.rows;
-    const dim3 grid((unsigned)(ntiles * ttiles), (unsigned)p.ks);
+    const unsigned grid = (unsigned)(ntiles * ttiles);
     if (p.rows == 128)
         a16_tile_kernel<T, 4><<<grid, 256, 0, stream>>>(a, ntiles, ttiles);
     else
         a16_tile_kernel<T, 2><<<grid, 256, 0, stream>>>(a, ntiles, ttiles);
-    e = hipGetLastError();
-    return e != hipSuccess || p.ks == 1 ? e : a16_join<T>(a, stream);
+    return hipGetLastError();
 }
 
 hipError_t launch_a16(const A16Args &a, const A16Plan &p, hipStream_t stream) {

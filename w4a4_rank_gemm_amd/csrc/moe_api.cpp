@@ -138,8 +138,8 @@ twq_status twq_linear_a16(const void *x, const void *qw, const float *sw, const 
     a.n = n;
     a.r = (int)r;
     a.bf16 = type == TWQ_BF16;
-    if (p.tks > 0 && !p.many) e = launch_a16_t(a, st);
-    if (r > 0 && p.many) {
+    if (p.tks > 0 && !p.shrink) e = launch_a16_t(a, st);
+    if (p.tks > 0 && p.shrink) {
         ShrinkArgs s{};
         s.v = u16(x);
         s.w = u16(l1t);

@@ -166,16 +166,20 @@ static bool a16_own_t(int64_t b, int64_t m, int64_t r) { return b <= 16 && r <= 
 A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     A16Plan p{};
-    p.many = b > kFewTokens;
-    if (r > 0 && p.many) p.tks = shrink_slices(b, m, r, (b + tile_rows(b) - 1) / tile_rows(b), 4);
+    const int64_t panels = n / 16, pieces = m / 128, blocks = (b + 63) / 64, plain = (panels + 7) / 8 * blocks;
+    p.many = b > kFewTokens && plain > kFewTiles;
+    // X L1 by the adapters' kernel, which reads L1 once for 64 or 128 rows: 2048 x 2048 -> 2048, 128 ranks 47.0 us,
+    // a16_t_kernel 50.0; 4096 x 4096 -> 512, 64 ranks 48.9 and 69.3; with 65536 sums (2048 x 32, 4096 x 16) 34.8
+    // and 34.2, 14.5 and 13.0; before the tile kernel 2048 x 4096 -> 4096, 32 ranks 90.4 and 93.5.
+    p.shrink = p.many || b * r > 65536;
+    if (r > 0 && p.shrink) p.tks = shrink_slices(b, m, r, (b + tile_rows(b) - 1) / tile_rows(b), 4);
     // T of few rows in slices of 1024: one token, 8192 -> 28672, 128 ranks 38.1 us; slices of 512, 2048 and
     // 4096: 41.7, 38.8, 40.6 (16 tokens, 4096 -> 4096, 32 ranks: 12.1; 11.3, 13.6, 17.1)
-    if (r > 0 && !p.many && !a16_own_t(b, m, r)) p.tks = m >= 16384 ? 16 : (int)((m + 1023) / 1024);
+    if (r > 0 && !p.shrink && !a16_own_t(b, m, r)) p.tks = m >= 16384 ? 16 : (int)((m + 1023) / 1024);
     p.ks = 1;
     p.x16 = up((size_t)p.tks * b * r * 4);
     p.total = p.x16;
     if (!p.many) {
-        const int64_t panels = n / 16, pieces = m / 128;
         p.rows = b <= 4 ? 4 : b <= 16 ? 16 : b <= 32 ? 32 : 64;
         if (p.rows <= 16) {
             // 5 to 16 rows: two panels a wave from 512 on (8192 channels). 4096 -> 8192: 9.7 us, one panel 9.9;
@@ -188,18 +192,23 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
             p.kw = 1;
             while (p.kw < 8 && units * p.kw < 256 * (p.rows == 4 ? 12 : 6) && pieces >= p.kw * 2) p.kw *= 2;
         } else {
-            // 64 rows, 8192 -> 28672: two panels a wave 50.8 us, one 57.5. Wave pairs that split K make CTAs of
-            // four panels, so that fewer K slices and no join fill the GPU: 32 rows, 4096 -> 6144, 8192, 14336
-            // 11.3, 11.7, 13.4 us, without 11.5, 12.2, 15.8 (4096 -> 4096 9.1 and 9.0; 14336 -> 4096 16.1 and
-            // 15.2; 4096 -> 22016 22.0 and 19.3); 64 rows 4096 -> 1024, 8192, 14336 8.9, 16.4, 20.0 and 9.6,
-            // 17.2, 22.8 (8192 -> 14336 36.6 and 35.3; 14336 -> 4096 22.9 and 21.6; 4096 -> 22016 33 and 28.5).
-            p.fn = p.rows == 64 && panels >= 1536 ? 2 : 1;
-            p.kw = panels <= 1024 && (p.rows == 32 ? panels >= 384 : m <= 4096) ? 2 : 1;
-            const int64_t per = 8 / p.kw * p.fn, ctas = (panels + per - 1) / per;
+            // Two panels a wave where one would give a compute unit more than one CTA: 768 x 4096 -> 4096 (384 CTAs)
+            // 37.6 us, one panel 40.1; 192 x 4096 -> 14336 (336) 37.8 and 39.8; below: 512 x 4096 -> 4096 (256) 29.3
+            // and 25.4, 64 x 4096 -> 28672 (224) 34.5 and 27, 64 x 8192 -> 28672 50.8 and 50.2.
+            // Wave pairs that split K make CTAs of four panels, so that fewer K slices and no join fill the GPU.
+            // More than 32 rows: 256 x 4096 -> 4096 (128 CTAs without) 17.9 us, without 21.8; 64 x 4096 -> 14336 (112)
+            // 20.0 and 22.8; 512 x 4096 -> 4096 (256) 28.8 and 25.4, 128 x 4096 -> 14336 (224) 28.4 and 25.0;
+            // longer rows of X: 61 x 14336 -> 4096 22.5 and 20.9, 128 x 14336 -> 4096 32.5 and 27.9.
+            // 32 rows: 4096 -> 6144, 8192, 14336 11.3, 11.7, 13.4 and 11.5, 12.2, 15.8; 4096 -> 4096 9.1 and 9.0,
+            // 14336 -> 4096 16.1 and 15.2, 4096 -> 22016 22.0 and 19.3.
+            p.fn = p.rows == 64 && plain > 256 ? 2 : 1;
+            p.kw = p.rows == 32 ? panels >= 384 && panels <= 1024 ? 2 : 1 : p.fn == 1 && plain < 192 && m <= 8192 ? 2 : 1;
+            const int64_t per = 8 / p.kw * p.fn, ctas = (panels + per - 1) / per * blocks;
             // K slices: as many as leave one CTA a compute unit. 61 rows, 14336 -> 4096 with 4, 8, 16 (rule: 8)
             // 28.7, 21.4, 25.1 us; 32 rows, 4096 -> 4096 with 4, 8 (8) 10.2, 9.8.
             int64_t ks = 256 / ctas;
             if (ks > pieces / 4) ks = pieces / 4;
+            if (pieces < 16) ks = 1;  // 256 x 1024 -> 1024 with 1, 2: 7.4, 8.7
             p.ks = ks < 1 ? 1 : ks > 16 ? 16 : (int)ks;
         }
         p.part = p.x16;
@@ -208,25 +217,16 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
     }
     const int64_t groups = m / 128, ntiles = (n + kA16N - 1) / kA16N;
     p.rows = 128;
-    // Tiles of 64 rows while those of 128 give a compute unit at most 1.5 on average (two fit): 1024 x 4096 ->
-    // 4096 59 and 69 us, 2048 x 4096 -> 4096 83 and 100 (256 tiles of 128), 1536 x 4096 -> 8192 124 and 127
-    // (384); 1024 x 4096 -> 14336 141 and 137 (448), 2048 x 4096 -> 8192 152 and 140 (512).
+    // Tiles of 64 rows while those of 128 give a compute unit at most 1.5 on average (two fit): 2048 x
+    // 4096 -> 4096 83 and 100 us (256 tiles of 128), 1536 x 4096 -> 8192 124 and 127 (384); 1024 x 4096 -> 14336 141 and 137 (448), 2048 x 4096 -> 8192 152 and 140 (512).
     if ((b + 127) / 128 * ntiles <= 384) p.rows = 64;
-    const int64_t ctas = (b + p.rows - 1) / p.rows * ntiles;
-    // K slices as many as leave one tile a compute unit: 256 x 4096 -> 4096 with 2, 4, 8 (rule: 4) 39.7, 32.1,
-    // 34.7 us; 128 x 14336 -> 4096 with 4, 8 (8) 61.6, 52.5; 1024 x 4096 -> 4096 with 1, 2, 4 (1) 57, 59, 71.
-    int64_t ks = 256 / ctas;
-    if (ks > groups / 4) ks = groups / 4;
-    if (ks > 8) ks = 8;
-    p.ks = ks < 1 ? 1 : (int)ks;
     p.xe = p.x16 + up((size_t)b * m * 2);
     p.mul = p.xe + up((size_t)b * 4);
     p.mask = p.mul + up((size_t)groups * n * 4);
     p.unit = p.mask + up((size_t)groups * n * 4);
-    p.t16 = p.unit + up((size_t)p.ks * n * 4);
+    p.t16 = p.unit + up((size_t)n * 4);
     p.te = p.t16 + up((size_t)b * r * 4);
-    p.part = p.te + up((size_t)b * 4);
-    p.total = p.part + (p.ks > 1 ? up((size_t)p.ks * b * n * 4) : 0);
+    p.total = p.te + up((size_t)b * 4);
     return p;
 }
 

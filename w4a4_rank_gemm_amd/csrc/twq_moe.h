@@ -9,11 +9,14 @@ namespace twq {
 
 // ---- the layer with 16-bit activations ------------------------------------------------------
 
-// Up to kFewTokens rows the product is bound by the weights' read (a few-row kernel); above by the
+// With few rows the product is bound by the weights' read (a few-row kernel); above by the
 // matrix cores (a tile kernel, which wants X in fp16 in the order of the expanded codes, and
-// the scales as ratios of neighbouring groups). 64 rows, 4096 -> 14336: few-row kernel 22 us, tile kernel
-// 36; 14336 -> 4096 22 and 53; 65 rows, 4096 -> 14336: 39. The few-row kernels hold at most 64 rows.
-constexpr int64_t kFewTokens = 64;
+// the scales as ratios of neighbouring groups). More rows take the few-row kernel too, in blocks of 64, while
+// blocks of 64 rows x 128 channels are at most kFewTiles, two a compute unit. Few-row and tile
+// kernel: 256 x 4096 -> 14336 (448) 40.6 and 53.7 us, 1024 x 4096 -> 4096 (512) 42.3 and 56.6, 2048 x 2048 -> 2048
+// (512) 33 and 43, 128 x 8192 -> 28672 (448) 77 and 133; 384 x 4096 -> 14336 (672) 74 and 73, 160 x 8192 -> 28672
+// (672) 142 and 138, 100 x 1024 -> 131072 (2048) 66 and 58.
+constexpr int64_t kFewTokens = 64, kFewTiles = 512;
 constexpr int kOwnRanks = 128;  // of X L1 that a few-row CTA may form for itself
 constexpr int kA16N = 256;  // channels of a tile CTA: 64 a wave
 
@@ -34,15 +37,17 @@ struct A16Args {
     int32_t *xe;          // [b] (bf16)
     float *mul;           // [m / 128][n]: unit of the group before over this group's
     uint32_t *mask;       // [m / 128][n]: all ones, or 0 for a group without weight
-    float *unit;          // [ks][n]: unit of a slice's last group
+    float *unit;          // [n]: unit of the last group
     uint16_t *t16;        // [b][r / 8][2][8]: X L1 2^-te in two fp16 parts
     int32_t *te;          // [b]
+    // few rows
     int ks;               // slices of K
     float *part;          // [ks][b][n] when ks > 1
 };
 
 struct A16Plan {
     int many;      // the tile kernel
+    int shrink;    // X L1 by the adapters' kernel
     int rows;      // token rows a CTA
     int fn, kw;    // few rows: panels of a wave, and neighbouring waves that share their K
     int tks;       // K slices of X L1, 0: formed by the product's CTAs (or r = 0)
@@ -50,7 +55,7 @@ struct A16Plan {
     size_t t, x16, xe, mul, mask, unit, t16, te, part, total;
 };
 A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r);  // plan.cpp
-hipError_t launch_a16_t(const A16Args &a, hipStream_t stream);  // few rows: t
+hipError_t launch_a16_t(const A16Args &a, hipStream_t stream);  // t, with few sums
 hipError_t launch_a16(const A16Args &a, const A16Plan &p, hipStream_t stream);
 
 // ---- the routed layer ------------------------------------------------------------------------
