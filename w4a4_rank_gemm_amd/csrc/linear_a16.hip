@@ -239,11 +239,11 @@ __global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a, in
     a16_store<T, FN, 1>(a, acc, 0, panel0, 0, kw, share);
 }
 
-// From 17 rows on, in blocks of XR: the CTA's eight waves, in groups of KG, own FN panels each and share the
-// rows and a slice of K. 32 x 8192 -> 28672 37.3 us (3.3 TB/s of weights), 64 rows 50, 128 rows 77, 1024 x 4096 -> 4096 42 (0.8 PFLOP/s): expansion and matrix
-// instructions beside the read. 61 x 14336 -> 4096 16.4 us and 4.6 to join eight slices: bound by the
-// steps' latency (LDS is in use for 30% of the cycles; reading row operands for two panels at once, or
-// two steps ahead, gained nothing).
+// From 17 rows on, in blocks of XR: the CTA's eight waves, in groups of KG, own FN panels each and share
+// the rows and a slice of K. 32 x 8192 -> 28672 37 us (3.3 TB/s of weights), 64 rows 50, 128 rows 77,
+// 1024 x 4096 -> 4096 42 (0.8 PFLOP/s): expansion and matrix instructions beside the read.
+// 61 x 14336 -> 4096 16.4 us and 4.6 to join eight slices: bound by the steps' latency (LDS is in use for
+// 30% of the cycles; reading row operands for two panels at once, or two steps ahead, gained nothing).
 template <class T, int FN, int XR, int U, int KG>
 __global__ __launch_bounds__(kSharedWaves *kWave) void a16_shared_kernel(A16Args a) {
     typedef SharedRows<T, FN, XR, 1, U, KG> Rows;

@@ -217,8 +217,9 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
     }
     const int64_t groups = m / 128, ntiles = (n + kA16N - 1) / kA16N;
     p.rows = 128;
-    // Tiles of 64 rows while those of 128 give a compute unit at most 1.5 on average (two fit): 2048 x
-    // 4096 -> 4096 83 and 100 us (256 tiles of 128), 1536 x 4096 -> 8192 124 and 127 (384); 1024 x 4096 -> 14336 141 and 137 (448), 2048 x 4096 -> 8192 152 and 140 (512).
+    // Tiles of 64 rows while those of 128 give a compute unit at most 1.5 on average (two fit): 2048 x 4096 -> 4096
+    // 83 and 100 us (256 tiles of 128), 1536 x 4096 -> 8192 124 and 127 (384); 1024 x 4096 -> 14336 141 and 137
+    // (448), 2048 x 4096 -> 8192 152 and 140 (512).
     if ((b + 127) / 128 * ntiles <= 384) p.rows = 64;
     p.xe = p.x16 + up((size_t)b * m * 2);
     p.mul = p.xe + up((size_t)b * 4);
