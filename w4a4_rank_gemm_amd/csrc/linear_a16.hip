@@ -336,9 +336,9 @@ static hipError_t a16_rows(const A16Args &a, const A16Plan &p, hipStream_t strea
 // The tile kernel multiplies its sums by mul[G] = unit[G - 1] / unit[G] before group G, so that
 // they are in units of the group's scale when its products (codes times X) are added: one
 // multiplication a sum and group, no second set of sums. unit[G] is s_W[G]; where that is below
-// 2^-90 of the channel's largest (zero among it) the group's codes are masked (its share is
-// below 2^-84 of what any element of X adds through the largest scale) and the unit is the
-// largest. Sums then stay below 7 2^17 2^16 2^90 < 2^126.
+// 2^-90 of the channel's largest (zero among it) the group's codes are masked and the unit is the
+// largest. Sums then stay below 7 2^17 2^16 2^90 < 2^126. A masked group with a scale marks its channel in
+// `small`: its products are added after the main loop, since X may be zero where the scales are large.
 constexpr int kPrepRows = 4, kPrepChannels = 32;
 
 template <class T>
@@ -382,16 +382,23 @@ __device__ __forceinline__ void prepare_scales(const A16Args &a, int64_t block, 
     red[threadIdx.x] = top;
     __syncthreads();
     for (int q = 0; q < 256 / kPrepChannels; ++q) top = __builtin_fmaxf(top, red[q * kPrepChannels + threadIdx.x % kPrepChannels]);
-    if (c >= a.n) return;
     const float least = top * 0x1p-90f;
+    bool small = false;
     auto on = [&](float s) { return s != 0.f && !(__builtin_fabsf(s) < least); };
     auto unit = [&](float s) { return on(s) ? s : top == 0.f ? 1.f : top; };
-    for (int g = gl; g < groups; g += 256 / kPrepChannels) {
+    for (int g = gl; c < a.n && g < groups; g += 256 / kPrepChannels) {
         const float s = a.sw[g * a.n + c], before = a.sw[(g > 0 ? g - 1 : 0) * a.n + c];
         a.mul[g * a.n + c] = unit(before) / unit(s);
         a.mask[g * a.n + c] = on(s) ? 0xFFFFFFFFu : 0u;
+        small |= s != 0.f && !on(s);
         if (g + 1 == groups) a.unit[c] = unit(s);
     }
+    __syncthreads();
+    red[threadIdx.x] = small ? 1.f : 0.f;
+    __syncthreads();
+    if (gl > 0 || c >= a.n) return;
+    for (int q = 1; q < 256 / kPrepChannels; ++q) small |= red[q * kPrepChannels + threadIdx.x] != 0.f;
+    a.small[c] = small;
 }
 
 // 16 rows, 16 threads a row: T summed over its slices in order, under a power of two a row, in two
@@ -595,9 +602,11 @@ __global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t nti
     // true values; then the low-rank term, T L2 2^te; then the stores, turned in this wave's LDS
     uint16_t *const turn = reinterpret_cast<uint16_t *>(ring) + wave * ROWS * 64;
     const int64_t last = a.b - 1;
+    const bool small = __ballot((a.small[chan[0]] | a.small[chan[1]]) != 0) != 0;
 #pragma unroll
     for (int t = 0; t < TB; ++t) {
         const int64_t tok = tok0 + t * 32 + half * 4;  // + 8 (v / 4) + v % 4
+        const int64_t i = tok0 + t * 32 + col;
         float f[16];
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
@@ -610,13 +619,35 @@ __global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t nti
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[q][t][v] = acc[q][t][v] * u * f[v];
         }
+        if (__builtin_expect(small, 0)) {  // rarely: masked groups with a scale, the products of each by themselves
+            const uint16_t *xp = a.x16 + (i < last ? i : last) * a.m + half * 32;
+            const DequantConst dc = dequant_const();  // and the codes' addresses again: none of them is held over the main loop
+            for (int64_t g = 0; g < groups; ++g)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float s = (a.mask + g * a.n)[chan[q]] == 0 ? (a.sw + g * a.n)[chan[q]] : 0.f;
+                    if (__ballot(s != 0.f) == 0) continue;
+                    v16f p;
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) p[v] = 0.f;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const v4i c = load16(a.qw + (chan[q] / 16 * groups + g) * 1024 + chan[q] % 16 * 64 + half * 16 + h * 32);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            p = mfma_f16_32(__builtin_bit_cast(v8h, load16(xp + g * 128 + h * 64 + e * 8)),
+                                            __builtin_bit_cast(v8h, dequant8((uint32_t)c[e], dc)), p);
+                    }
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) acc[q][t][v] += s != 0.f ? s * (p[v] * f[v]) : 0.f;
+                }
+        }
         if (a.r > 0) {
             v16f low[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) low[q][v] = 0.f;
-            const int64_t i = tok0 + t * 32 + col;
             const uint16_t *tp = a.t16 + ((i < last ? i : last) * a.r + half * 8) * 2;
             for (int k = 0; k < a.r; k += 16) {
                 const v8h hi = __builtin_bit_cast(v8h, load16(tp + k * 2)), lo = __builtin_bit_cast(v8h, load16(tp + k * 2 + 8));

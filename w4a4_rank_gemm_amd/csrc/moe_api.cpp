@@ -127,6 +127,7 @@ twq_status twq_linear_a16(const void *x, const void *qw, const float *sw, const 
     a.xe = reinterpret_cast<int32_t *>(ws + p.xe);
     a.mul = reinterpret_cast<float *>(ws + p.mul);
     a.mask = reinterpret_cast<uint32_t *>(ws + p.mask);
+    a.small = reinterpret_cast<uint32_t *>(ws + p.small);
     a.unit = reinterpret_cast<float *>(ws + p.unit);
     a.t16 = reinterpret_cast<uint16_t *>(ws + p.t16);
     a.te = reinterpret_cast<int32_t *>(ws + p.te);

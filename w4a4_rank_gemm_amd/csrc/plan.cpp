@@ -224,7 +224,8 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
     p.xe = p.x16 + up((size_t)b * m * 2);
     p.mul = p.xe + up((size_t)b * 4);
     p.mask = p.mul + up((size_t)groups * n * 4);
-    p.unit = p.mask + up((size_t)groups * n * 4);
+    p.small = p.mask + up((size_t)groups * n * 4);
+    p.unit = p.small + up((size_t)n * 4);
     p.t16 = p.unit + up((size_t)n * 4);
     p.te = p.t16 + up((size_t)b * r * 4);
     p.total = p.te + up((size_t)b * 4);

@@ -36,7 +36,8 @@ struct A16Args {
     uint16_t *x16;        // [b][m] fp16: X 2^-xe, eight elements in the order 0 4 1 5 2 6 3 7
     int32_t *xe;          // [b] (bf16)
     float *mul;           // [m / 128][n]: unit of the group before over this group's
-    uint32_t *mask;       // [m / 128][n]: all ones, or 0 for a group without weight
+    uint32_t *mask;       // [m / 128][n]: all ones, or 0 for a group with little or no weight
+    uint32_t *small;      // [n]: 1 where a group with weight is masked
     float *unit;          // [n]: unit of the last group
     uint16_t *t16;        // [b][r / 8][2][8]: X L1 2^-te in two fp16 parts
     int32_t *te;          // [b]
@@ -52,7 +53,7 @@ struct A16Plan {
     int fn, kw;    // few rows: panels of a wave, and neighbouring waves that share their K
     int tks;       // K slices of X L1, 0: formed by the product's CTAs (or r = 0)
     int ks;        // K slices of the product
-    size_t t, x16, xe, mul, mask, unit, t16, te, part, total;
+    size_t t, x16, xe, mul, mask, small, unit, t16, te, part, total;
 };
 A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r);  // plan.cpp
 hipError_t launch_a16_t(const A16Args &a, hipStream_t stream);  // t, with few sums
