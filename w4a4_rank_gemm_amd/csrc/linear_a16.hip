@@ -3,7 +3,7 @@
 //   y[i][j] = sum_G s_W[G][j] sum_{k in G} x[i][k] q[j][k] + sum_t (sum_k x[i][k] L1[k][t]) L2[t][j]
 //
 // G: groups of 128 input channels. X is fp16 or bf16 and used as it is; codes are exact in both
-// types, so the only roundings are those of the binary32 sums, of T = X L1 to 16 (tile kernel: 22) bits and
+// types, so the only roundings are those of the binary32 sums, of T = X L1 to 16 or more bits and
 // the output's. T comes in partial sums over K slices from a launch of its own (with few sums
 // a16_t_kernel, otherwise the adapters' shrink kernel), or from the product's own CTAs where L1 is small.
 #include "twq_few_device.h"
@@ -330,6 +330,10 @@ static hipError_t a16_rows(const A16Args &a, const A16Plan &p, hipStream_t strea
 
 // ---- many rows ---------------------------------------------------------------------------
 
+__device__ __forceinline__ v16f mfma_bf16_32(v4i a, v4i b, v16f c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
 // What the tile kernel reads: X in fp16, the scales as ratios, T in two parts. One pass over each,
 // bound by memory: 4001 x 8192 (bf16, 28672 channels) 45 us, 2048 x 4096 10 us.
 //
@@ -402,7 +406,9 @@ __device__ __forceinline__ void prepare_scales(const A16Args &a, int64_t block, 
 }
 
 // 16 rows, 16 threads a row: T summed over its slices in order, under a power of two a row, in two
-// fp16 parts (22 significant bits).
+// fp16 parts (22 significant bits of elements within 2^-17 of the row's largest, 16 within 2^-22). A row with smaller
+// elements is left as it is, in two bf16 parts (16 significant bits of all of them) in an array of its
+// own and zeros in the other's place. te: exponent times two, plus one for such a row.
 __device__ __forceinline__ void prepare_t(const A16Args &a, int64_t block) {
     const int q = threadIdx.x % 16;
     const int64_t row = block * 16 + threadIdx.x / 16, rc = row < a.b ? row : a.b - 1;
@@ -415,18 +421,33 @@ __device__ __forceinline__ void prepare_t(const A16Args &a, int64_t block) {
         mx = __builtin_fmaxf(mx, __builtin_fabsf(t[u]));
     }
     for (int off = 8; off > 0; off >>= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, off, kWave));
-    if (row >= a.b) return;
     const int e = scale_exponent(mx);
-    if (q == 0) a.te[row] = e - 14;
+    const float scale = pow2(14 - e);  // to a largest element in [2^14, 2^15)
+    bool small = false;                // the second fp16 part ends at 2^-24
+#pragma unroll
+    for (int u = 0; u < 16; ++u) small |= t[u] != 0.f && __builtin_fabsf(t[u] * scale) < 0x1p-8f;
+    const bool wide = (__ballot(small) >> (threadIdx.x % kWave & 48) & 0xFFFF) != 0;
+    if (row >= a.b) return;
+    if (q == 0) a.te[row] = wide ? 1 : (e - 14) * 2;
 #pragma unroll
     for (int u = 0; u < 16; ++u) {
         if (u * 16 >= a.r) continue;
         const int k = u * 16 + q;
-        const float v = t[u] * pow2(14 - e);
+        const float v = t[u] * scale;
         const uint16_t hi = F16::from_f32(v), lo = F16::from_f32(v - F16::to_f32(hi));
-        uint16_t *p = a.t16 + (row * a.r + k / 8 * 8) * 2 + k % 8;
-        p[0] = hi;
-        p[8] = lo;
+        const int64_t at = (row * a.r + k / 8 * 8) * 2 + k % 8;
+        a.t16[at] = wide ? 0 : hi;
+        a.t16[at + 8] = wide ? 0 : lo;
+    }
+    if (__builtin_expect(wide, 0)) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            if (u * 16 >= a.r) continue;
+            const int64_t at = (row * a.r + (u * 16 + q) / 8 * 8) * 2 + q % 8;
+            const uint16_t hi = BF16::from_f32(t[u]);
+            a.twide[at] = hi;
+            a.twide[at + 8] = BF16::from_f32(t[u] - BF16::to_f32(hi));
+        }
     }
 }
 
@@ -649,6 +670,7 @@ __global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t nti
 #pragma unroll
                 for (int v = 0; v < 16; ++v) low[q][v] = 0.f;
             const uint16_t *tp = a.t16 + ((i < last ? i : last) * a.r + half * 8) * 2;
+            const int wide = -(a.te[i < last ? i : last] & 1);  // all ones: a row in bf16 parts
             for (int k = 0; k < a.r; k += 16) {
                 const v8h hi = __builtin_bit_cast(v8h, load16(tp + k * 2)), lo = __builtin_bit_cast(v8h, load16(tp + k * 2 + 8));
 #pragma unroll
@@ -658,10 +680,28 @@ __global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t nti
                     low[q] = mfma_f16_32(hi, l2, low[q]);
                 }
             }
+            if (__builtin_expect(__ballot(wide) != 0, 0)) {
+                const uint16_t *wp = a.twide + (tp - a.t16);
+#pragma unroll 1
+                for (int k = 0; k < a.r; k += 16) {
+                    v4i hi = load16(wp + k * 2), lo = load16(wp + k * 2 + 8);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) hi[e] &= wide, lo[e] &= wide;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        v4i wh, wl;
+                        split_f16(load16(a.l2t + chan[q] * a.r + k + half * 8), wh, wl);
+                        low[q] = mfma_bf16_32(lo, wl, low[q]);
+                        low[q] = mfma_bf16_32(hi, wl, low[q]);
+                        low[q] = mfma_bf16_32(lo, wh, low[q]);
+                        low[q] = mfma_bf16_32(hi, wh, low[q]);
+                    }
+                }
+            }
 #pragma unroll
             for (int v = 0; v < 16; ++v) {
                 const int64_t i2 = tok + v / 4 * 8 + v % 4;
-                const float te = pow2(a.te[i2 < last ? i2 : last]);
+                const float te = pow2(a.te[i2 < last ? i2 : last] >> 1);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) acc[q][t][v] += low[q][v] * te;
             }

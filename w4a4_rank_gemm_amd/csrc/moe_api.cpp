@@ -130,6 +130,7 @@ twq_status twq_linear_a16(const void *x, const void *qw, const float *sw, const 
     a.small = reinterpret_cast<uint32_t *>(ws + p.small);
     a.unit = reinterpret_cast<float *>(ws + p.unit);
     a.t16 = reinterpret_cast<uint16_t *>(ws + p.t16);
+    a.twide = reinterpret_cast<uint16_t *>(ws + p.twide);
     a.te = reinterpret_cast<int32_t *>(ws + p.te);
     a.ks = p.ks;
     a.part = reinterpret_cast<float *>(ws + p.part);

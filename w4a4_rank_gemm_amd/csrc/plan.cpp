@@ -227,7 +227,8 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
     p.small = p.mask + up((size_t)groups * n * 4);
     p.unit = p.small + up((size_t)n * 4);
     p.t16 = p.unit + up((size_t)n * 4);
-    p.te = p.t16 + up((size_t)b * r * 4);
+    p.twide = p.t16 + up((size_t)b * r * 4);
+    p.te = p.twide + up((size_t)b * r * 4);
     p.total = p.te + up((size_t)b * 4);
     return p;
 }

@@ -39,7 +39,8 @@ struct A16Args {
     uint32_t *mask;       // [m / 128][n]: all ones, or 0 for a group with little or no weight
     uint32_t *small;      // [n]: 1 where a group with weight is masked
     float *unit;          // [n]: unit of the last group
-    uint16_t *t16;        // [b][r / 8][2][8]: X L1 2^-te in two fp16 parts
+    uint16_t *t16;        // [b][r / 8][2][8]: X L1 2^-(te / 2) in two fp16 parts; zeros where te is odd
+    uint16_t *twide;      // the same of X L1 in two bf16 parts, in rows where te is odd
     int32_t *te;          // [b]
     // few rows
     int ks;               // slices of K
@@ -53,7 +54,7 @@ struct A16Plan {
     int fn, kw;    // few rows: panels of a wave, and neighbouring waves that share their K
     int tks;       // K slices of X L1, 0: formed by the product's CTAs (or r = 0)
     int ks;        // K slices of the product
-    size_t t, x16, xe, mul, mask, small, unit, t16, te, part, total;
+    size_t t, x16, xe, mul, mask, small, unit, t16, twide, te, part, total;
 };
 A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r);  // plan.cpp
 hipError_t launch_a16_t(const A16Args &a, hipStream_t stream);  // t, with few sums
