@@ -192,16 +192,20 @@ A16Plan plan_a16(int64_t b, int64_t m, int64_t n, int64_t r) {
             p.kw = 1;
             while (p.kw < 8 && units * p.kw < 256 * (p.rows == 4 ? 12 : 6) && pieces >= p.kw * 2) p.kw *= 2;
         } else {
-            // Two panels a wave where one would give a compute unit more than one CTA: 768 x 4096 -> 4096 (384 CTAs)
-            // 37.6 us, one panel 40.1; 192 x 4096 -> 14336 (336) 37.8 and 39.8; below: 512 x 4096 -> 4096 (256) 29.3
-            // and 25.4, 64 x 4096 -> 28672 (224) 34.5 and 27, 64 x 8192 -> 28672 50.8 and 50.2.
+            // Two panels a wave where one would give a compute unit more than one CTA and two do not: 768 x 4096 -> 4096
+            // (384 CTAs, 192) 42.4 us, one panel 44.2; 200 x 4096 -> 14336 (448, 224) 41.7 and 46.4; 8000 x 4096 -> 512
+            // (500, 250) 49 and 57; 12000 x 4096 -> 192 (376, 188) 46.9 and 50.1. With 256 CTAs or fewer of one panel:
+            // 512 x 4096 -> 4096 (256) 29.3 and 25.4, 64 x 4096 -> 28672 (224) 34.5 and 27, 64 x 8192 -> 28672 50.8
+            // and 50.2. With more than 256 of two, where waves of narrow layers own no second panel: 17000 x 4096 ->
+            // 128 (266, 266) 88 and 53, 10000 x 4096 -> 272 (471, 314) 83 and 52, 10000 x 1024 -> 384 (471, 314) 28.2
+            // and 18.9, 20000 x 2048 -> 16 (313, 313) 47 and 27.4.
             // Wave pairs that split K make CTAs of four panels, so that fewer K slices and no join fill the GPU.
             // More than 32 rows: 256 x 4096 -> 4096 (128 CTAs without) 17.9 us, without 21.8; 64 x 4096 -> 14336 (112)
             // 20.0 and 22.8; 512 x 4096 -> 4096 (256) 28.8 and 25.4, 128 x 4096 -> 14336 (224) 28.4 and 25.0;
             // longer rows of X: 61 x 14336 -> 4096 22.5 and 20.9, 128 x 14336 -> 4096 32.5 and 27.9.
             // 32 rows: 4096 -> 6144, 8192, 14336 11.3, 11.7, 13.4 and 11.5, 12.2, 15.8; 4096 -> 4096 9.1 and 9.0,
             // 14336 -> 4096 16.1 and 15.2, 4096 -> 22016 22.0 and 19.3.
-            p.fn = p.rows == 64 && plain > 256 ? 2 : 1;
+            p.fn = p.rows == 64 && plain > 256 && (panels + 15) / 16 * blocks <= 256 ? 2 : 1;
             p.kw = p.rows == 32 ? panels >= 384 && panels <= 1024 ? 2 : 1 : p.fn == 1 && plain < 192 && m <= 8192 ? 2 : 1;
             const int64_t per = 8 / p.kw * p.fn, ctas = (panels + per - 1) / per * blocks;
             // K slices: as many as leave one CTA a compute unit. 61 rows, 14336 -> 4096 with 4, 8, 16 (rule: 8)
