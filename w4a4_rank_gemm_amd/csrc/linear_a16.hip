@@ -628,17 +628,22 @@ __global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t nti
     for (int t = 0; t < TB; ++t) {
         const int64_t tok = tok0 + t * 32 + half * 4;  // + 8 (v / 4) + v % 4
         const int64_t i = tok0 + t * 32 + col;
-        float f[16];
+        int xe[16];
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
             const int64_t i = tok + v / 4 * 8 + v % 4;
-            f[v] = T::kBf16 ? pow2(a.xe[i < last ? i : last]) : 1.f;
+            xe[v] = T::kBf16 ? a.xe[i < last ? i : last] : 0;
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const float u = a.unit[chan[q]];
+            // fraction and exponents apart: the unit's and the row's may each leave the range that their product is in
+            const float u = a.unit[chan[q]], fraction = T::kBf16 ? __builtin_amdgcn_frexp_mantf(u) : u;
+            const int ue = T::kBf16 ? __builtin_amdgcn_frexp_expf(u) : 0;
 #pragma unroll
-            for (int v = 0; v < 16; ++v) acc[q][t][v] = acc[q][t][v] * u * f[v];
+            for (int v = 0; v < 16; ++v) {
+                acc[q][t][v] *= fraction;
+                if constexpr (T::kBf16) acc[q][t][v] = __builtin_ldexpf(acc[q][t][v], ue + xe[v]);
+            }
         }
         if (__builtin_expect(small, 0)) {  // rarely: masked groups with a scale, the products of each by themselves
             const uint16_t *xp = a.x16 + (i < last ? i : last) * a.m + half * 32;
@@ -660,7 +665,7 @@ __global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t nti
                                             __builtin_bit_cast(v8h, dequant8((uint32_t)c[e], dc)), p);
                     }
 #pragma unroll
-                    for (int v = 0; v < 16; ++v) acc[q][t][v] += s != 0.f ? s * (p[v] * f[v]) : 0.f;
+                    for (int v = 0; v < 16; ++v) acc[q][t][v] += s != 0.f ? s * (T::kBf16 ? p[v] * pow2(xe[v]) : p[v]) : 0.f;
                 }
         }
         if (a.r > 0) {
