@@ -504,7 +504,8 @@ twq_status twq_linear_dx(const void *dy, const void *qw, const float *sw, const 
  *   b is small: NULL is then allowed), rules as above
  * g must be 128 (TWQ_ERR_UNSUPPORTED otherwise); n at most 2^22, b n at most 2^37. y overlaps no
  * input. A weight of twq_pack_weight (one scale a channel) serves with its scales repeated m / g times.
- * A group's sum of products has to stay in binary32's range: |X| below 2^113 is always enough.
+ * A group's sum of products has to stay in binary32's range: |X| below 2^113 is always enough. With few bf16 rows
+ * a scale below 2^-122 in magnitude may lose its last bits.
  */
 size_t twq_linear_a16_workspace_bytes(int64_t b, int64_t m, int64_t n, int64_t r, int64_t g);
 twq_status twq_linear_a16(const void *x, const void *qw, const float *sw, const void *l1t, const void *l2t, int64_t r,

@@ -128,7 +128,8 @@ __device__ __forceinline__ void few_lowrank(const A16Args &a, F &&rank8, const i
 }
 
 // T's parts of the R rows from row0 on to LDS, [r / 8][R rows][hi, lo], by the whole CTA: each of its waves would
-// otherwise read T's slices again (64 tokens, 4096 -> 14336, 64 ranks: 44 us, this way 31).
+// otherwise read T's slices again (64 tokens, fp16: 4096 -> 14336, 64 ranks 38.5 us, this way 27.5; 8192 -> 28672,
+// 128 ranks 111 and 64).
 template <int R>
 __device__ __forceinline__ void stage_t(const A16Args &a, int64_t row0, uint8_t *lds) {
     __syncthreads();
@@ -241,9 +242,12 @@ __global__ __launch_bounds__(kFewWaves *kWave) void a16_few_kernel(A16Args a, in
 
 // From 17 rows on, in blocks of XR: the CTA's eight waves, in groups of KG, own FN panels each and share
 // the rows and a slice of K. 32 x 8192 -> 28672 37 us (3.3 TB/s of weights), 64 rows 50, 128 rows 77,
-// 1024 x 4096 -> 4096 42 (0.8 PFLOP/s): expansion and matrix instructions beside the read.
-// 61 x 14336 -> 4096 16.4 us and 4.6 to join eight slices: bound by the steps' latency (LDS is in use for
-// 30% of the cycles; reading row operands for two panels at once, or two steps ahead, gained nothing).
+// 1024 x 4096 -> 4096 46-48 (0.75 PFLOP/s). Bound by the steps themselves, which turn rows through LDS, expand
+// codes and feed chains of matrix instructions with two waves a SIMD: with rows and codes that come from a
+// cache, 61 x 14336 -> 4096 took 18.0 us instead of 18.8, 32 x 4096 -> 14336 10.9 of 12.6, 512 x 4096 -> 4096 24.1 of
+// 26.1, 128 x 8192 -> 28672 74 of 79 (matrix cores busy 23%, LDS in use for 31% of the cycles in the first; reading
+// row operands for two panels at once, or two steps ahead, gained nothing). Joining eight slices of the first
+// takes 4.7 us.
 template <class T, int FN, int XR, int U, int KG>
 __global__ __launch_bounds__(kSharedWaves *kWave) void a16_shared_kernel(A16Args a) {
     typedef SharedRows<T, FN, XR, 1, U, KG> Rows;
@@ -335,7 +339,7 @@ __device__ __forceinline__ v16f mfma_bf16_32(v4i a, v4i b, v16f c) {
 }
 
 // What the tile kernel reads: X in fp16, the scales as ratios, T in two parts. One pass over each,
-// bound by memory: 4001 x 8192 (bf16, 28672 channels) 45 us, 2048 x 4096 10 us.
+// bound by memory: 4001 x 8192 (bf16, 28672 channels, 128 ranks) 46.5 us, 2048 x 4096 (fp16, 14336, 32) 11 us.
 //
 // The tile kernel multiplies its sums by mul[G] = unit[G - 1] / unit[G] before group G, so that
 // they are in units of the group's scale when its products (codes times X) are added: one
@@ -507,9 +511,10 @@ __device__ __forceinline__ void a16_read(uint32_t a0, uint32_t a1, v4i (&r)[2][T
 // channel l % 32, and of each half group the 32 codes of K quarter l / 32. Tokens are the
 // rows of the result and channels its columns, so that a group's scale is one register a lane.
 // A wave's group is 64 matrix instructions (2048 cycles) and beside them 128 multiplications by scale
-// ratios and 144 operations of expansion (1090 cycles). 4001 x 8192 -> 28672 1.67-1.85 ms, 1.1 PFLOP/s:
-// matrix cores busy 60% of the cycles at about 1.9 GHz, no LDS conflicts. 2048 x 4096 -> 14336 265-291 us:
-// 896 tiles on 512 places, 51%. Interleaving the multiplications with the matrix instructions by
+// ratios and 144 operations of expansion (1090 cycles). 4001 x 8192 -> 28672 1.66-1.82 ms, 1.1 PFLOP/s:
+// matrix cores busy 60% of the cycles at about 1.9 GHz, no LDS conflicts. 2048 x 4096 -> 14336 by itself
+// 262-295 us (clocks differ by card and by what ran before; the whole call, with two passes before it, 255-286): 896
+// tiles on 512 places, 53%. Interleaving the multiplications with the matrix instructions by
 // hand was 3-10% slower than leaving it to two waves a SIMD.
 template <class T, int TB>
 __global__ __launch_bounds__(256, 2) void a16_tile_kernel(A16Args a, int64_t ntiles, int64_t ttiles) {

@@ -5,7 +5,8 @@
 //
 // with G, U (one array of 2 f rows an expert) and D in the layer's packed format with group-wise
 // scales. Launches: the logits; the choice; gate, up and the activation; down; the sum over a token's
-// choices. Bound by the read of the chosen experts' codes.
+// choices. One token is bound by the read of its experts' codes and by the chain of launches, more tokens by the
+// work of the CTAs (see the kernels).
 #include "twq_few_device.h"
 #include "twq_moe.h"
 
@@ -400,7 +401,8 @@ __device__ __forceinline__ void expert_entries(const MoeArgs &a, EntryScratch &s
 
 // kw waves to a panel of gate and up rows. One more row of CTAs than there are slots (few tokens)
 // makes the down kernel's work list. One token, 2 of 8 experts of 4096 -> 14336 (125 MB): 30.6 us, 4.1
-// TB/s; 13 tokens, 4 of 60 of 2048 -> 1408 (71 MB) 24; 8 of 64 of 2048 -> 768 (14 MB) 8.6.
+// TB/s; 13 tokens, 4 of 60 of 2048 -> 1408 (71 MB) 24, and 21.6 with rows and codes that
+// come from a cache: the CTAs' start, search and steps; one token, 8 of 64 of 2048 -> 768 (14 MB) 8.9.
 template <class T>
 __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a, int slots, int kw) {
     // one place a wave, whatever the rows of a tile: waves may be at different tiles
@@ -479,8 +481,10 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_few_kernel(MoeArgs a) {
 // Many rows an expert, or many experts: the CTA's eight waves share an expert's rows and K, and own
 // eight panels of inner (output) channels together. 128 tokens, 8 of 128 experts of 4096 and 1408: gate and
 // up 158-189 us for 798 MB (4.2-5.0 TB/s), down 104-130 for 444 MB (3.4-4.3): its CTAs have 11 steps only,
-// and finding the expert's rows and the first loads are a larger part of them. Two panels a wave, wave
-// pairs that split K and two pieces a step were all slower there (1-7%).
+// and finding the expert's rows and the first loads are a larger part of them. With many rows an expert a CTA takes
+// its tiles of 32 one after the other and expands the same codes for each: 256 tokens, 8 of 64 of 2048 -> 768 60 and
+// 44 us, 58.6 and 43 with rows and codes that come from a cache; 2 of 8 of 4096 -> 14336 266 and 285, 245 and 257.
+// Two panels a wave, wave pairs that split K and two pieces a step were all slower with 128 tokens (1-7%).
 template <class T>
 __global__ __launch_bounds__(kMoeThreads) void moe_up_shared_kernel(MoeArgs a) {
     constexpr int XR = 32;

@@ -258,21 +258,29 @@ MoePlan plan_moe(int64_t b, int64_t m, int64_t f, int64_t experts, int64_t k) {
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     MoePlan p{};
     const int64_t pairs = b * k, slots = pairs < experts ? pairs : experts;
-    // The down kernel that sums a token's outputs itself against the shared one with its join: 1 token, 8 of
-    // 64 experts 22.5 and 26 us, 2 of 8 wide ones 53 and 62; 2 tokens 26.5 and 29.7; 4 37.4 and 37.2;
-    // 13 54.3 and 52.2.
+    // Layers below: A 8 of 64 experts, 2048 -> 768, bf16; B 2 of 8, 4096 -> 14336, fp16; C 4 of 60, 2048 -> 1408, bf16;
+    // D 8 of 128, 4096 -> 1408, fp16; us of a whole call, the router's launches among them.
+    // The down kernel that sums a token's outputs itself against the shared one with its join: 1 token A 23.0 and 26.0,
+    // B 57 and 63; 2 tokens A 29.0 and 30.1, B 91 and 102; 4 tokens B 124 and 155, D 78 and 80, but A 39.2 and 37.5,
+    // C 37.7 and 36.7. Its list holds four.
     p.few = b <= kFewMoe;
     p.slots = (int)slots;
-    // CTAs that share an expert's rows from 4 rows an expert on average: 128 tokens, 8 of 128 experts 314 us,
-    // waves with rows of their own 334; 256, 8 of 64 381 and 472; 64, 2 of 8 119 and 143; with 2 rows an
-    // expert (32, 8 of 128) 119 and 115, with 1 (13, 4 of 60) 55.6 and 51.9.
+    // CTAs that share an expert's rows from 4 rows an expert on average. Shared, and waves with rows of their own: 256
+    // tokens A (32 rows an expert) 121 and 155, B (64) 557 and 859; 64 B (16) 216 and 292; 128 C (8) 99 and 111, D
+    // (8) 284 and 307; 6 rows A (48) 65 and 63, C (90) 94 and 96, D (96) 283 and 288; 4 rows A (32) 62.5 and 61, C
+    // (60) 88.5 and 84.5, D (64) 263 and 280, B (16) 195 and 192; 2 rows D (32) 229 and 220, 1 row C (13)
+    // 59.4 and 58.8. And where there are CTAs of 128 inner channels for the compute units: waves that split K
+    // fill the GPU with fewer (256 tokens, 2 of 8 experts of 2048 -> 768: 75 and 65; 2 of 4 of 4096 -> 2048: 192 and
+    // 141). Short K loses by that: 200 tokens, 8 of 10 of 1024 -> 768 105 and 116; 256, 4 of 16 of 512 -> 256 45 and 57.
     p.up_shared = !p.few && pairs >= experts * 4 && f / 128 * slots >= 256;
-    // Waves that share K, 1, 2, 4, 8: one token, 8 of 64 experts 28.8, 24.5, 22.0, 22.5 us (rule: 4); 2 of 8 wide
-    // ones 55.6, 53.1, 54.5 (2); 13 tokens, 4 of 60 56.0, 52.2, 52.8 (2).
+    // Waves that share K, 1, 2, 4, 8: one token A 29.6, 25.1, 22.7, 23.0 (rule: 4), C 28.7, 24.0, 21.6, 22.0 (4), B 56, 56,
+    // 56, 59 (4), D 41, 34, 35, 34.5 (8); 4 tokens A 38, 39, 39, 42.5 (4); 8 tokens B 169, 163, 162, 182 (1), 2 of 4 of
+    // 4096 -> 2048, bf16 47.6, 36.3, 31, 31.4 (8); 13 tokens C 57.7, 58.9, 61, 69.5 (2).
     p.up_waves = 1;
     while (p.up_waves < 8 && f / 16 * slots * p.up_waves < 5000 && m / 128 >= p.up_waves * 8) p.up_waves *= 2;
-    // Rows of a down tile, 16 or 32: 8 an expert (128 tokens, 8 of 128) 296 and 337 us; 16 (64, 2 of 8) 110 and
-    // 100; 32 (256, 8 of 64) 421 and 408.
+    // Rows of a down tile, 16 or 32: 8 rows an expert A (64) 68 and 70.6, B (32) 196 and 211, D (128) 282-325 and
+    // 310-337, C (120) 101 and 99.6; 10 A (80) 73.5 and 73.2, B (40) 197 and 216; 12 A (96) 77 and 74, B (48) 262 and 216,
+    // D (192) 303-330 and 321-335, C (180) 111 and 109; 32 A (256) 131 and 122.
     p.down_rows = pairs >= experts * 12 ? 32 : 16;
     p.ks = 1;
     if (!p.few)
