@@ -64,3 +64,31 @@ def test_small_scales_count_among_large_ones(b, n):
         err[i::m // 128] += 2.0 ** -39 * x64[i::m // 128].abs().amax(1, keepdim=True) * w[:, k].abs().sum(1)
     value = x64 @ w.T
     check(twq.linear_a16(lone, qw, sw), (value, rounded(value, err, torch.bfloat16)), "rows of one group")
+
+
+@pytest.mark.parametrize("b,n", [(40, 400), (100, 33040), (3000, 4112)])
+def test_groups_of_zeros_under_a_least_scale(b, n):
+    """Pruned groups whose scale is the smallest normal number instead of zero: Y is that of zero scales, bit for
+    bit, and one such group with codes beside them counts in rows that live there."""
+    _say(f"linear_a16 pruned groups under a least scale b={b} n={n}")
+    g = _gen(b + 7)
+    m = 1152
+    codes = torch.clamp(torch.round(torch.randn(n, m, generator=g, device="cuda") * 2.2), -7, 7)
+    sw = 0.002 + 0.008 * torch.rand(m // 128, n, generator=g, device="cuda")
+    least = torch.finfo(torch.float32).tiny
+    for i in (1, 2, 5, 8):
+        codes[:, i * 128:(i + 1) * 128] = 0
+        sw[i] = least
+    qw = ref.pack(codes)
+    x = torch.randn(b, m, generator=g, device="cuda").bfloat16()
+    zero = torch.where(sw == least, torch.zeros_like(sw), sw)
+    assert torch.equal(twq.linear_a16(x, qw, sw), twq.linear_a16(x, qw, zero))
+    codes[5::16, 128:256] = 1
+    qw = ref.pack(codes)
+    x[0] = 0
+    x[0, 128:256] = 2.0 ** 20
+    y = twq.linear_a16(x, qw, sw)
+    assert torch.equal(y[1:], twq.linear_a16(x, qw, zero)[1:])
+    want = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    want[5::16] = 2.0 ** 27 * least  # 128 times 2^20
+    assert torch.equal(y[0], want)

@@ -345,7 +345,7 @@ __device__ __forceinline__ v16f mfma_bf16_32(v4i a, v4i b, v16f c) {
 // they are in units of the group's scale when its products (codes times X) are added: one
 // multiplication a sum and group, no second set of sums. unit[G] is s_W[G]; where that is below
 // 2^-90 of the channel's largest (zero among it) the group's codes are masked and the unit is the
-// largest. Sums then stay below 7 2^17 2^16 2^90 < 2^126. A masked group with a scale marks its channel in
+// largest. Sums then stay below 7 2^17 2^16 2^90 < 2^126. A masked group with weight marks its channel in
 // `small`: its products are added after the main loop, since X may be zero where the scales are large.
 constexpr int kPrepRows = 4, kPrepChannels = 32;
 
@@ -398,7 +398,13 @@ __device__ __forceinline__ void prepare_scales(const A16Args &a, int64_t block, 
         const float s = a.sw[g * a.n + c], before = a.sw[(g > 0 ? g - 1 : 0) * a.n + c];
         a.mul[g * a.n + c] = unit(before) / unit(s);
         a.mask[g * a.n + c] = on(s) ? 0xFFFFFFFFu : 0u;
-        small |= s != 0.f && !on(s);
+        if (s != 0.f && !on(s)) {  // codes of zeros (pruned, under a least scale) need no adding
+            const uint8_t *const w = a.qw + (c / 16 * groups + g) * 1024 + c % 16 * 64;
+            v4i any = load16(w);
+#pragma unroll
+            for (int e = 1; e < 4; ++e) any |= load16(w + e * 16);
+            small |= (any[0] | any[1] | any[2] | any[3]) != 0;
+        }
         if (g + 1 == groups) a.unit[c] = unit(s);
     }
     __syncthreads();
